@@ -253,6 +253,137 @@ MOE_API int moe_router_topk_noalloc(const uint8_t *router_q, const uint16_t *rou
                                     int hidden, int n_experts, int top_k, const void *x, int T, int32_t *ids,
                                     float *weights, float *sgate, void *stream);
 
+/* ---- paged key-value cache (Qwen3.6-35B-A3B decode demo, section 9: the gated attention layer's (1 + w) QK-RMSNorm,
+ * partial rotary embedding, cache append, grouped-query attention and sigmoid output gate; TileFoundry tutorial,
+ * step 2: the decode step's cache contract) ----
+ *
+ * A cache is a pool of n_pages pages of page_size tokens, one pool for keys and one for values per layer:
+ *   k_cache, v_cache [n_pages][n_kv_heads][page_size][head_dim]      caller-owned device memory
+ * The pages of request b are tables[b][0 ..], in the order of its tokens: token p lies in slot
+ *   tables[b][p / page_size] * page_size + p % page_size.
+ * A moe_cache_t holds what the calls need besides: the shape, the rotary frequencies and the workspace. One handle
+ * serves every layer of a model. The pointers of the calls are device memory; a call is asynchronous on `stream`,
+ * allocates nothing, makes no host synchronisation and can be captured in a CUDA graph. Calls on one handle must
+ * not overlap in time, on the device either.
+ *
+ * Free pages lie in a ring: free_pages[n_pages] int32 and free_state[3] int32 = {head, count, refused}: the free
+ * pages are free_pages[(head + i) mod n_pages], 0 <= i < count. */
+enum { MOE_DTYPE_E4M3 = 2 };   /* a cache's element type, beside MOE_DTYPE_F16 and MOE_DTYPE_BF16 */
+
+typedef struct moe_cache moe_cache_t;   /* opaque, owned by the library */
+
+typedef struct {
+  int n_heads;        /* query heads: a multiple of n_kv_heads, at most 64 to a key-value head */
+  int n_kv_heads;     /* 1..256 */
+  int head_dim;       /* 64, 128 or 256 */
+  int page_size;      /* tokens per page: 16, 32, 64, 128 or 256 */
+  int n_pages;        /* pages of a pool: n_pages * page_size < 2^31 */
+  int max_requests;   /* largest B any call will pass: 1..4096 */
+  int max_pages;      /* entries of a table row: max_pages * page_size < 2^31 */
+  int act_dtype;      /* q, k, v, gate, out: MOE_DTYPE_F16 or MOE_DTYPE_BF16 */
+  int cache_dtype;    /* act_dtype, or MOE_DTYPE_E4M3 with fp32 scales per key-value head */
+  int rope_dim;       /* R: elements of a head that are rotated, a multiple of 16 up to head_dim; 0 for none */
+  double rope_theta;  /* > 1 */
+  float gamma_offset; /* a norm weight is gamma_offset + gamma: 1 for weights stored around zero, 0 for plain ones */
+  float norm_eps;     /* >= 0 */
+} moe_cache_config_t;
+
+/* A [rows][heads][head_dim] tensor: strides in elements, the innermost 1. The pointer is 16-byte aligned and the
+ * strides are multiples of 8. */
+typedef struct {
+  const void *p;
+  int64_t row_stride, head_stride;
+} moe_rows_t;
+
+/* MOE_ERR_INVALID_ARG: a NULL pointer; MOE_ERR_UNSUPPORTED: a shape or type outside the ranges above. */
+MOE_API int moe_cache_create(const moe_cache_config_t *cfg, moe_cache_t **out);
+MOE_API void moe_cache_destroy(moe_cache_t *cache);
+
+/* One step's block tables and slot maps. Request b has lengths[b] tokens in the cache and brings new_tokens[b] more
+ * (0: none this step; NULL: one for every request; negative: the request has ended). The rows of the step's token
+ * batch are the requests' new tokens one after another: starts[b] .. starts[b + 1] - 1 are request b's.
+ *   - An ended request's pages go to the tail of the ring and its length becomes 0.
+ *   - A request whose tokens need further pages takes them from the head of the ring, in the order of the requests,
+ *     into the next entries of its table row. Pages given back in a call are not taken in the same call. When the
+ *     running need passes the pages that are free, that request and every later one that needs a page are refused:
+ *     no page, no slot, the length unchanged. So is a request that would pass max_pages or whose rows pass n_rows.
+ *   - slots[r] is the slot of row r's token and positions[r] its position; rows of refused requests and rows past
+ *     the last token get -1 and 0.
+ * lengths_out may be lengths, free_state_out may be free_state (with them in place a captured graph steps the cache);
+ * no other buffers may overlap. A page id outside the pool gives slot -1; it, a length outside
+ * 0 .. max_pages * page_size and a free_state outside the ring are reported by moe_cache_get_status. */
+typedef struct {
+  const int32_t *lengths;      /* [B] */
+  const int32_t *new_tokens;   /* [B], or NULL */
+  int32_t *tables;             /* [B][table_stride], max_pages entries of a row in use */
+  int64_t table_stride;
+  int32_t *free_pages;         /* [n_pages] */
+  const int32_t *free_state;   /* [3] */
+  int32_t *free_state_out;     /* [3]: the new head and count, and the number of requests refused in this call */
+  int32_t *lengths_out;        /* [B] */
+  int32_t *starts;             /* [B + 1] */
+  int32_t *slots, *positions;  /* [n_rows] */
+  int64_t n_requests, n_rows;  /* B: 0..max_requests; n_rows >= 0 */
+} moe_cache_plan_t;
+
+MOE_API int moe_cache_plan(moe_cache_t *cache, const moe_cache_plan_t *plan, void *stream);
+
+/* T rows of q, k, v as the projections leave them. For each row and head of q and k:
+ *   y = x / sqrt(mean(x^2) + norm_eps) * (gamma_offset + gamma)      (gamma NULL: y = x)
+ *   (y_i, y_{i+R/2}) <- (y_i cos a - y_{i+R/2} sin a, y_{i+R/2} cos a + y_i sin a),  a = positions[t] * theta^(-2i/R),
+ *   0 <= i < R/2.
+ * q goes to q_out (which may be q itself), k and v to slots[t] of the pools; a negative slot writes neither. The
+ * pools' page strides are in elements (n_kv_heads * page_size * head_dim when the pool is dense). With an e4m3 cache
+ * k / k_scale[head] and v / v_scale[head] are rounded to e4m3, values past its range to its largest. Computed in
+ * fp32 (angles in fp64), rounded once. q may be NULL together with q_out. Slots past the pool write nothing and are
+ * reported by moe_cache_get_status. Rows with the same slot race. */
+typedef struct {
+  moe_rows_t q, k, v;                          /* [T][n_heads | n_kv_heads][head_dim] */
+  moe_rows_t q_out;                            /* written */
+  const void *q_gamma, *k_gamma;               /* [head_dim] of act_dtype, or NULL */
+  const int32_t *positions, *slots;            /* [T] */
+  void *k_cache, *v_cache;
+  int64_t k_page_stride, v_page_stride;
+  const float *k_scale, *v_scale;              /* [n_kv_heads]: both given with an e4m3 cache, NULL otherwise */
+  int64_t n_rows;                              /* T >= 0 */
+} moe_cache_write_t;
+
+MOE_API int moe_cache_write(moe_cache_t *cache, const moe_cache_write_t *write, void *stream);
+
+/* Attention of one token of each request over the request's lengths[b] tokens in the cache (its own among them, once
+ * moe_cache_write has put it there): with g = the key-value head of query head h (h / (n_heads / n_kv_heads)),
+ *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j[g]) v_j[g]  * sigmoid(gate[b][h])       (gate.p NULL: no gate)
+ * and 0 for a request of length 0. Values of an e4m3 cache are multiplied by k_scale and v_scale. Softmax statistics
+ * and sums are fp32; the weights of the second product are rounded to act_dtype (fp16 with an e4m3 cache), the output
+ * once to act_dtype. What lies in a page past the request's end has no effect, NaN included. Table entries past the
+ * request's pages are not read. A page id outside the pool reads as zeros, and a length outside
+ * 0 .. max_pages * page_size as the nearest of the two; both are reported by moe_cache_get_status. */
+typedef struct {
+  moe_rows_t q, gate;                          /* [B][n_heads][head_dim] */
+  moe_rows_t out;                              /* written; may be q or gate itself */
+  const int32_t *tables;                       /* [B][table_stride] */
+  int64_t table_stride;
+  const int32_t *lengths;                      /* [B] */
+  const void *k_cache, *v_cache;               /* 16-byte aligned; page strides multiples of 16 bytes */
+  int64_t k_page_stride, v_page_stride;
+  const float *k_scale, *v_scale;              /* [n_kv_heads]: both given with an e4m3 cache, NULL otherwise */
+  int64_t n_requests;                          /* B: 0..max_requests */
+  double scale;                                /* finite; usually 1 / sqrt(head_dim) */
+} moe_cache_attend_t;
+
+MOE_API int moe_cache_attend(moe_cache_t *cache, const moe_cache_attend_t *attend, void *stream);
+
+/* Waits for the stream of the handle's last call and returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side
+ * wait of an attend call ran out: its outputs are wrong) or MOE_ERR_INVALID_ARG (a call met a value on the device
+ * that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits: 1 a wait ran out,
+ * 2 a length, 4 a page id or slot, 8 a free_state out of range. */
+MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);
+
+/* Host-only check of a shape and of any of the three calls' arguments (each may be NULL): the status that
+ * moe_cache_create (bar MOE_ERR_NO_DEVICE) and the call would return before they touch the device. */
+MOE_API int moe_debug_cache_check(const moe_cache_config_t *cfg, const moe_cache_plan_t *plan,
+                                  const moe_cache_write_t *write, const moe_cache_attend_t *attend);
+
 /* Number of CUDA kernel launches the last forward call made. */
 MOE_API int moe_block_last_launch_count(moe_block_t *blk);
 

@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include "../../include/moe_block.h"
+#include "cache.cuh"
 #include "chunk.cuh"
 #include "decode.cuh"
 #include "layout.cuh"
@@ -50,10 +51,11 @@ struct moe_block {
 
 static thread_local char g_cuda_err[256] = "";
 
-static int cuda_fail(cudaError_t e, const char* what) {
+int moe::report_cuda(cudaError_t e, const char* what) {
   snprintf(g_cuda_err, sizeof(g_cuda_err), "%s: %s", what, cudaGetErrorString(e));
   return MOE_ERR_CUDA;
 }
+static int cuda_fail(cudaError_t e, const char* what) { return moe::report_cuda(e, what); }
 #define CK(call)                                        \
   do {                                                  \
     cudaError_t _e = (call);                            \

@@ -1,0 +1,58 @@
+// The paged key-value cache: the handle, and what its three operators (cache_plan.cu, cache_write.cu,
+// cache_attend.cu) get from the C ABI (cache.cu). Layouts and formulas are in include/moe_block.h.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe_block.h"
+
+namespace moe {
+
+// records a CUDA runtime error for moe_last_cuda_error and returns MOE_ERR_CUDA (api.cu)
+int report_cuda(cudaError_t e, const char* what);
+
+constexpr int CACHE_MAX_REQUESTS = 4096;
+constexpr int CACHE_MAX_GROUP = 64;      // query heads to a key-value head
+
+enum : uint32_t {                        // bits of the handle's status word
+  CACHE_BAD_WAIT = 1, CACHE_BAD_LENGTH = 2, CACHE_BAD_PAGE = 4, CACHE_BAD_STATE = 8,
+};
+
+// the shape as the kernels use it
+struct CacheShape {
+  int Hq, Hkv, D, page_log2, n_pages, max_pages;
+  int rope;                              // rotated elements of a head
+  bool bf16, e4m3;                       // activations; cache elements
+  float gamma_offset, eps;
+};
+
+cudaError_t cache_plan_init();           // once per device: the kernel's shared-memory limit
+cudaError_t cache_plan_launch(const CacheShape& S, const moe_cache_plan_t& p, uint32_t* arrivals, uint32_t* status,
+                              int num_sms, cudaStream_t st);
+cudaError_t cache_write_launch(const CacheShape& S, const moe_cache_write_t& w, const double* turns,
+                               uint32_t* status, cudaStream_t st);
+cudaError_t cache_attend_launch(const CacheShape& S, const moe_cache_attend_t& a, uint32_t* status, cudaStream_t st);
+
+// ---- 16-bit pairs ----
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if (BF16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the low half
+  uint32_t r;
+  if (BF16) *reinterpret_cast<__nv_bfloat162*>(&r) = __floats2bfloat162_rn(a, b);
+  else *reinterpret_cast<__half2*>(&r) = __floats2half2_rn(a, b);
+  return r;
+}
+// two e4m3 codes (the lower one first) as a pair of fp16: exact
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
+  return (uint32_t)r.x | (uint32_t)r.y << 16;
+}
+
+}  // namespace moe

@@ -1,0 +1,195 @@
+// Block tables and slot maps of a step from the requests' lengths (moe_cache_plan).
+//
+// Two exclusive scans over the requests decide everything: of the new tokens (where a request's rows start, and so
+// whether they fit), then of the pages needed and the pages given back (which entries of the ring of free pages they
+// are). What follows is independent for each page and each row. The scans are a few thousand integers, so every CTA
+// repeats them and no CTA waits for another: the last one to have read the inputs writes the outputs that may lie in
+// place of them.
+#include "cache.cuh"
+
+namespace moe {
+namespace {
+
+struct PlanArgs {
+  moe_cache_plan_t p;
+  int B, rows, page_log2, n_pages, max_pages;
+  uint32_t *arrivals, *status;
+};
+
+// exclusive scan of one value per thread over the block; *total: the sum. ws: 33 words
+__device__ __forceinline__ long long block_scan(long long v, long long* ws, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) ws[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    long long s = lane < nw ? ws[lane] : 0;
+    const long long mine = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (lane < nw) ws[lane] = s - mine;
+    if (lane == 31) ws[32] = s;
+  }
+  __syncthreads();
+  const long long r = ws[warp] + x - v;
+  *total = ws[32];
+  __syncthreads();
+  return r;
+}
+
+__global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
+  extern __shared__ int sm[];
+  // per request: the row after its last, its cached tokens, its first page's place among the pages taken (-1: not
+  // admitted; -2 - place: its first page's place among the pages given back)
+  int *s_end = sm, *s_len = sm + a.B, *s_at = sm + 2 * a.B;
+  __shared__ long long ws[33];
+  __shared__ int s_refused;
+  __shared__ bool s_last;
+  const moe_cache_plan_t& p = a.p;
+  const int ps = 1 << a.page_log2;
+  const long long max_len = (long long)a.max_pages << a.page_log2;
+  const int tid = threadIdx.x, nth = blockDim.x;
+  int head = p.free_state[0], count = p.free_state[1];
+  if (head < 0 || head >= a.n_pages || count < 0 || count > a.n_pages) {
+    head = count = 0;
+    if (tid == 0) atomicOr(a.status, CACHE_BAD_STATE);
+  }
+  if (tid == 0) s_refused = 0;
+  __syncthreads();
+
+  long long row0 = 0, need0 = 0, back0 = 0, taken_mine = 0;
+  for (int b0 = 0; b0 < a.B; b0 += nth) {
+    const int b = b0 + tid;
+    const bool in = b < a.B;
+    const int len = in ? p.lengths[b] : 0;
+    const int nw = in ? (p.new_tokens ? p.new_tokens[b] : 1) : 0;
+    const bool good = len >= 0 && len <= max_len;
+    const bool done = nw < 0;
+    const long long n = nw > 0 ? nw : 0;
+    long long total;
+    const long long end = row0 + block_scan(n, ws, &total) + n;
+    row0 += total;
+    const int held = good ? (int)(((long long)len + ps - 1) >> a.page_log2) : 0;
+    const bool fits = in && good && !done && len + n <= max_len && end <= a.rows;
+    const int need = fits ? (int)((len + n + ps - 1) >> a.page_log2) - held : 0;
+    const int back = in && done ? held : 0;
+    const long long need_at = need0 + block_scan(need, ws, &total);
+    need0 += total;
+    const long long back_at = back0 + block_scan(back, ws, &total);
+    back0 += total;
+    const bool ok = fits && (need == 0 || need_at + need <= count);
+    if (ok) taken_mine += need;
+    if (in) {
+      s_end[b] = (int)(end < 0x7FFFFFFF ? end : 0x7FFFFFFF);
+      s_len[b] = len;
+      // a place among the pages is below n_pages (taken) or max_requests * max_pages clamped (given back)
+      s_at[b] = ok ? (int)(need ? need_at : 0)
+                   : done ? (int)(-2 - (back_at < 0x3FFFFFFF ? back_at : 0x3FFFFFFF)) : -1;
+      if (!ok && !done) atomicAdd(&s_refused, 1);
+      if (!good) atomicOr(a.status, CACHE_BAD_LENGTH);
+    }
+  }
+  long long taken;
+  block_scan(taken_mine, ws, &taken);
+
+  // the pages: a warp to a request
+  {
+    const int lane = tid & 31;
+    const int gw = (blockIdx.x * nth + tid) >> 5, n_w = (gridDim.x * nth) >> 5;
+    for (int b = gw; b < a.B; b += n_w) {
+      const int at = s_at[b], len = s_len[b];
+      int32_t* row = p.tables + (size_t)b * p.table_stride;
+      if (at >= 0) {
+        const int n = s_end[b] - (b ? s_end[b - 1] : 0);
+        const int held = (int)(((long long)len + ps - 1) >> a.page_log2);
+        const int want = (int)(((long long)len + n + ps - 1) >> a.page_log2);
+        for (int j = held + lane; j < want; j += 32)
+          row[j] = p.free_pages[((uint32_t)head + (uint32_t)at + (uint32_t)(j - held)) % (uint32_t)a.n_pages];
+      } else if (at <= -2 && len > 0 && len <= max_len) {
+        const int held = (int)(((long long)len + ps - 1) >> a.page_log2);
+        const uint32_t to = (uint32_t)head + (uint32_t)count + (uint32_t)(-2 - at);
+        for (int j = lane; j < held; j += 32) p.free_pages[(to + (uint32_t)j) % (uint32_t)a.n_pages] = row[j];
+      }
+    }
+  }
+  // the rows
+  for (long long r = (long long)blockIdx.x * nth + tid; r < a.rows; r += (long long)gridDim.x * nth) {
+    int lo = 0, hi = a.B;              // the first request that ends past row r
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_end[mid] > r) hi = mid; else lo = mid + 1;
+    }
+    int slot = -1, pos = 0;
+    if (lo < a.B && s_at[lo] >= 0) {
+      const int len = s_len[lo];
+      pos = len + (int)(r - (lo ? s_end[lo - 1] : 0));
+      const int held = (int)(((long long)len + ps - 1) >> a.page_log2), j = pos >> a.page_log2;
+      // a page taken in this call is read where it comes from
+      const int page = j < held ? p.tables[(size_t)lo * p.table_stride + j]
+                                : p.free_pages[((uint32_t)head + (uint32_t)s_at[lo] + (uint32_t)(j - held)) %
+                                               (uint32_t)a.n_pages];
+      if (page >= 0 && page < a.n_pages) slot = (page << a.page_log2) + (pos & (ps - 1));
+      else atomicOr(a.status, CACHE_BAD_PAGE);
+    }
+    p.slots[r] = slot;
+    p.positions[r] = pos;
+  }
+  // what may lie in place of the inputs: written once every CTA has read them
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      s_last = atomicAdd(a.arrivals, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+  }
+  for (int b = tid; b < a.B; b += nth) {
+    const int at = s_at[b], n = s_end[b] - (b ? s_end[b - 1] : 0);
+    p.lengths_out[b] = at >= 0 ? s_len[b] + n : at <= -2 ? 0 : s_len[b];
+    p.starts[b + 1] = s_end[b];
+  }
+  if (tid == 0) {
+    p.starts[0] = 0;
+    p.free_state_out[0] = (int)((uint32_t)(head + taken) % (uint32_t)a.n_pages);
+    const long long left = count - taken + back0;
+    p.free_state_out[1] = (int)(left < a.n_pages ? left : a.n_pages);
+    p.free_state_out[2] = s_refused;
+    if (gridDim.x > 1) *a.arrivals = 0;
+  }
+}
+
+}  // namespace
+
+cudaError_t cache_plan_init() {
+  return cudaFuncSetAttribute(k_cache_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, CACHE_MAX_REQUESTS * 12);
+}
+
+cudaError_t cache_plan_launch(const CacheShape& S, const moe_cache_plan_t& p, uint32_t* arrivals, uint32_t* status,
+                              int num_sms, cudaStream_t st) {
+  PlanArgs a;
+  a.p = p;
+  a.B = (int)p.n_requests;
+  a.rows = (int)p.n_rows;
+  a.page_log2 = S.page_log2;
+  a.n_pages = S.n_pages;
+  a.max_pages = S.max_pages;
+  a.arrivals = arrivals;
+  a.status = status;
+  int threads = (a.B + 31) & ~31;
+  threads = threads < 128 ? 128 : threads > 1024 ? 1024 : threads;
+  const long long want = ((long long)a.rows + threads - 1) / threads;
+  const int grid = (int)(want < 1 ? 1 : want > num_sms ? num_sms : want);
+  k_cache_plan<<<grid, threads, (size_t)a.B * 12, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

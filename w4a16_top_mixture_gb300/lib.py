@@ -2,8 +2,10 @@
 runs in the library's CUDA kernels; torch supplies device memory and streams. A missing library raises."""
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -25,7 +27,9 @@ EXPORTS = ["moe_block_create", "moe_block_load_weights", "moe_block_forward", "m
            "moe_block_debug_set_wait", "moe_block_debug_set_trace", "moe_block_last_launch_count",
            "moe_router_topk_noalloc", "moe_debug_decode_plan", "moe_stack_create", "moe_stack_load_layer",
            "moe_stack_forward", "moe_stack_get_status", "moe_stack_layer", "moe_stack_destroy",
-           "moe_affine_convert", "moe_affine_free", "moe_block_load_affine"]
+           "moe_affine_convert", "moe_affine_free", "moe_block_load_affine",
+           "moe_cache_create", "moe_cache_destroy", "moe_cache_plan", "moe_cache_write", "moe_cache_attend",
+           "moe_cache_get_status", "moe_debug_cache_check"]
 
 
 class MoeError(RuntimeError):
@@ -62,6 +66,20 @@ class AffineWeights(ctypes.Structure):
 
 
 DTYPES = {"f16": 0, "bf16": 1}
+CACHE_DTYPES = {"f16": 0, "bf16": 1, "e4m3": 2}
+
+
+class CacheConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_heads", "n_kv_heads", "head_dim", "page_size", "n_pages", "max_requests",
+                                            "max_pages", "act_dtype", "cache_dtype", "rope_dim")] + [
+        ("rope_theta", ctypes.c_double), ("gamma_offset", ctypes.c_float), ("norm_eps", ctypes.c_float)]
+
+
+# The argument structures of the cache's calls hold pointers, int64_t and double alone (moe_cache_plan_t,
+# moe_cache_write_t, moe_cache_attend_t), so each is packed in one go.
+CACHE_PLAN = struct.Struct("@3Pq7P2q")
+CACHE_WRITE = struct.Struct("@" + 4 * "P2q" + "6P2q2Pq")
+CACHE_ATTEND = struct.Struct("@" + 3 * "P2q" + "Pq3P2q2Pqd")
 
 
 def _affine_struct(aff: dict):
@@ -154,6 +172,13 @@ def load_library(path: str = LIB_PATH):
     lib.moe_stack_layer.restype = vp
     lib.moe_stack_destroy.argtypes = [vp]
     lib.moe_stack_destroy.restype = None
+    lib.moe_cache_create.argtypes = [ctypes.POINTER(CacheConfig), ctypes.POINTER(vp)]
+    for f in (lib.moe_cache_plan, lib.moe_cache_write, lib.moe_cache_attend):
+        f.argtypes = [vp, vp, vp]
+    lib.moe_debug_cache_check.argtypes = [ctypes.POINTER(CacheConfig), vp, vp, vp]
+    lib.moe_cache_get_status.argtypes = [vp, ctypes.POINTER(u32)]
+    lib.moe_cache_destroy.argtypes = [vp]
+    lib.moe_cache_destroy.restype = None
     for n in EXPORTS:
         if not hasattr(lib, n):
             raise RuntimeError(f"{path} does not export {n}")
@@ -399,6 +424,151 @@ class MoeStack:
         _check(self.lib.moe_block_debug_last_routing(ctypes.c_void_p(hb), T, None, _ptr(ids), _ptr(w), None,
                                                      _stream_ptr(None)), "moe_block_debug_last_routing")
         return {"ids": ids, "w": w}
+
+
+CachePlan = collections.namedtuple("CachePlan", "slots positions starts lengths free_state")
+
+
+class PagedCache:
+    """A paged key-value cache of one shape: the page plan of a step, the write of its rows, the attention that
+    reads them (the paged key-value cache's section of include/moe_block.h has the formulas). One handle serves every
+    layer; the pools [n_pages, n_kv_heads, page_size, head_dim], the tables and the ring of free pages are the
+    caller's. Outputs are new tensors unless given, allocated on `stream`."""
+
+    def __init__(self, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests, max_pages, dtype="f16",
+                 cache_dtype=None, rope_dim=0, rope_theta=10000.0, gamma_offset=0.0, eps=1e-6):
+        import torch
+        self.lib = load_library()
+        cache_dtype = cache_dtype or dtype
+        self.cfg = CacheConfig(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests, max_pages, DTYPES[dtype],
+                               CACHE_DTYPES[cache_dtype], rope_dim, rope_theta, gamma_offset, eps)
+        h = ctypes.c_void_p()
+        _check(self.lib.moe_cache_create(ctypes.byref(self.cfg), ctypes.byref(h)), "moe_cache_create")
+        self.h = h
+        self.dtype = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+        self.cache_dtype = self.dtype if cache_dtype == dtype else torch.float8_e4m3fn
+        self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
+        self.page_size, self.n_pages, self.max_pages = page_size, n_pages, max_pages
+        self.pool_shape = (n_pages, n_kv_heads, page_size, head_dim)
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._i32 = torch.int32
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.lib.moe_cache_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _rows(self, t, heads, rows):
+        """(pointer, row stride, head stride) of a [rows, heads, head_dim] tensor of the activations' type."""
+        st = t.stride()
+        if t.dtype != self.dtype or t.shape != (rows, heads, self.head_dim) or st[2] != 1 or t.device != self.device:
+            raise ValueError(f"want {self.dtype} [{rows}, {heads}, {self.head_dim}] on {self.device}, innermost stride 1; "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
+        return t.data_ptr(), st[0] if rows > 1 else 0, st[1] if heads > 1 else 0
+
+    def _ints(self, t, *shape):
+        if t.dtype != self._i32 or t.shape != shape or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"want a contiguous int32 {shape} on {self.device}; got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def _table(self, t, rows):
+        if (t.dtype != self._i32 or t.shape != (rows, self.max_pages) or t.device != self.device
+                or (t.stride(1) != 1 and rows and self.max_pages > 1) or (rows > 1 and t.stride(0) < self.max_pages)):
+            raise ValueError(f"want tables int32 [{rows}, {self.max_pages}] on {self.device}, rows apart; got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
+        return t.data_ptr(), max(t.stride(0), self.max_pages)
+
+    def _pool(self, t):
+        st, (_, _, p, d) = t.stride(), self.pool_shape
+        if (t.dtype != self.cache_dtype or t.shape != self.pool_shape or st[3] != 1 or st[2] != d
+                or (st[1] != p * d and self.n_kv_heads > 1) or t.device != self.device):
+            raise ValueError(f"want a pool {self.cache_dtype} {self.pool_shape} on {self.device}, dense within a page; got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
+        return t.data_ptr(), max(st[0], self.n_kv_heads * p * d)
+
+    def _scales(self, k, v):
+        import torch
+        for t in (k, v):
+            if t is not None and (t.dtype != torch.float32 or t.shape != (self.n_kv_heads,) or not t.is_contiguous()
+                                  or t.device != self.device):
+                raise ValueError(f"want scales fp32 [{self.n_kv_heads}] on {self.device}; got {t.dtype} {tuple(t.shape)}")
+        return (k.data_ptr() if k is not None else 0), (v.data_ptr() if v is not None else 0)
+
+    def _empty(self, shape, dtype, stream):
+        import torch
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def plan(self, lengths, new_tokens, tables, free_pages, free_state, n_rows, out=None, stream=None):
+        """Block tables and slot maps of a step (moe_cache_plan): lengths, new_tokens int32 [B] (new_tokens may be None:
+        one each), tables int32 [B, max_pages] and free_pages int32 [n_pages] (both updated in place), free_state
+        int32 [3]. out: a CachePlan to write into, whose lengths and free_state may be the inputs themselves."""
+        B = lengths.shape[0]
+        if out is None:
+            out = CachePlan(*self._empty((2 * n_rows + 2 * B + 4,), self._i32, stream).split(
+                (n_rows, n_rows, B + 1, B, 3)))
+        tab, tab_stride = self._table(tables, B)
+        args = CACHE_PLAN.pack(
+            self._ints(lengths, B), self._ints(new_tokens, B) if new_tokens is not None else 0, tab, tab_stride,
+            self._ints(free_pages, self.n_pages), self._ints(free_state, 3), self._ints(out.free_state, 3),
+            self._ints(out.lengths, B), self._ints(out.starts, B + 1), self._ints(out.slots, n_rows),
+            self._ints(out.positions, n_rows), B, n_rows)
+        _check(self.lib.moe_cache_plan(self.h, args, _stream_ptr(stream)), "moe_cache_plan")
+        return out
+
+    def write(self, q, k, v, positions, slots, k_cache, v_cache, q_gamma=None, k_gamma=None, k_scale=None, v_scale=None,
+              q_out=None, stream=None):
+        """RMSNorm and rotary embedding of q and k, and k, v into the pools by slot (moe_cache_write). q [T, n_heads,
+        head_dim] (or None), k and v [T, n_kv_heads, head_dim], views of a projection's output among them; returns
+        the new q (q_out, which may be q itself)."""
+        T = k.shape[0]
+        if q is not None and q_out is None:
+            q_out = self._empty((T, self.n_heads, self.head_dim), self.dtype, stream)
+        for g in (q_gamma, k_gamma):
+            if g is not None and (g.dtype != self.dtype or g.shape != (self.head_dim,) or not g.is_contiguous()
+                                  or g.device != self.device):
+                raise ValueError(f"want a norm weight {self.dtype} [{self.head_dim}] on {self.device}; got {g.dtype} "
+                                 f"{tuple(g.shape)} on {g.device}")
+        kc, ks = self._pool(k_cache)
+        vc, vs = self._pool(v_cache)
+        args = CACHE_WRITE.pack(
+            *(self._rows(q, self.n_heads, T) if q is not None else (0, 0, 0)), *self._rows(k, self.n_kv_heads, T),
+            *self._rows(v, self.n_kv_heads, T), *(self._rows(q_out, self.n_heads, T) if q is not None else (0, 0, 0)),
+            q_gamma.data_ptr() if q_gamma is not None else 0, k_gamma.data_ptr() if k_gamma is not None else 0,
+            self._ints(positions, T), self._ints(slots, T), kc, vc, ks, vs, *self._scales(k_scale, v_scale), T)
+        _check(self.lib.moe_cache_write(self.h, args, _stream_ptr(stream)), "moe_cache_write")
+        return q_out
+
+    def attend(self, q, tables, lengths, k_cache, v_cache, gate=None, scale=None, k_scale=None, v_scale=None, out=None,
+               stream=None):
+        """Attention of one token of each request over its pages (moe_cache_attend): q [B, n_heads, head_dim], tables
+        int32 [B, max_pages], lengths int32 [B], gate None or like q (the output is multiplied by its sigmoid), scale
+        1 / sqrt(head_dim) unless given."""
+        B = q.shape[0]
+        if out is None:
+            out = self._empty((B, self.n_heads, self.head_dim), self.dtype, stream)
+        tab, tab_stride = self._table(tables, B)
+        kc, ks = self._pool(k_cache)
+        vc, vs = self._pool(v_cache)
+        args = CACHE_ATTEND.pack(
+            *self._rows(q, self.n_heads, B), *(self._rows(gate, self.n_heads, B) if gate is not None else (0, 0, 0)),
+            *self._rows(out, self.n_heads, B), tab, tab_stride, self._ints(lengths, B), kc, vc, ks, vs,
+            *self._scales(k_scale, v_scale), B, float(scale) if scale is not None else self.head_dim ** -0.5)
+        _check(self.lib.moe_cache_attend(self.h, args, _stream_ptr(stream)), "moe_cache_attend")
+        return out
+
+    def status(self):
+        f = ctypes.c_uint32(0)
+        s = self.lib.moe_cache_get_status(self.h, ctypes.byref(f))
+        return s, f.value
 
 
 def upload_weights(w: dict, device="cuda"):
