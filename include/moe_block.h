@@ -279,7 +279,7 @@ typedef struct {
   int page_size;      /* tokens per page: 16, 32, 64, 128 or 256 */
   int n_pages;        /* pages of a pool: n_pages * page_size < 2^31 */
   int max_requests;   /* largest B any call will pass: 1..4096 */
-  int max_pages;      /* entries of a table row: max_pages * page_size < 2^31 */
+  int max_pages;      /* entries of a table row: max_pages * page_size < 2^31, times max_requests at most 2^36 */
   int act_dtype;      /* q, k, v, gate, out: MOE_DTYPE_F16 or MOE_DTYPE_BF16 */
   int cache_dtype;    /* act_dtype, or MOE_DTYPE_E4M3 with fp32 scales per key-value head */
   int rope_dim;       /* R: elements of a head that are rotated, a multiple of 16 up to head_dim; 0 for none */
@@ -333,7 +333,8 @@ MOE_API int moe_cache_plan(moe_cache_t *cache, const moe_cache_plan_t *plan, voi
  *   (y_i, y_{i+R/2}) <- (y_i cos a - y_{i+R/2} sin a, y_{i+R/2} cos a + y_i sin a),  a = positions[t] * theta^(-2i/R),
  *   0 <= i < R/2.
  * q goes to q_out (which may be q itself), k and v to slots[t] of the pools; a negative slot writes neither. The
- * pools' page strides are in elements (n_kv_heads * page_size * head_dim when the pool is dense). With an e4m3 cache
+ * pools are 16-byte aligned, their page strides in elements, multiples of head_dim (n_kv_heads * page_size * head_dim
+ * when the pool is dense). With an e4m3 cache
  * k / k_scale[head] and v / v_scale[head] are rounded to e4m3, values past its range to its largest. Computed in
  * fp32 (angles in fp64), rounded once. q may be NULL together with q_out. Slots past the pool write nothing and are
  * reported by moe_cache_get_status. Rows with the same slot race. */
@@ -364,7 +365,7 @@ typedef struct {
   const int32_t *tables;                       /* [B][table_stride] */
   int64_t table_stride;
   const int32_t *lengths;                      /* [B] */
-  const void *k_cache, *v_cache;               /* 16-byte aligned; page strides multiples of 16 bytes */
+  const void *k_cache, *v_cache;
   int64_t k_page_stride, v_page_stride;
   const float *k_scale, *v_scale;              /* [n_kv_heads]: both given with an e4m3 cache, NULL otherwise */
   int64_t n_requests;                          /* B: 0..max_requests */
@@ -378,6 +379,11 @@ MOE_API int moe_cache_attend(moe_cache_t *cache, const moe_cache_attend_t *atten
  * that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits: 1 a wait ran out,
  * 2 a length, 4 a page id or slot, 8 a free_state out of range. */
 MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);
+
+/* Test control of the attention's bounded device waits: timeout_us = microseconds a wait for a copy may last before it
+ * gives up (0 = the default, 500 ms); skip_copy = 1 leaves out the first copy of the next call's first CTA, so that the
+ * wait for it runs out: the call ends with wrong outputs, which moe_cache_get_status reports. No fault is involved. */
+MOE_API int moe_cache_debug_set_wait(moe_cache_t *cache, uint32_t timeout_us, int skip_copy);
 
 /* Host-only check of a shape and of any of the three calls' arguments (each may be NULL): the status that
  * moe_cache_create (bar MOE_ERR_NO_DEVICE) and the call would return before they touch the device. */

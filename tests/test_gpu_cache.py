@@ -441,6 +441,23 @@ def test_attend_reports_bad_pages_and_lengths():
     attend_check(d, out, 16, 2, 128, "f16", "f16")
 
 
+def test_attend_wait_that_runs_out_is_reported():
+    """A copy that never comes: the call ends, the status says so, and the handle works again."""
+    torch = torch_()
+    for lengths in ([700, 90], [30000]):
+        d, n_pages, width = attend_case(lengths, 16, 2, 256, 16, "f16", "f16", 16)
+        c = lib.PagedCache(16, 2, 256, 16, n_pages, 2, width)
+        want = c.attend(**d)
+        c.set_wait(timeout_us=2000, skip_copy=True)
+        c.attend(**d)
+        s, f = c.status()
+        assert s == -5 and f & 1, (s, f)
+        assert c.status() == (0, 0)
+        c.set_wait()
+        assert torch.equal(c.attend(**d), want)
+        assert c.status() == (0, 0)
+
+
 def test_attend_offsets_past_32_bits():
     """Pools of more than 2^32 bytes: pages far apart."""
     torch = torch_()

@@ -14,9 +14,13 @@ struct moe_cache {
   moe_cache_config_t cfg;
   CacheShape S;
   int dev = 0, num_sms = 0;
-  uint8_t* mem = nullptr;                // one allocation: control words, then the frequencies
+  uint8_t* mem = nullptr;                // one allocation: control words, the frequencies (1 KB), the workspace
   uint32_t *status = nullptr, *arrivals = nullptr;
   double* turns = nullptr;
+  uint8_t* workspace = nullptr;          // of the attention: counts, partial results
+  size_t workspace_bytes = 0;
+  uint64_t timeout_ns = 500ull * 1000 * 1000;
+  int skip_copy = 0;
   cudaStream_t last_stream = nullptr;
 };
 
@@ -36,6 +40,8 @@ int check_config(const moe_cache_config_t& c, CacheShape* S) {
       ((int64_t)c.max_pages << lg) > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (c.max_requests < 1 || c.max_requests > CACHE_MAX_REQUESTS) return MOE_ERR_UNSUPPORTED;
+  // the attention counts tiles of 64 tokens or more in 32 bits
+  if (((int64_t)c.max_requests * c.max_pages << lg) > (int64_t)1 << 36) return MOE_ERR_UNSUPPORTED;
   if (c.act_dtype != MOE_DTYPE_F16 && c.act_dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
   if (c.cache_dtype != c.act_dtype && c.cache_dtype != MOE_DTYPE_E4M3) return MOE_ERR_UNSUPPORTED;
   if (c.rope_dim < 0 || c.rope_dim > c.head_dim || c.rope_dim % 16) return MOE_ERR_UNSUPPORTED;
@@ -62,10 +68,10 @@ bool rows_ok(const moe_rows_t& r) {
   return aligned(r.p, 16) && r.row_stride % 8 == 0 && r.head_stride % 8 == 0 && llabs(r.row_stride) < most &&
          llabs(r.head_stride) < most;
 }
-// a pool: 16-byte aligned, pages that do not overlap, each on a 16-byte boundary
+// a pool: 16-byte aligned, pages that do not overlap, whole rows of D apart
 bool pool_ok(const CacheShape& S, const void* p, int64_t page_stride) {
   return aligned(p, 16) && page_stride >= ((int64_t)S.Hkv << S.page_log2) * S.D && page_stride < (int64_t)1 << 38 &&
-         page_stride % (S.e4m3 ? 16 : 8) == 0;
+         page_stride % S.D == 0;
 }
 bool scales_ok(const CacheShape& S, const float* k, const float* v) {
   return S.e4m3 ? aligned(k, 4) && aligned(v, 4) : !k && !v;
@@ -124,7 +130,8 @@ extern "C" int moe_cache_create(const moe_cache_config_t* cfg, moe_cache_t** out
   c->S = S;
   c->dev = dev;
   c->num_sms = prop.multiProcessorCount;
-  const size_t bytes = CTL_WORDS * 4 + (size_t)(S.rope / 2) * 8;
+  c->workspace_bytes = cache_attend_workspace(c->num_sms);
+  const size_t bytes = CTL_WORDS * 4 + 1024 + c->workspace_bytes;
   double turns[128];
   for (int i = 0; i < S.rope / 2; ++i)
     turns[i] = pow(cfg->rope_theta, -2.0 * i / S.rope) / (2.0 * 3.14159265358979323846);
@@ -142,6 +149,7 @@ extern "C" int moe_cache_create(const moe_cache_config_t* cfg, moe_cache_t** out
   c->status = (uint32_t*)c->mem;
   c->arrivals = c->status + 1;
   c->turns = (double*)(c->mem + CTL_WORDS * 4);
+  c->workspace = c->mem + CTL_WORDS * 4 + 1024;
   *out = c;
   return MOE_OK;
 }
@@ -187,8 +195,17 @@ extern "C" int moe_cache_attend(moe_cache_t* c, const moe_cache_attend_t* a, voi
   const int r = check_attend(c->cfg, c->S, *a);
   if (r != MOE_OK || a->n_requests == 0) return r;
   c->last_stream = (cudaStream_t)stream;
-  const cudaError_t e = cache_attend_launch(c->S, *a, c->status, (cudaStream_t)stream);
+  const CacheAttendState w{c->workspace, c->status, c->num_sms, c->timeout_ns, c->skip_copy};
+  c->skip_copy = 0;
+  const cudaError_t e = cache_attend_launch(c->S, *a, w, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_attend");
+}
+
+extern "C" int moe_cache_debug_set_wait(moe_cache_t* c, uint32_t timeout_us, int skip_copy) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  c->timeout_ns = timeout_us ? (uint64_t)timeout_us * 1000ull : 500ull * 1000 * 1000;
+  c->skip_copy = skip_copy ? 1 : 0;
+  return MOE_OK;
 }
 
 extern "C" int moe_cache_get_status(moe_cache_t* c, uint32_t* flags) {
@@ -196,7 +213,9 @@ extern "C" int moe_cache_get_status(moe_cache_t* c, uint32_t* flags) {
   cudaError_t e = cudaStreamSynchronize(c->last_stream);
   uint32_t st = 0;
   if (e == cudaSuccess) e = cudaMemcpy(&st, c->status, 4, cudaMemcpyDeviceToHost);
+  // the counts of parts too: a call that gave up may have left some behind
   if (e == cudaSuccess && st) e = cudaMemset(c->mem, 0, CTL_WORDS * 4);
+  if (e == cudaSuccess && st) e = cudaMemset(c->workspace, 0, c->workspace_bytes);
   if (e == cudaSuccess && st) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return report_cuda(e, "moe_cache_get_status");
   if (flags) *flags = st;

@@ -34,7 +34,17 @@ cudaError_t cache_plan_launch(const CacheShape& S, const moe_cache_plan_t& p, ui
                               int num_sms, cudaStream_t st);
 cudaError_t cache_write_launch(const CacheShape& S, const moe_cache_write_t& w, const double* turns,
                                uint32_t* status, cudaStream_t st);
-cudaError_t cache_attend_launch(const CacheShape& S, const moe_cache_attend_t& a, uint32_t* status, cudaStream_t st);
+
+struct CacheAttendState {
+  void* workspace;                       // cache_attend_workspace bytes, 16-byte aligned, zeroed once
+  uint32_t* status;
+  int num_sms;
+  uint64_t timeout_ns;                   // of the device's waits
+  int skip_copy;
+};
+size_t cache_attend_workspace(int num_sms);
+cudaError_t cache_attend_launch(const CacheShape& S, const moe_cache_attend_t& a, const CacheAttendState& w,
+                                cudaStream_t st);
 
 // ---- 16-bit pairs ----
 template <bool BF16>

@@ -29,7 +29,7 @@ EXPORTS = ["moe_block_create", "moe_block_load_weights", "moe_block_forward", "m
            "moe_stack_forward", "moe_stack_get_status", "moe_stack_layer", "moe_stack_destroy",
            "moe_affine_convert", "moe_affine_free", "moe_block_load_affine",
            "moe_cache_create", "moe_cache_destroy", "moe_cache_plan", "moe_cache_write", "moe_cache_attend",
-           "moe_cache_get_status", "moe_debug_cache_check"]
+           "moe_cache_get_status", "moe_debug_cache_check", "moe_cache_debug_set_wait"]
 
 
 class MoeError(RuntimeError):
@@ -176,6 +176,7 @@ def load_library(path: str = LIB_PATH):
     for f in (lib.moe_cache_plan, lib.moe_cache_write, lib.moe_cache_attend):
         f.argtypes = [vp, vp, vp]
     lib.moe_debug_cache_check.argtypes = [ctypes.POINTER(CacheConfig), vp, vp, vp]
+    lib.moe_cache_debug_set_wait.argtypes = [vp, u32, i]
     lib.moe_cache_get_status.argtypes = [vp, ctypes.POINTER(u32)]
     lib.moe_cache_destroy.argtypes = [vp]
     lib.moe_cache_destroy.restype = None
@@ -564,6 +565,9 @@ class PagedCache:
             *self._scales(k_scale, v_scale), B, float(scale) if scale is not None else self.head_dim ** -0.5)
         _check(self.lib.moe_cache_attend(self.h, args, _stream_ptr(stream)), "moe_cache_attend")
         return out
+
+    def set_wait(self, timeout_us=0, skip_copy=False):
+        _check(self.lib.moe_cache_debug_set_wait(self.h, int(timeout_us), int(bool(skip_copy))), "set_wait")
 
     def status(self):
         f = ctypes.c_uint32(0)
