@@ -139,6 +139,66 @@ struct Place {
   }
 };
 
+// o += V^T P^T over the first `groups` groups of 16 tokens of a tile, of which the first `left` tokens count (EDGE). from:
+// the lane's address in the tile's values, pbase: in P.
+template <class S, bool EDGE>
+__device__ __forceinline__ void add_values(float (&o)[S::MD][S::NT][4], uint32_t from, uint32_t pbase, int groups, int left,
+                                           int t4) {
+#pragma unroll
+  for (int kt = 0; kt < S::KT; kt += 2) {
+    if (EDGE && kt >= groups) break;
+    const bool both = !EDGE || kt + 1 < groups;
+    uint32_t p[S::NT][4];                  // two steps of 16 tokens
+#pragma unroll
+    for (int nt = 0; nt < S::NT; ++nt) ldsm4(p[nt], pbase + (nt * 8 * S::PP + kt * 16) * 2);
+    // tokens past the end hold whatever memory holds: their values become zeros (their weights are)
+    uint32_t keep[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = kt * 16 + i * 8 + 2 * t4;
+      keep[i] = EDGE ? (tok < left ? 0xFFFFu : 0u) | (tok + 1 < left ? 0xFFFF0000u : 0u) : ~0u;
+    }
+    if (S::E4M3) {
+      // a 16-byte chunk of 8 tokens, transposed as 16-bit units: bytes (t0 d0, t0 d1, t1 d0, t1 d1)
+#pragma unroll
+      for (int md = 0; md < S::MD; ++md) {
+        uint32_t v[4], x[4][2];
+        ldsm4_t(v, (from ^ (md << 4)) + kt * S::GROUP_BYTES);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t y = __byte_perm(v[i], 0, 0x3120);
+          x[i][0] = e4m3x2_to_f16x2((uint16_t)y) & keep[i];
+          x[i][1] = e4m3x2_to_f16x2((uint16_t)(y >> 16)) & keep[i];
+        }
+#pragma unroll
+        for (int nt = 0; nt < S::NT; ++nt) {
+          mma16816<false>(o[md][nt], x[0][0], x[0][1], x[1][0], x[1][1], p[nt][0], p[nt][1]);
+          if (both) mma16816<false>(o[md][nt], x[2][0], x[2][1], x[3][0], x[3][1], p[nt][2], p[nt][3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        if (k2 && !both) break;
+#pragma unroll
+        for (int md = 0; md < S::MD; ++md) {
+          uint32_t v[4];
+          ldsm4_t(v, (from ^ (md << 5)) + (kt + k2) * S::GROUP_BYTES);
+          if (EDGE) {
+            v[0] &= keep[2 * k2];
+            v[1] &= keep[2 * k2];
+            v[2] &= keep[2 * k2 + 1];
+            v[3] &= keep[2 * k2 + 1];
+          }
+#pragma unroll
+          for (int nt = 0; nt < S::NT; ++nt)
+            mma16816<S::MMA_BF16>(o[md][nt], v[0], v[1], v[2], v[3], p[nt][2 * k2], p[nt][2 * k2 + 1]);
+        }
+      }
+    }
+  }
+}
+
 template <class S>
 __global__ void __launch_bounds__(THREADS, 2)
     k_cache_attend(const __grid_constant__ AttendArgs A, const __grid_constant__ CUtensorMap kmap,
@@ -281,12 +341,18 @@ __global__ void __launch_bounds__(THREADS, 2)
         *reinterpret_cast<uint4*>(rows_at(a.out, b, i / (D / 8), i % (D / 8) * 8)) = make_uint4(0, 0, 0, 0);
   if (first >= last) return;
 
-  // byte offset, within the 16 tokens of a group, of 16-byte chunk c of row r (the copies' swizzle)
+  // Where a lane's rows of a stage lie. 16-byte chunk c of row r of a group of 16 tokens is at
+  //   c / PER * 16 * CB + r * CB + ((c % PER) ^ swizzle(r)) * 16,      PER = CB / 16,
+  // so with chunks that differ in a constant's bits alone, the address differs by an exclusive or with 16 * constant.
+  constexpr int PER = S::CB / 16;
   auto in_group = [](int r, int c) {
-    constexpr int PER = S::CB / 16;
     const int sw = S::CB == 128 ? r & 7 : (r >> 1) & 3;
-    return (c / PER) * (16 * S::CB) + r * S::CB + (((c % PER) ^ sw) << 4);
+    return (uint32_t)((c / PER) * (16 * S::CB) + r * S::CB + (((c % PER) ^ sw) << 4));
   };
+  const uint32_t ring0 = smem_u32(ring);
+  const uint32_t k_lane = ring0 + in_group(lane & 15, lane >> 4);
+  const uint32_t v_lane = ring0 + (S::E4M3 ? (lane >> 4) * S::GROUP_BYTES + in_group(lane & 15, warp * MD)
+                                           : in_group((lane & 7) + ((lane >> 4) << 3), warp * MD * 2 + ((lane >> 3) & 1)));
   auto wait_full = [&](int stage, uint32_t phase) {
     // once a wait has run out the outputs are lost: run to the end without waiting
     if (!mbar_try_wait(&full[stage], phase) && !s_flags[0] && !mbar_wait(&full[stage], phase, A.timeout_ns)) {
@@ -379,7 +445,6 @@ __global__ void __launch_bounds__(THREADS, 2)
       float s[MT][NT][4];
       wait_full(stage, phase);
       {
-        const uint32_t base = smem_u32(ring + stage * S::STAGE);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const int gr = mt * MATH_WARPS + warp;
@@ -390,13 +455,12 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[mt][nt][i] = s2[nt][i] = 0.f;
           if (gr < groups) {
-            const uint32_t from = base + gr * S::GROUP_BYTES;
-            const int r = lane & 15, hi = lane >> 4;
+            const uint32_t from = k_lane + stage * S::STAGE + gr * S::GROUP_BYTES;
             if (S::E4M3) {
 #pragma unroll
               for (int c = 0; c < S::RB / 16; c += 2) {
                 uint32_t k[4];
-                ldsm4(k, from + in_group(r, c + hi));
+                ldsm4(k, (from ^ (c % PER << 4)) + c / PER * (16 * S::CB));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   mma16816<false>(s[mt][nt], e4m3x2_to_f16x2((uint16_t)k[0]), e4m3x2_to_f16x2((uint16_t)k[1]),
@@ -411,7 +475,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
                 uint32_t k[4];
-                ldsm4(k, from + in_group(r, 2 * ks + hi));
+                ldsm4(k, (from ^ (2 * ks % PER << 4)) + 2 * ks / PER * (16 * S::CB));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma16816<S::MMA_BF16>(ks & 1 ? s2[nt] : s[mt][nt], k[0], k[1], k[2], k[3], q[ks][nt][0], q[ks][nt][1]);
@@ -501,62 +565,10 @@ __global__ void __launch_bounds__(THREADS, 2)
       // ---- O^T += V^T P^T for this warp's quarter of d
       wait_full(stage, phase);
       {
-        const uint32_t base = smem_u32(ring + stage * S::STAGE);
+        const uint32_t from = v_lane + stage * S::STAGE;
         const uint32_t pbase = smem_u32(s_p) + ((lane & 7) * PP + (lane >> 3) * 8) * 2;
-        const bool edge = left < TN;
-#pragma unroll
-        for (int kt = 0; kt < KT; kt += 2) {
-          if (kt >= groups) break;
-          uint32_t p[NT][4];               // two steps of 16 tokens
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) ldsm4(p[nt], pbase + (nt * 8 * PP + kt * 16) * 2);
-          // tokens past the end hold whatever memory holds: their values become zeros (their weights are)
-          uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-          if (edge)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = kt * 16 + i * 8 + 2 * t4;
-              keep[i] = (tok < left ? 0xFFFFu : 0u) | (tok + 1 < left ? 0xFFFF0000u : 0u);
-            }
-          if (S::E4M3) {
-            // a 16-byte chunk of 8 tokens, transposed as 16-bit units: bytes (t0 d0, t0 d1, t1 d0, t1 d1)
-#pragma unroll
-            for (int md = 0; md < MD; ++md) {
-              const int tok = lane & 15;
-              uint32_t v[4], x[4][2];
-              ldsm4_t(v, base + (kt + (lane >> 4)) * S::GROUP_BYTES + in_group(tok, warp * MD + md));
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t y = __byte_perm(v[i], 0, 0x3120);
-                x[i][0] = e4m3x2_to_f16x2((uint16_t)y) & keep[i];
-                x[i][1] = e4m3x2_to_f16x2((uint16_t)(y >> 16)) & keep[i];
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma16816<false>(o[md][nt], x[0][0], x[0][1], x[1][0], x[1][1], p[nt][0], p[nt][1]);
-                if (kt + 1 < groups) mma16816<false>(o[md][nt], x[2][0], x[2][1], x[3][0], x[3][1], p[nt][2], p[nt][3]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-              if (kt + k2 >= groups) break;
-#pragma unroll
-              for (int md = 0; md < MD; ++md) {
-                uint32_t v[4];
-                ldsm4_t(v, base + (kt + k2) * S::GROUP_BYTES +
-                               in_group((lane & 7) + ((lane >> 4) << 3), (warp * MD + md) * 2 + ((lane >> 3) & 1)));
-                v[0] &= keep[2 * k2];
-                v[1] &= keep[2 * k2];
-                v[2] &= keep[2 * k2 + 1];
-                v[3] &= keep[2 * k2 + 1];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma16816<S::MMA_BF16>(o[md][nt], v[0], v[1], v[2], v[3], p[nt][2 * k2], p[nt][2 * k2 + 1]);
-              }
-            }
-          }
-        }
+        if (left >= TN) add_values<S, false>(o, from, pbase, KT, TN, t4);
+        else add_values<S, true>(o, from, pbase, groups, left, t4);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);

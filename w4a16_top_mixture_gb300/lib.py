@@ -452,7 +452,9 @@ class PagedCache:
         self.page_size, self.n_pages, self.max_pages = page_size, n_pages, max_pages
         self.pool_shape = (n_pages, n_kv_heads, page_size, head_dim)
         self.device = torch.device("cuda", torch.cuda.current_device())
-        self._i32 = torch.int32
+        # a call costs the host about as much as the smallest one costs the GPU: what it looks up is kept at hand
+        self._torch, self._dev, self._i32, self._f32 = torch, self.device.index, torch.int32, torch.float32
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
 
     def close(self):
         if getattr(self, "h", None):
@@ -467,19 +469,18 @@ class PagedCache:
 
     def _rows(self, t, heads, rows):
         """(pointer, row stride, head stride) of a [rows, heads, head_dim] tensor of the activations' type."""
-        st = t.stride()
-        if t.dtype != self.dtype or t.shape != (rows, heads, self.head_dim) or st[2] != 1 or t.device != self.device:
+        if t.dtype is not self.dtype or t.shape != (rows, heads, self.head_dim) or t.get_device() != self._dev or t.stride(2) != 1:
             raise ValueError(f"want {self.dtype} [{rows}, {heads}, {self.head_dim}] on {self.device}, innermost stride 1; "
-                             f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
-        return t.data_ptr(), st[0] if rows > 1 else 0, st[1] if heads > 1 else 0
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+        return t.data_ptr(), t.stride(0) if rows > 1 else 0, t.stride(1) if heads > 1 else 0
 
-    def _ints(self, t, *shape):
-        if t.dtype != self._i32 or t.shape != shape or not t.is_contiguous() or t.device != self.device:
-            raise ValueError(f"want a contiguous int32 {shape} on {self.device}; got {t.dtype} {tuple(t.shape)} on {t.device}")
+    def _vector(self, t, n, dtype):
+        if t.dtype is not dtype or t.shape != (n,) or t.get_device() != self._dev or not t.is_contiguous():
+            raise ValueError(f"want a contiguous {dtype} [{n}] on {self.device}; got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
     def _table(self, t, rows):
-        if (t.dtype != self._i32 or t.shape != (rows, self.max_pages) or t.device != self.device
+        if (t.dtype is not self._i32 or t.shape != (rows, self.max_pages) or t.get_device() != self._dev
                 or (t.stride(1) != 1 and rows and self.max_pages > 1) or (rows > 1 and t.stride(0) < self.max_pages)):
             raise ValueError(f"want tables int32 [{rows}, {self.max_pages}] on {self.device}, rows apart; got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
@@ -487,26 +488,26 @@ class PagedCache:
 
     def _pool(self, t):
         st, (_, _, p, d) = t.stride(), self.pool_shape
-        if (t.dtype != self.cache_dtype or t.shape != self.pool_shape or st[3] != 1 or st[2] != d
-                or (st[1] != p * d and self.n_kv_heads > 1) or t.device != self.device):
+        if (t.dtype is not self.cache_dtype or t.shape != self.pool_shape or t.get_device() != self._dev or st[3] != 1
+                or st[2] != d or (st[1] != p * d and self.n_kv_heads > 1)):
             raise ValueError(f"want a pool {self.cache_dtype} {self.pool_shape} on {self.device}, dense within a page; got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
         return t.data_ptr(), max(st[0], self.n_kv_heads * p * d)
 
     def _scales(self, k, v):
-        import torch
-        for t in (k, v):
-            if t is not None and (t.dtype != torch.float32 or t.shape != (self.n_kv_heads,) or not t.is_contiguous()
-                                  or t.device != self.device):
-                raise ValueError(f"want scales fp32 [{self.n_kv_heads}] on {self.device}; got {t.dtype} {tuple(t.shape)}")
-        return (k.data_ptr() if k is not None else 0), (v.data_ptr() if v is not None else 0)
+        return (self._vector(k, self.n_kv_heads, self._f32) if k is not None else 0,
+                self._vector(v, self.n_kv_heads, self._f32) if v is not None else 0)
 
     def _empty(self, shape, dtype, stream):
-        import torch
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self._torch.empty(shape, dtype=dtype, device=self.device)
+        with self._torch.cuda.stream(stream):
+            return self._torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _call(self, f, args, stream, what):
+        s = f(self.h, args, stream.cuda_stream if stream is not None else self._raw_stream(self._dev))
+        if s != MOE_OK:
+            raise MoeError(s, what)
 
     def plan(self, lengths, new_tokens, tables, free_pages, free_state, n_rows, out=None, stream=None):
         """Block tables and slot maps of a step (moe_cache_plan): lengths, new_tokens int32 [B] (new_tokens may be None:
@@ -516,13 +517,13 @@ class PagedCache:
         if out is None:
             out = CachePlan(*self._empty((2 * n_rows + 2 * B + 4,), self._i32, stream).split(
                 (n_rows, n_rows, B + 1, B, 3)))
-        tab, tab_stride = self._table(tables, B)
+        i32 = self._i32
         args = CACHE_PLAN.pack(
-            self._ints(lengths, B), self._ints(new_tokens, B) if new_tokens is not None else 0, tab, tab_stride,
-            self._ints(free_pages, self.n_pages), self._ints(free_state, 3), self._ints(out.free_state, 3),
-            self._ints(out.lengths, B), self._ints(out.starts, B + 1), self._ints(out.slots, n_rows),
-            self._ints(out.positions, n_rows), B, n_rows)
-        _check(self.lib.moe_cache_plan(self.h, args, _stream_ptr(stream)), "moe_cache_plan")
+            self._vector(lengths, B, i32), self._vector(new_tokens, B, i32) if new_tokens is not None else 0,
+            *self._table(tables, B), self._vector(free_pages, self.n_pages, i32), self._vector(free_state, 3, i32),
+            self._vector(out.free_state, 3, i32), self._vector(out.lengths, B, i32), self._vector(out.starts, B + 1, i32),
+            self._vector(out.slots, n_rows, i32), self._vector(out.positions, n_rows, i32), B, n_rows)
+        self._call(self.lib.moe_cache_plan, args, stream, "moe_cache_plan")
         return out
 
     def write(self, q, k, v, positions, slots, k_cache, v_cache, q_gamma=None, k_gamma=None, k_scale=None, v_scale=None,
@@ -533,19 +534,16 @@ class PagedCache:
         T = k.shape[0]
         if q is not None and q_out is None:
             q_out = self._empty((T, self.n_heads, self.head_dim), self.dtype, stream)
-        for g in (q_gamma, k_gamma):
-            if g is not None and (g.dtype != self.dtype or g.shape != (self.head_dim,) or not g.is_contiguous()
-                                  or g.device != self.device):
-                raise ValueError(f"want a norm weight {self.dtype} [{self.head_dim}] on {self.device}; got {g.dtype} "
-                                 f"{tuple(g.shape)} on {g.device}")
         kc, ks = self._pool(k_cache)
         vc, vs = self._pool(v_cache)
         args = CACHE_WRITE.pack(
             *(self._rows(q, self.n_heads, T) if q is not None else (0, 0, 0)), *self._rows(k, self.n_kv_heads, T),
             *self._rows(v, self.n_kv_heads, T), *(self._rows(q_out, self.n_heads, T) if q is not None else (0, 0, 0)),
-            q_gamma.data_ptr() if q_gamma is not None else 0, k_gamma.data_ptr() if k_gamma is not None else 0,
-            self._ints(positions, T), self._ints(slots, T), kc, vc, ks, vs, *self._scales(k_scale, v_scale), T)
-        _check(self.lib.moe_cache_write(self.h, args, _stream_ptr(stream)), "moe_cache_write")
+            self._vector(q_gamma, self.head_dim, self.dtype) if q_gamma is not None else 0,
+            self._vector(k_gamma, self.head_dim, self.dtype) if k_gamma is not None else 0,
+            self._vector(positions, T, self._i32), self._vector(slots, T, self._i32), kc, vc, ks, vs,
+            *self._scales(k_scale, v_scale), T)
+        self._call(self.lib.moe_cache_write, args, stream, "moe_cache_write")
         return q_out
 
     def attend(self, q, tables, lengths, k_cache, v_cache, gate=None, scale=None, k_scale=None, v_scale=None, out=None,
@@ -556,14 +554,13 @@ class PagedCache:
         B = q.shape[0]
         if out is None:
             out = self._empty((B, self.n_heads, self.head_dim), self.dtype, stream)
-        tab, tab_stride = self._table(tables, B)
         kc, ks = self._pool(k_cache)
         vc, vs = self._pool(v_cache)
         args = CACHE_ATTEND.pack(
             *self._rows(q, self.n_heads, B), *(self._rows(gate, self.n_heads, B) if gate is not None else (0, 0, 0)),
-            *self._rows(out, self.n_heads, B), tab, tab_stride, self._ints(lengths, B), kc, vc, ks, vs,
-            *self._scales(k_scale, v_scale), B, float(scale) if scale is not None else self.head_dim ** -0.5)
-        _check(self.lib.moe_cache_attend(self.h, args, _stream_ptr(stream)), "moe_cache_attend")
+            *self._rows(out, self.n_heads, B), *self._table(tables, B), self._vector(lengths, B, self._i32), kc, vc, ks, vs,
+            *self._scales(k_scale, v_scale), B, scale if scale is not None else self.head_dim ** -0.5)
+        self._call(self.lib.moe_cache_attend, args, stream, "moe_cache_attend")
         return out
 
     def set_wait(self, timeout_us=0, skip_copy=False):
