@@ -40,8 +40,8 @@ int check_config(const moe_cache_config_t& c, CacheShape* S) {
       ((int64_t)c.max_pages << lg) > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (c.max_requests < 1 || c.max_requests > CACHE_MAX_REQUESTS) return MOE_ERR_UNSUPPORTED;
-  // the attention counts tiles of 64 tokens or more in 32 bits
-  if (((int64_t)c.max_requests * c.max_pages << lg) > (int64_t)1 << 36) return MOE_ERR_UNSUPPORTED;
+  // the attention numbers its tiles, of 64 tokens or more for each head, in 31 bits
+  if (((int64_t)c.max_pages << lg) * c.max_requests > ((int64_t)1 << 36) / c.n_heads) return MOE_ERR_UNSUPPORTED;
   if (c.act_dtype != MOE_DTYPE_F16 && c.act_dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
   if (c.cache_dtype != c.act_dtype && c.cache_dtype != MOE_DTYPE_E4M3) return MOE_ERR_UNSUPPORTED;
   if (c.rope_dim < 0 || c.rope_dim > c.head_dim || c.rope_dim % 16) return MOE_ERR_UNSUPPORTED;

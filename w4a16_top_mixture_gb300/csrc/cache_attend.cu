@@ -5,12 +5,14 @@
 //   Work. The tokens of a request and key-value head (an item) are cut into tiles of TN. The tiles of all items, one
 //   after another, are divided evenly over the CTAs, whatever the requests' lengths are: a CTA walks its range, and an
 //   item that crosses a CTA's border is split. Nobody waits: every CTA of a split item leaves its partial sums in the
-//   workspace, and the one that counts itself last joins them, in the order of the tiles.
+//   workspace, and the one that counts itself last joins them, in the order of the tiles (in two steps where they are many).
 //   Copies. One warp walks the block table ahead of the rest and brings 16 tokens x 128 bytes at a time with TMA into a
-//   ring of stages, keys and values of a tile in stages of their own, across the borders of items.
+//   ring of stages, keys and values in stages of their own, across the borders of items; queries and gates of the next
+//   item with it.
 //   Products. Heads are the narrow side of the tensor cores' m16n8k16: S^T[tokens x heads] = K Q^T and
-//   O^T[d x heads] = V^T P^T, so that eight query heads fill a tile. Four warps share a tile: each takes 16 (32) tokens
-//   of S and then a quarter of d of O. One maximum for the four, exchanged through shared memory, lets O be kept once.
+//   O^T[d x heads] = V^T P^T, so that eight query heads fill a tile. The math warps share a tile: each takes 16 tokens
+//   (or 32) of S and then its share of the rows d of O. One maximum for all of them, exchanged through shared memory, lets
+//   O be kept once.
 #include <cuda.h>
 
 #include "cache.cuh"
@@ -19,8 +21,9 @@
 namespace moe {
 namespace {
 
-constexpr int MATH_WARPS = 4, THREADS = 32 * (MATH_WARPS + 1);
-constexpr int COUNT_WORDS = 2048;                 // of the workspace; two CTAs to each of at most 1024 SMs
+constexpr int GROUP = 10, FLAT = 20;              // CTAs whose parts are joined first; from FLAT + 1 parts on
+constexpr int MAX_CTAS = 2048, COUNT_WORDS = MAX_CTAS + MAX_CTAS / GROUP * 2;    // of the workspace
+constexpr int PART_MAX = 16 * 256 + 32;           // floats of the largest part
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -28,8 +31,10 @@ struct AttendArgs {
   int B, Hq, Hkv, group, head_tiles, page_log2, n_pages, n_stages;
   long long max_len;
   float scale;
-  float* parts;              // [CTA][2][part_floats]: the item a CTA began in the middle of, the one it left so
+  float* parts;              // [CTA][2][part floats]: the item a CTA begins in the middle of, the one it leaves so
   uint32_t* counts;          // [CTA]: parts that have arrived of the item that crosses the CTA's end
+  float* group_parts;        // [group of CTAs][2], as parts: the joined parts of a group
+  uint32_t* group_counts;    // [group of CTAs][2]
   uint32_t* status;
   uint64_t timeout_ns;
   int skip_copy;             // test: the first copy of CTA 0 is left out, so that its wait runs out
@@ -40,17 +45,20 @@ struct Shape {
   static constexpr int D = D_, NT = NT_, NH = 8 * NT_;      // query heads of an item
   static constexpr bool BF16 = BF16_, E4M3 = E4M3_;
   static constexpr bool MMA_BF16 = BF16_ && !E4M3_;         // e4m3 is exact in fp16
+  static constexpr int WARPS = 4;                           // of the products
+  static constexpr int MATH = 32 * WARPS, THREADS = MATH + 32;
   static constexpr int RB = D * (E4M3 ? 1 : 2);             // bytes of a token's row
   static constexpr int CB = RB < 128 ? RB : 128, CH = RB / CB;
-  static constexpr int TN = RB >= 512 ? 64 : 128;           // tokens of a tile: stages of 8 to 32 KB
-  static constexpr int MT = TN / 64;                        // 16-token tiles of S per warp
+  static constexpr int TN = RB >= 512 ? 64 : 128;           // tokens of a tile
+  static constexpr int MT = TN / 16 / WARPS;                // 16-token tiles of S per warp
   static constexpr int KT = TN / 16;
-  static constexpr int STAGE = TN * RB, GROUP_BYTES = 16 * RB;
-  static constexpr int MD = D / 64;                         // 16-row tiles of O per warp
+  static constexpr int GPS = 16384 / (16 * RB) < KT ? 16384 / (16 * RB) : KT;   // 16-token groups of a stage
+  static constexpr int GROUP_BYTES = 16 * RB, STAGE = GPS * GROUP_BYTES;
+  static constexpr int MD = D / 16 / WARPS;                 // 16-row tiles of O per warp
   static constexpr int PP = TN + 8;                         // pitch of P: rows of 8 fall on different banks
+  static constexpr int QP = D + 8;                          // pitch of queries and gates
   static constexpr int PART = NH * D + 2 * NH;              // floats of a partial result: O, maxima, sums
-  static constexpr int JOIN = 64;                           // parts joined per step
-  static constexpr int MISC = 1024 /* barriers */ + NH * PP * 2 + MATH_WARPS * NH * 8 + JOIN * NH * 4 + 2 * NH * 4;
+  static constexpr int MISC = 1024 /* barriers */ + 2 * NH * QP * 2 + NH * PP * 2 + 2 * WARPS * NH * 4;
 };
 
 // ---- instructions ----
@@ -90,72 +98,60 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// y * sigmoid(x): exp and quotient good to a few 2^-23
+__device__ __forceinline__ float gated(float y, float x) { return __fdividef(y, 1.f + __expf(-x)); }
 __device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* m, int x, int row, int page, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
       ::"r"(smem_u32(dst)), "l"(m), "r"(x), "r"(row), "r"(page), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void math_barrier() { named_bar(1, 32 * MATH_WARPS); }
-
-// ---- the division of the work ----
-// Tiles are numbered request by request, within a request head by head; chunk of them go to a CTA.
-struct Division {
-  long long tiles, chunk;
-};
-__host__ __device__ inline Division divide(long long tiles, int ctas) {
-  Division d;
-  d.tiles = tiles;
-  d.chunk = (tiles + ctas - 1) / ctas;
-  if (d.chunk < 1) d.chunk = 1;
-  return d;
+__device__ __forceinline__ uint16_t* rows_at(const moe_rows_t& r, int b, int h, int d) {
+  return (uint16_t*)r.p + b * r.row_stride + h * r.head_stride + d;
 }
+template <class S>
+__device__ __forceinline__ void math_barrier() { named_bar(1, S::MATH); }
+// ---- the division of the work ----
+// Tiles are numbered request by request, within a request head by head; CTA c takes tiles c * share .. (c + 1) * share - 1.
+__host__ __device__ inline int even_share(int tiles, int ctas) {
+  return tiles > 0 ? (int)(((long long)tiles + ctas - 1) / ctas) : 1;
+}
+
+template <class S>
+__device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + S::TN - 1) / S::TN); }
 
 // A place in the list of tiles: tile j of request b's head h (h: key-value head and its tile of query heads).
 struct Place {
   int b, h, j, n;      // n: tiles of each head of request b
-  __device__ void find(const int* upto, int B, int heads, long long tile) {
-    int lo = 0, hi = B - 1;      // the request that holds the tile: the first whose tiles end past it
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if ((long long)upto[mid] * heads > tile) hi = mid; else lo = mid + 1;
-    }
-    b = lo;
-    const int first = b ? upto[b - 1] : 0;
-    n = upto[b] - first;
-    const long long in = tile - (long long)first * heads;
-    h = (int)(in / n);
-    j = (int)(in - (long long)h * n);
-  }
   // to the first tile of the next item (which exists)
-  __device__ void next_item(const int* upto, int heads) {
+  template <class S>
+  __device__ __forceinline__ void next_item(const int* len, int heads) {
     j = 0;
     if (++h < heads) return;
     h = 0;
-    do {
-      ++b;
-      n = upto[b] - upto[b - 1];
-    } while (n == 0);
+    do n = tiles_of<S>(len[++b]);
+    while (n == 0);
   }
 };
 
-// o += V^T P^T over the first `groups` groups of 16 tokens of a tile, of which the first `left` tokens count (EDGE). from:
-// the lane's address in the tile's values, pbase: in P.
+// o += V^T P^T over the groups of 16 tokens of one stage, from group g0 of the tile on; the first `left` tokens of the tile
+// count (EDGE). from: the lane's address in the stage, pbase: in P.
 template <class S, bool EDGE>
-__device__ __forceinline__ void add_values(float (&o)[S::MD][S::NT][4], uint32_t from, uint32_t pbase, int groups, int left,
+__device__ __forceinline__ void add_values(float (&o)[S::MD][S::NT][4], uint32_t from, uint32_t pbase, int g0, int left,
                                            int t4) {
 #pragma unroll
-  for (int kt = 0; kt < S::KT; kt += 2) {
-    if (EDGE && kt >= groups) break;
-    const bool both = !EDGE || kt + 1 < groups;
+  for (int kt = 0; kt < S::GPS; kt += 2) {
+    const int tok0 = (g0 + kt) * 16;
+    if (EDGE && tok0 >= left) break;
+    const bool both = !EDGE || tok0 + 16 < left;
     uint32_t p[S::NT][4];                  // two steps of 16 tokens
 #pragma unroll
-    for (int nt = 0; nt < S::NT; ++nt) ldsm4(p[nt], pbase + (nt * 8 * S::PP + kt * 16) * 2);
+    for (int nt = 0; nt < S::NT; ++nt) ldsm4(p[nt], pbase + nt * 8 * S::PP * 2 + tok0 * 2);
     // tokens past the end hold whatever memory holds: their values become zeros (their weights are)
     uint32_t keep[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int tok = kt * 16 + i * 8 + 2 * t4;
+      const int tok = tok0 + i * 8 + 2 * t4;
       keep[i] = EDGE ? (tok < left ? 0xFFFFu : 0u) | (tok + 1 < left ? 0xFFFF0000u : 0u) : ~0u;
     }
     if (S::E4M3) {
@@ -199,25 +195,133 @@ __device__ __forceinline__ void add_values(float (&o)[S::MD][S::NT][4], uint32_t
   }
 }
 
+// An item of which a CTA holds a part: request, head, and the CTAs that hold parts. b < 0: none.
+struct Split {
+  int b, h, c0, c1;
+};
+
+// The joined parts of a split item: NH * D / 4 groups of four d, PER of them to a thread.
 template <class S>
-__global__ void __launch_bounds__(THREADS, 2)
+struct Joined {
+  static constexpr int NH = S::NH, D = S::D, VECS = NH * D / 4, PER = (VECS + S::MATH - 1) / S::MATH;
+  static_assert(VECS % S::MATH == 0, "whole vectors for each thread");
+  float4 y[PER];
+  float sum[PER];
+  uint2 gate[PER];
+
+  float top;               // of head tid % NH
+
+  __device__ __forceinline__ void clear() {
+    top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      sum[e] = 0.f;
+    }
+  }
+  // n further parts, from shared memory; the order of the sum is that of the parts. All math warps, in step.
+  // s_max: [WARPS][NH], s_w: [n][NH] weights beside weighted sums, and [NH] factors of what is there already
+  __device__ __forceinline__ void add(const float* parts, int n, float* s_max, float2* s_w, int tid) {
+    const int h = tid % NH, lane = tid & 31, warp = tid >> 5;
+    float x = top;
+    for (int k = tid / NH; k < n; k += S::MATH / NH) x = fmaxf(x, parts[k * S::PART + NH * D + h]);
+#pragma unroll
+    for (int w = NH; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
+    if (lane < NH) s_max[warp * NH + h] = x;
+    math_barrier<S>();
+#pragma unroll
+    for (int w = 0; w < S::WARPS; ++w) x = fmaxf(x, s_max[w * NH + h]);
+    const float base = x == -INFINITY ? 0.f : x;
+    for (int k = tid / NH; k < n; k += S::MATH / NH) {
+      const float w = exp2_fast(parts[k * S::PART + NH * D + h] - base);
+      s_w[k * NH + h] = make_float2(w, w * parts[k * S::PART + NH * D + NH + h]);
+    }
+    if (tid < NH) s_w[n * NH + h].x = exp2_fast(top - base);
+    top = x;
+    math_barrier<S>();
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int at4 = (e * S::MATH + tid) * 4, he = at4 / D;
+      const float c = s_w[n * NH + he].x;
+      y[e] = make_float4(y[e].x * c, y[e].y * c, y[e].z * c, y[e].w * c);
+      sum[e] *= c;
+    }
+#pragma unroll 4
+    for (int k = 0; k < n; ++k)
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const int at4 = (e * S::MATH + tid) * 4, he = at4 / D;
+        const float4 v = *reinterpret_cast<const float4*>(parts + k * S::PART + at4);
+        const float2 w = s_w[k * NH + he];
+        y[e].x = fmaf(v.x, w.x, y[e].x);
+        y[e].y = fmaf(v.y, w.x, y[e].y);
+        y[e].z = fmaf(v.z, w.x, y[e].z);
+        y[e].w = fmaf(v.w, w.x, y[e].w);
+        sum[e] += w.y;
+      }
+  }
+  // as a part of its own
+  __device__ __forceinline__ void keep(float* part, int tid) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int at4 = (e * S::MATH + tid) * 4;
+      *reinterpret_cast<float4*>(part + at4) = y[e];
+      if (at4 % D == 0) part[NH * D + NH + at4 / D] = sum[e];
+    }
+    if (tid < NH) part[NH * D + tid] = top;
+  }
+  // the gates, on their way while the parts are joined
+  __device__ __forceinline__ void fetch_gates(const AttendArgs& A, int b, int h0, int nh, int tid) {
+    if (!A.a.gate.p) return;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int at4 = (e * S::MATH + tid) * 4, h = at4 / D, d = at4 % D;
+      gate[e] = h < nh ? __ldcg(reinterpret_cast<const uint2*>(rows_at(A.a.gate, b, h0 + h, d))) : make_uint2(0, 0);
+    }
+  }
+  // as the output
+  __device__ __forceinline__ void finish(const AttendArgs& A, int b, int h0, int nh, float vs, int tid) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int at4 = (e * S::MATH + tid) * 4, h = at4 / D, d = at4 % D;
+      if (h >= nh) continue;
+      const float f = vs / sum[e];
+      float x[4] = {y[e].x * f, y[e].y * f, y[e].z * f, y[e].w * f};
+      if (A.a.gate.p) {
+        const float2 g0 = unpack2<S::BF16>(gate[e].x), g1 = unpack2<S::BF16>(gate[e].y);
+        x[0] = gated(x[0], g0.x);
+        x[1] = gated(x[1], g0.y);
+        x[2] = gated(x[2], g1.x);
+        x[3] = gated(x[3], g1.y);
+      }
+      *reinterpret_cast<uint2*>(rows_at(A.a.out, b, h0 + h, d)) =
+          make_uint2(pack2<S::BF16>(x[0], x[1]), pack2<S::BF16>(x[2], x[3]));
+    }
+  }
+};
+
+template <class S>
+__global__ void __launch_bounds__(S::THREADS, 2)
     k_cache_attend(const __grid_constant__ AttendArgs A, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
-  constexpr int D = S::D, NT = S::NT, NH = S::NH, TN = S::TN, MT = S::MT, KT = S::KT, MD = S::MD, PP = S::PP;
+  constexpr int D = S::D, NT = S::NT, NH = S::NH, TN = S::TN, MT = S::MT, KT = S::KT, MD = S::MD, PP = S::PP, QP = S::QP;
+  constexpr int GPS = S::GPS, WARPS = S::WARPS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* const misc = ring + A.n_stages * S::STAGE;
   uint64_t* const full = (uint64_t*)misc;            // [n_stages <= 32]
   uint64_t* const empty = full + 32;
-  volatile int* const s_flags = (int*)(empty + 32);  // 0: a wait ran out; 1: last to arrive
-  int* const s_scan = (int*)(empty + 32) + 4;        // [THREADS / 32 + 1]
-  uint16_t* const s_p = (uint16_t*)(misc + 1024);    // [NH][PP]
-  float* const s_max = (float*)(s_p + NH * PP);      // [MATH_WARPS][NH]
-  float* const s_sum = s_max + MATH_WARPS * NH;      // [MATH_WARPS][NH]
-  float* const s_w = s_sum + MATH_WARPS * NH;        // [JOIN][NH]
-  float* const s_top = s_w + S::JOIN * NH;           // [2][NH]
-  int* const s_upto = (int*)(s_top + 2 * NH);        // [B]: tiles of a head, of the requests up to this one
-  int* const s_len = s_upto + A.B;                   // [B]
+  uint64_t* const rows_full = empty + 32;            // 0: queries, 1: gates
+  uint64_t* const rows_empty = rows_full + 2;
+  uint64_t* const join_full = rows_empty + 2;        // parts, when the ring is done with
+  volatile int* const s_flags = (int*)(join_full + 1);    // 0: a wait ran out; 1, 2: last to arrive
+  int* const s_scan = (int*)(join_full + 1) + 4;     // [THREADS / 32]
+  int* const s_place = s_scan + 16;                  // [3]
+  uint16_t* const s_q = (uint16_t*)(misc + 1024);    // [2][NH][QP]: queries, gates
+  uint16_t* const s_p = s_q + 2 * NH * QP;           // [NH][PP]
+  float* const s_max = (float*)(s_p + NH * PP);      // [WARPS][NH]
+  float* const s_sum = s_max + WARPS * NH;           // [WARPS][NH]
+  int* const s_len = (int*)(s_sum + WARPS * NH);     // [B]
 
   const moe_cache_attend_t& a = A.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -226,102 +330,153 @@ __global__ void __launch_bounds__(THREADS, 2)
   if (tid == 0) {
     for (int s = 0; s < A.n_stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], MATH_WARPS);
+      mbar_init(&empty[s], WARPS);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&rows_full[s], 1);
+      mbar_init(&rows_empty[s], WARPS);
+    }
+    mbar_init(join_full, 1);
     fence_mbar_init();
     s_flags[0] = 0;
   }
-  // lengths and the running number of tiles
-  int carry = 0;
-  for (int b0 = 0; b0 < A.B; b0 += THREADS) {
-    const int b = b0 + tid;
-    int len = b < A.B ? a.lengths[b] : 0;
+  // lengths and the running number of tiles: a thread's requests lie side by side, so that all its loads are on their way
+  // at once
+  const int each = (A.B + S::THREADS - 1) / S::THREADS, b_begin = tid * each < A.B ? tid * each : A.B;
+  const int b_end = b_begin + each < A.B ? b_begin + each : A.B;
+  int mine = 0;
+#pragma unroll 4
+  for (int b = b_begin; b < b_end; ++b) {
+    int len = __ldcg(a.lengths + b);
     if (len < 0 || len > A.max_len) {
       atomicOr(A.status, CACHE_BAD_LENGTH);
       len = len < 0 ? 0 : (int)A.max_len;
     }
-    int x = (int)(((long long)len + TN - 1) / TN);
+    s_len[b] = len;
+    mine += tiles_of<S>(len);
+  }
+  // a wait ran out in an earlier call, or has in this one: the counts are off until the status is read
+  const bool dead = tid == 0 && (*(volatile uint32_t*)A.status & CACHE_BAD_WAIT);
+  int upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) s_scan[warp] = upto;
+  if (__syncthreads_or(dead)) return;
+  int carry = 0;
+  for (int w = 0; w < S::THREADS / 32; ++w) {
+    if (w < warp) upto += s_scan[w];
+    carry += s_scan[w];
+  }
+  const int tiles = carry * heads, share = even_share(tiles, gridDim.x);
+  const int first = (long long)share * blockIdx.x < tiles ? share * blockIdx.x : tiles;
+  const int last = share < tiles - first ? first + share : tiles;
+  // where the CTA begins: found by the thread that holds the request
+  if (first < last && (upto - mine) * heads <= first && first < upto * heads) {
+    int before = upto - mine, b = b_begin, n = tiles_of<S>(s_len[b]);
+    while ((before + n) * heads <= first) {
+      before += n;
+      n = tiles_of<S>(s_len[++b]);
     }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    int before = carry;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) before += s_scan[w];
-      carry += s_scan[w];
-    }
-    if (b < A.B) {
-      s_upto[b] = before + x;
-      s_len[b] = len;
-    }
+    const int in = first - before * heads;
+    s_place[0] = b;
+    s_place[1] = in / n;
+    s_place[2] = in % n;
   }
   __syncthreads();
-  const Division dv = divide((long long)carry * heads, gridDim.x);
-  const long long first = dv.chunk * blockIdx.x;
-  const long long last = first + dv.chunk < dv.tiles ? first + dv.chunk : dv.tiles;
+  const Place begin = {s_place[0], s_place[1], s_place[2], first < last ? tiles_of<S>(s_len[s_place[0]]) : 0};
 
-  if (warp == MATH_WARPS) {
+  if (warp == WARPS) {
     // ---------------------------------------------------------------- copies
-    if (first >= last) return;
-    Place at;
-    at.find(s_upto, A.B, heads, first);
-    const int grp = lane / S::CH, chunk = lane % S::CH;
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, n_rows[2] = {0, 0};          // copies of queries and of gates so far
     bool skip = A.skip_copy && blockIdx.x == 0;
-    // the page of this lane's 16 tokens, one tile ahead of its copies
+    // Waits until a buffer is free. False: a wait ran out, here or in a math warp, which then no longer waits. Nothing
+    // more is copied then, and what is on its way is waited for (boundedly) before the CTA ends: earlier stages of this
+    // lap, later ones of the last, the rows.
+    auto free_to_fill = [&](uint64_t* bar, uint32_t parity) {
+      if (!mbar_wait(bar, parity, A.timeout_ns)) {
+        s_flags[0] = 1;
+        atomicOr(A.status, CACHE_BAD_WAIT);
+      }
+      __syncwarp();
+      if (!s_flags[0]) return true;
+      int s = stage;
+      uint32_t ph = phase;
+      for (int i = 0; i < A.n_stages; ++i) {
+        if (s == 0) { s = A.n_stages; ph ^= 1; }
+        --s;
+        mbar_wait(&full[s], ph, A.timeout_ns);
+      }
+      for (int i = 0; i < 2; ++i)
+        if (n_rows[i]) mbar_wait(&rows_full[i], (n_rows[i] - 1) & 1, A.timeout_ns);
+      return false;
+    };
+    // the item's rows of queries (0) or gates (1), a head's D elements each
+    auto copy_rows = [&](int which, const Place& p) {
+      const uint32_t n = n_rows[which];
+      if (!free_to_fill(&rows_empty[which], (n & 1) ^ 1)) return false;
+      const int h_in = (p.h % A.head_tiles) * NH;
+      const int h0 = (p.h / A.head_tiles) * A.group + h_in;
+      const int nh = A.group - h_in < NH ? A.group - h_in : NH;
+      if (lane == 0) mbar_expect_tx(&rows_full[which], nh * D * 2);
+      __syncwarp();
+      if (lane < nh)
+        bulk_g2s(s_q + (which * NH + lane) * QP, rows_at(which ? a.gate : a.q, p.b, h0 + lane, 0), D * 2,
+                 &rows_full[which]);
+      n_rows[which] = n + 1;
+      return true;
+    };
+    // the page of group `lane` of a tile, one tile ahead of its copies
     auto page_of = [&](const Place& p) {
-      const long long tok = (long long)p.j * TN + grp * 16;
-      if (grp >= KT || tok >= s_len[p.b]) return -1;
-      int page = __ldg(a.tables + (long long)p.b * a.table_stride + (tok >> A.page_log2));
+      const long long tok = (long long)p.j * TN + lane * 16;
+      if (lane >= KT || tok >= s_len[p.b]) return -1;
+      int page = __ldcg(a.tables + (long long)p.b * a.table_stride + (tok >> A.page_log2));
       if (page < 0 || page >= A.n_pages) {
         atomicOr(A.status, CACHE_BAD_PAGE);
         page = A.n_pages;               // out of range: the copy reads zeros
       }
       return page;
     };
-    int page = page_of(at);
-    for (long long t = first; t < last; ++t) {
+    if (first >= last) return;
+    Place at = begin;
+    int page = page_of(at), j_begin = at.j;
+    if (!copy_rows(0, at)) return;
+    for (int t = first; t < last; ++t) {
       Place nx = at;
-      if (t + 1 < last) {
-        if (++nx.j == nx.n) nx.next_item(s_upto, heads);
+      const bool more = t + 1 < last, ends = at.j + 1 == at.n;
+      if (more) {
+        ++nx.j;
+        if (ends) nx.template next_item<S>(s_len, heads);
       }
-      const int page_next = t + 1 < last ? page_of(nx) : -1;
+      const int page_next = more ? page_of(nx) : -1;
       const int left = s_len[at.b] - at.j * TN;
       const int groups = left >= TN ? KT : (left + 15) >> 4;
-      const int row = ((at.h / A.head_tiles) << A.page_log2) + (((at.j * TN) + grp * 16) & ((1 << A.page_log2) - 1));
-#pragma unroll
+      const int row0 = (at.h / A.head_tiles) << A.page_log2;
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        const bool ok = mbar_wait(&empty[stage], phase ^ 1, A.timeout_ns);
-        if (!ok && lane == 0) {
-          s_flags[0] = 1;
-          atomicOr(A.status, CACHE_BAD_WAIT);
+#pragma unroll 1
+        for (int g0 = 0; g0 < groups; g0 += GPS) {
+          if (!free_to_fill(&empty[stage], phase ^ 1)) return;
+          const int n = groups - g0 < GPS ? groups - g0 : GPS;
+          if (lane == 0) mbar_expect_tx(&full[stage], n * S::GROUP_BYTES);
+          const int grp = lane / S::CH, x = lane % S::CH;
+          const int pg = __shfl_sync(0xFFFFFFFFu, page, (g0 + grp) & 31);
+          if (grp < n && !skip)
+            tma_rows(ring + stage * S::STAGE + grp * S::GROUP_BYTES + x * 16 * S::CB, kv ? &vmap : &kmap,
+                     x * (D / S::CH), row0 + ((at.j * TN + (g0 + grp) * 16) & ((1 << A.page_log2) - 1)), pg,
+                     &full[stage]);
+          skip = false;
+          if (++stage == A.n_stages) { stage = 0; phase ^= 1; }
         }
-        __syncwarp();
-        if (s_flags[0]) {
-          // a wait ran out, here or in a math warp, which then no longer waits: nothing more is copied, and what is on
-          // its way is waited for (boundedly) before the CTA ends. Earlier stages of this lap, later ones of the last.
-          int s = stage;
-          uint32_t ph = phase;
-          for (int i = 0; i < A.n_stages; ++i) {
-            if (s == 0) { s = A.n_stages; ph ^= 1; }
-            --s;
-            mbar_wait(&full[s], ph, A.timeout_ns);
-          }
-          return;
-        }
-        uint8_t* const dst = ring + stage * S::STAGE;
-        if (lane == 0) mbar_expect_tx(&full[stage], groups * S::GROUP_BYTES);
-        __syncwarp();
-        if (page >= 0 && !skip)
-          tma_rows(dst + grp * S::GROUP_BYTES + chunk * 16 * S::CB, kv ? &vmap : &kmap, chunk * (D / S::CH), row, page,
-                   &full[stage]);
-        skip = false;
-        if (++stage == A.n_stages) { stage = 0; phase ^= 1; }
+      }
+      if (ends) {
+        // gates are wanted where the whole item is this CTA's, at its end
+        if (a.gate.p && j_begin == 0 && !copy_rows(1, at)) return;
+        if (more && !copy_rows(0, nx)) return;
+        j_begin = 0;
       }
       at = nx;
       page = page_next;
@@ -331,15 +486,11 @@ __global__ void __launch_bounds__(THREADS, 2)
 
   // ------------------------------------------------------------------ products
   const int g = lane >> 2, t4 = lane & 3;
-  auto rows_at = [&](const moe_rows_t& r, int b, int h, int d) {
-    return (uint16_t*)r.p + b * r.row_stride + h * r.head_stride + d;
-  };
   // requests of length 0
   for (int b = blockIdx.x; b < A.B; b += gridDim.x)
     if (s_len[b] == 0)
-      for (int i = tid; i < A.Hq * D / 8; i += 32 * MATH_WARPS)
+      for (int i = tid; i < A.Hq * D / 8; i += S::MATH)
         *reinterpret_cast<uint4*>(rows_at(a.out, b, i / (D / 8), i % (D / 8) * 8)) = make_uint4(0, 0, 0, 0);
-  if (first >= last) return;
 
   // Where a lane's rows of a stage lie. 16-byte chunk c of row r of a group of 16 tokens is at
   //   c / PER * 16 * CB + r * CB + ((c % PER) ^ swizzle(r)) * 16,      PER = CB / 16,
@@ -353,44 +504,60 @@ __global__ void __launch_bounds__(THREADS, 2)
   const uint32_t k_lane = ring0 + in_group(lane & 15, lane >> 4);
   const uint32_t v_lane = ring0 + (S::E4M3 ? (lane >> 4) * S::GROUP_BYTES + in_group(lane & 15, warp * MD)
                                            : in_group((lane & 7) + ((lane >> 4) << 3), warp * MD * 2 + ((lane >> 3) & 1)));
-  auto wait_full = [&](int stage, uint32_t phase) {
+  const uint32_t p_lane = smem_u32(s_p) + ((lane & 7) * PP + (lane >> 3) * 8) * 2;
+  auto wait_full = [&](uint64_t* bar, uint32_t parity) {
     // once a wait has run out the outputs are lost: run to the end without waiting
-    if (!mbar_try_wait(&full[stage], phase) && !s_flags[0] && !mbar_wait(&full[stage], phase, A.timeout_ns)) {
+    if (!mbar_try_wait(bar, parity) && !s_flags[0] && !mbar_wait(bar, parity, A.timeout_ns)) {
       s_flags[0] = 1;
       atomicOr(A.status, CACHE_BAD_WAIT);
     }
     __syncwarp();
   };
+  auto release = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
 
-  Place at;
-  at.find(s_upto, A.B, heads, first);
   int stage = 0;
-  uint32_t phase = 0;
-  long long t = first;
+  uint32_t phase = 0, rows_phase[2] = {0, 0};
+  if (first >= last) return;
+  int t = first;
+  Place at = begin;
+  Split split[2] = {{-1, 0, 0, 0}, {-1, 0, 0, 0}};           // of the first item and of the last
   while (t < last) {
     const int kvh = at.h / A.head_tiles, h_in = (at.h % A.head_tiles) * NH;
     const int h0 = kvh * A.group + h_in;                       // first query head of the item
     const int nh = A.group - h_in < NH ? A.group - h_in : NH;
     const int len = s_len[at.b];
     const int j0 = at.j;
-    const int j1 = last - t < at.n - j0 ? j0 + (int)(last - t) : at.n;
+    const int j1 = last - t < at.n - j0 ? j0 + last - t : at.n;
 
-    // Q as B fragments; with an e4m3 cache the k index runs 4t..4t+3 within 16 bytes of a row, as the codes do
+    // Q as B fragments; with an e4m3 cache the k index runs 4t..4t+3 within 16 bytes of a row, as the codes do. Heads
+    // past nh hold whatever memory holds: no head's column reaches another's, and theirs are not written.
     uint32_t q[D / 16][NT][2];
     float sf[NT][2];                                           // what a product is multiplied by, for 2^x
+    wait_full(&rows_full[0], rows_phase[0]);
+    rows_phase[0] ^= 1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const bool in = nt * 8 + g < nh;
-      const uint16_t* src = rows_at(a.q, at.b, h0 + (in ? nt * 8 + g : 0), 0);
+      if (S::E4M3) {
+        const uint16_t* src = s_q + (nt * 8 + g) * QP + 4 * t4;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        if (S::E4M3) {
-          const uint2 v = *reinterpret_cast<const uint2*>(src + ks * 16 + 4 * t4);
-          q[ks][nt][0] = in ? v.x : 0;
-          q[ks][nt][1] = in ? v.y : 0;
-        } else {
-          q[ks][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4) : 0;
-          q[ks][nt][1] = in ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * t4 + 8) : 0;
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src + ks * 16);
+          q[ks][nt][0] = v.x;
+          q[ks][nt][1] = v.y;
+        }
+      } else {
+        const uint32_t src = smem_u32(s_q + (nt * 8 + (lane & 7)) * QP + (lane >> 3) * 8);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks += 2) {
+          uint32_t r[4];
+          ldsm4(r, src + ks * 32);
+          q[ks][nt][0] = r[0];
+          q[ks][nt][1] = r[1];
+          q[ks + 1][nt][0] = r[2];
+          q[ks + 1][nt][1] = r[3];
         }
       }
       float up = 1.f;
@@ -423,6 +590,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       for (int i = 0; i < 2; ++i)
         sf[nt][i] = A.scale * (S::E4M3 ? a.k_scale[kvh] * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + i) * 4) : 1.f);
     }
+    release(&rows_empty[0]);
 
     float o[MD][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -441,60 +609,66 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int j = j0; j < j1; ++j) {
       const int left = len - j * TN;                           // tokens of the request from this tile on
       const int groups = left >= TN ? KT : (left + 15) >> 4;
-      // ---- S^T = K Q^T for this warp's groups of 16 tokens
-      float s[MT][NT][4];
-      wait_full(stage, phase);
-      {
+      // ---- S^T = K Q^T for this warp's groups of 16 tokens; two chains of accumulators, as one would wait for each
+      // product's latency
+      float s[MT][NT][4], s2[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][nt][i] = s2[mt][nt][i] = 0.f;
+#pragma unroll 1
+      for (int g0 = 0; g0 < groups; g0 += GPS) {
+        // every warp waits for every stage: one that went ahead could release a stage twice before the others once
+        wait_full(&full[stage], phase);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const int gr = mt * MATH_WARPS + warp;
-          // two chains of accumulators: one would wait for each product's latency
-          float s2[NT][4];
+          const int gr = mt * WARPS + warp - g0;
+          if (gr < 0 || gr >= GPS || g0 + gr >= groups) continue;
+          const uint32_t from = k_lane + stage * S::STAGE + gr * S::GROUP_BYTES;
+          if (S::E4M3) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int c = 0; c < S::RB / 16; c += 2) {
+              uint32_t k[4];
+              ldsm4(k, (from ^ (c % PER << 4)) + c / PER * (16 * S::CB));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][nt][i] = s2[nt][i] = 0.f;
-          if (gr < groups) {
-            const uint32_t from = k_lane + stage * S::STAGE + gr * S::GROUP_BYTES;
-            if (S::E4M3) {
-#pragma unroll
-              for (int c = 0; c < S::RB / 16; c += 2) {
-                uint32_t k[4];
-                ldsm4(k, (from ^ (c % PER << 4)) + c / PER * (16 * S::CB));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  mma16816<false>(s[mt][nt], e4m3x2_to_f16x2((uint16_t)k[0]), e4m3x2_to_f16x2((uint16_t)k[1]),
-                                  e4m3x2_to_f16x2((uint16_t)(k[0] >> 16)), e4m3x2_to_f16x2((uint16_t)(k[1] >> 16)),
-                                  q[c][nt][0], q[c][nt][1]);
-                  mma16816<false>(s2[nt], e4m3x2_to_f16x2((uint16_t)k[2]), e4m3x2_to_f16x2((uint16_t)k[3]),
-                                  e4m3x2_to_f16x2((uint16_t)(k[2] >> 16)), e4m3x2_to_f16x2((uint16_t)(k[3] >> 16)),
-                                  q[c + 1][nt][0], q[c + 1][nt][1]);
-                }
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816<false>(s[mt][nt], e4m3x2_to_f16x2((uint16_t)k[0]), e4m3x2_to_f16x2((uint16_t)k[1]),
+                                e4m3x2_to_f16x2((uint16_t)(k[0] >> 16)), e4m3x2_to_f16x2((uint16_t)(k[1] >> 16)),
+                                q[c][nt][0], q[c][nt][1]);
+                mma16816<false>(s2[mt][nt], e4m3x2_to_f16x2((uint16_t)k[2]), e4m3x2_to_f16x2((uint16_t)k[3]),
+                                e4m3x2_to_f16x2((uint16_t)(k[2] >> 16)), e4m3x2_to_f16x2((uint16_t)(k[3] >> 16)),
+                                q[c + 1][nt][0], q[c + 1][nt][1]);
               }
-            } else {
+            }
+          } else {
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t k[4];
-                ldsm4(k, (from ^ (2 * ks % PER << 4)) + 2 * ks / PER * (16 * S::CB));
+            for (int ks = 0; ks < D / 16; ++ks) {
+              uint32_t k[4];
+              ldsm4(k, (from ^ (2 * ks % PER << 4)) + 2 * ks / PER * (16 * S::CB));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma16816<S::MMA_BF16>(ks & 1 ? s2[nt] : s[mt][nt], k[0], k[1], k[2], k[3], q[ks][nt][0], q[ks][nt][1]);
-              }
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<S::MMA_BF16>(ks & 1 ? s2[mt][nt] : s[mt][nt], k[0], k[1], k[2], k[3], q[ks][nt][0],
+                                      q[ks][nt][1]);
             }
           }
-          const bool edge = left < (gr + 1) * 16;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x = (s[mt][nt][i] + s2[nt][i]) * sf[nt][i & 1];
-              s[mt][nt][i] = edge && gr * 16 + g + (i >> 1) * 8 >= left ? -INFINITY : x;
-            }
         }
+        release(&empty[stage]);
+        if (++stage == A.n_stages) { stage = 0; phase ^= 1; }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == A.n_stages) { stage = 0; phase ^= 1; }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int tok = (mt * WARPS + warp) * 16;
+        const bool edge = left < tok + 16;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = (s[mt][nt][i] + s2[mt][nt][i]) * sf[nt][i & 1];
+            s[mt][nt][i] = edge && tok + g + (i >> 1) * 8 >= left ? -INFINITY : x;
+          }
+      }
 
       // ---- the tile's maximum for each head
       float top[NT][2];
@@ -513,14 +687,14 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           *reinterpret_cast<float2*>(&s_max[warp * NH + nt * 8 + 2 * t4]) = make_float2(top[nt][0], top[nt][1]);
-      math_barrier();
+      math_barrier<S>();
       bool moved = false;
       float c[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float2 x = make_float2(m[nt][0], m[nt][1]);
 #pragma unroll
-        for (int w = 0; w < MATH_WARPS; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
           const float2 y = *reinterpret_cast<const float2*>(&s_max[w * NH + nt * 8 + 2 * t4]);
           x.x = fmaxf(x.x, y.x);
           x.y = fmaxf(x.y, y.y);
@@ -549,7 +723,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<uint32_t*>(&s_p[(nt * 8 + g) * PP + (mt * MATH_WARPS + warp) * 16 + 8 * r + 2 * t4]) =
+            *reinterpret_cast<uint32_t*>(&s_p[(nt * 8 + g) * PP + (mt * WARPS + warp) * 16 + 8 * r + 2 * t4]) =
                 transpose8x8(pack2<S::MMA_BF16>(s[mt][nt][2 * r], s[mt][nt][2 * r + 1]));
       }
       if (__any_sync(0xFFFFFFFFu, moved)) {
@@ -560,19 +734,18 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[md][nt][i] *= c[nt][i & 1];
       }
-      math_barrier();
+      math_barrier<S>();
 
-      // ---- O^T += V^T P^T for this warp's quarter of d
-      wait_full(stage, phase);
-      {
+      // ---- O^T += V^T P^T for this warp's rows of d
+#pragma unroll 1
+      for (int g0 = 0; g0 < groups; g0 += GPS) {
+        wait_full(&full[stage], phase);
         const uint32_t from = v_lane + stage * S::STAGE;
-        const uint32_t pbase = smem_u32(s_p) + ((lane & 7) * PP + (lane >> 3) * 8) * 2;
-        if (left >= TN) add_values<S, false>(o, from, pbase, KT, TN, t4);
-        else add_values<S, true>(o, from, pbase, groups, left, t4);
+        if (left >= (g0 + GPS) * 16) add_values<S, false>(o, from, p_lane, g0, left, t4);
+        else add_values<S, true>(o, from, p_lane, g0, left, t4);
+        release(&empty[stage]);
+        if (++stage == A.n_stages) { stage = 0; phase ^= 1; }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == A.n_stages) { stage = 0; phase ^= 1; }
     }
 
     // ---- the end of the item, or of the CTA's share of it
@@ -586,14 +759,14 @@ __global__ void __launch_bounds__(THREADS, 2)
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
         if (lane < 4) s_sum[warp * NH + nt * 8 + 2 * t4 + i] = x;
       }
-    math_barrier();
+    math_barrier<S>();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < MATH_WARPS; ++w) x += s_sum[w * NH + nt * 8 + 2 * t4 + i];
+        for (int w = 0; w < WARPS; ++w) x += s_sum[w * NH + nt * 8 + 2 * t4 + i];
         l[nt][i] = x;
       }
     const float vs = S::E4M3 ? a.v_scale[kvh] : 1.f;
@@ -602,6 +775,10 @@ __global__ void __launch_bounds__(THREADS, 2)
       return S::E4M3 ? (warp * MD + md) * 16 + 2 * g + r : (warp * MD + md) * 16 + g + 8 * r;
     };
     if (j0 == 0 && j1 == at.n) {
+      if (a.gate.p) {
+        wait_full(&rows_full[1], rows_phase[1]);
+        rows_phase[1] ^= 1;
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -616,18 +793,19 @@ __global__ void __launch_bounds__(THREADS, 2)
               float y = o[md][nt][2 * r + i] * f;
               const int d = d_of(md, r);
               if (a.gate.p) {
-                const float x = unpack2<S::BF16>(*rows_at(a.gate, at.b, h0 + h, d)).x;
-                y = y / (1.f + __expf(-x));
+                y = gated(y, unpack2<S::BF16>(s_q[(NH + h) * QP + d]).x);
               }
               *rows_at(a.out, at.b, h0 + h, d) = (uint16_t)pack2<S::BF16>(y, 0.f);
             }
         }
+      if (a.gate.p) release(&rows_empty[1]);
     } else {
-      // a part: the item's tiles are those of CTAs c0 .. c1; c0 holds its part as the item it left, the others as the
-      // item they began in the middle of
-      const long long t0 = t - j0;
-      const int c0 = (int)(t0 / dv.chunk), c1 = (int)((t0 + at.n - 1) / dv.chunk);
-      float* part = A.parts + ((long long)blockIdx.x * 2 + (j0 == 0 ? 1 : 0)) * S::PART;
+      // a part, joined with the others once this CTA has nothing else to do: the item's tiles are those of CTAs c0 .. c1;
+      // c0 holds its part as the item it leaves, the others as the item they begin in the middle of
+      const int which = j0 == 0 ? 1 : 0;
+      const Split sp = {at.b, at.h, (t - j0) / share, (t - j0 + at.n - 1) / share};
+      if (which) split[1] = sp; else split[0] = sp;
+      float* part = A.parts + ((long long)blockIdx.x * 2 + which) * S::PART;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -642,81 +820,83 @@ __global__ void __launch_bounds__(THREADS, 2)
             part[NH * D + NH + h] = l[nt][i];
           }
         }
-      __threadfence();
-      math_barrier();
-      if (tid == 0) s_flags[1] = atomicAdd(&A.counts[c0], 1u) == (uint32_t)(c1 - c0);
-      math_barrier();
-      if (s_flags[1]) {
-        __threadfence();
-        if (tid == 0) A.counts[c0] = 0;
-        const int n = c1 - c0 + 1;
-        auto nth = [&](int i) { return A.parts + ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * S::PART; };
-        // the largest maximum of each head
-        {
-          const int h = tid % NH;
-          float x = -INFINITY;
-          for (int i = tid / NH; i < n; i += 32 * MATH_WARPS / NH) x = fmaxf(x, __ldcg(nth(i) + NH * D + h));
-#pragma unroll
-          for (int w = NH; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
-          if (lane < NH) s_max[warp * NH + lane] = x;
-          math_barrier();
-          x = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < MATH_WARPS; ++w) x = fmaxf(x, s_max[w * NH + h]);
-          if (tid < NH) s_top[h] = x == -INFINITY ? 0.f : x;
-          math_barrier();
-        }
-        constexpr int PER = NH * D / 4 / (32 * MATH_WARPS);     // groups of four d per thread
-        float4 y[PER];
-        float sum[PER];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          sum[e] = 0.f;
-        }
-        for (int i0 = 0; i0 < n; i0 += S::JOIN) {
-          const int ni = n - i0 < S::JOIN ? n - i0 : S::JOIN;
-          for (int i = tid; i < ni * NH; i += 32 * MATH_WARPS)
-            s_w[i] = exp2_fast(__ldcg(nth(i0 + i / NH) + NH * D + i % NH) - s_top[i % NH]);
-          math_barrier();
-#pragma unroll 4
-          for (int i = 0; i < ni; ++i) {
-            const float* p = nth(i0 + i);
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-              const int at4 = (e * 32 * MATH_WARPS + tid) * 4, h = at4 / D;
-              const float w = s_w[i * NH + h];
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(p + at4));
-              y[e].x = fmaf(v.x, w, y[e].x);
-              y[e].y = fmaf(v.y, w, y[e].y);
-              y[e].z = fmaf(v.z, w, y[e].z);
-              y[e].w = fmaf(v.w, w, y[e].w);
-              sum[e] = fmaf(__ldcg(p + NH * D + NH + h), w, sum[e]);
-            }
-          }
-          math_barrier();
-        }
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          const int at4 = (e * 32 * MATH_WARPS + tid) * 4, h = at4 / D, d = at4 % D;
-          if (h >= nh) continue;
-          const float f = vs / sum[e];
-          float x[4] = {y[e].x * f, y[e].y * f, y[e].z * f, y[e].w * f};
-          if (a.gate.p) {
-            const uint2 gr = *reinterpret_cast<const uint2*>(rows_at(a.gate, at.b, h0 + h, d));
-            const float2 g0 = unpack2<S::BF16>(gr.x), g1 = unpack2<S::BF16>(gr.y);
-            x[0] /= 1.f + __expf(-g0.x);
-            x[1] /= 1.f + __expf(-g0.y);
-            x[2] /= 1.f + __expf(-g1.x);
-            x[3] /= 1.f + __expf(-g1.y);
-          }
-          *reinterpret_cast<uint2*>(rows_at(a.out, at.b, h0 + h, d)) =
-              make_uint2(pack2<S::BF16>(x[0], x[1]), pack2<S::BF16>(x[2], x[3]));
-        }
-      }
     }
     t += j1 - j0;
-    if (t < last) at.next_item(s_upto, heads);
+    if (t < last) at.template next_item<S>(s_len, heads);
+  }
+
+  // ---- joining the split items: the last of an item's parts to arrive joins them
+  if (split[0].b < 0 && split[1].b < 0) return;
+  __threadfence();
+  math_barrier<S>();
+  const int gi = blockIdx.x / GROUP;
+  if (lane == 0 && warp < 2) {
+    const Split sp = warp ? split[1] : split[0];
+    bool all = false;
+    if (sp.b >= 0) {
+      const bool flat = sp.c1 - sp.c0 < FLAT;
+      uint32_t* const count = flat ? &A.counts[sp.c0] : &A.group_counts[2 * gi + (gi == sp.c0 / GROUP)];
+      const int from = flat || sp.c0 > gi * GROUP ? sp.c0 : gi * GROUP;
+      const int to = flat || sp.c1 < gi * GROUP + GROUP ? sp.c1 : gi * GROUP + GROUP - 1;
+      all = atomicAdd(count, 1u) == (uint32_t)(to - from);
+      if (all) *count = 0;
+    }
+    s_flags[1 + warp] = all;
+  }
+  math_barrier<S>();
+  Joined<S> y;
+  uint32_t join_phase = 0;
+  const int fit = A.n_stages * S::STAGE / (S::PART * 4);
+  const int at_once = fit < PP / 4 - 1 ? fit : PP / 4 - 1;      // the weights lie where P did
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (!s_flags[1 + i]) continue;
+    __threadfence();
+    const Split sp = i ? split[1] : split[0];
+    const int kvh = sp.h / A.head_tiles, h_in = (sp.h % A.head_tiles) * NH;
+    const int nh = A.group - h_in < NH ? A.group - h_in : NH;
+    const float vs = S::E4M3 ? a.v_scale[kvh] : 1.f;
+    auto join = [&](const float* parts, int ia, int ib, int i0) {
+      y.clear();
+      for (int k0 = ia; k0 <= ib; k0 += at_once) {
+        const int n = ib - k0 + 1 < at_once ? ib - k0 + 1 : at_once;
+        math_barrier<S>();                       // what the ring held has been read
+        if (tid == 0) {
+          fence_proxy_async_global();
+          mbar_expect_tx(join_full, n * S::PART * 4);
+          for (int k = 0; k < n; ++k)
+            bulk_g2s(ring + k * S::PART * 4, parts + ((long long)(k0 + k) * 2 + (k0 + k == i0 ? 1 : 0)) * S::PART,
+                     S::PART * 4, join_full);
+        }
+        wait_full(join_full, join_phase);
+        if (s_flags[0]) mbar_wait(join_full, join_phase, A.timeout_ns);   // lost; the copies must not outlive the CTA
+        join_phase ^= 1;
+        y.add((const float*)ring, n, s_max, reinterpret_cast<float2*>(s_p), tid);
+      }
+    };
+    const int h0 = kvh * A.group + h_in;
+    if (sp.c1 - sp.c0 < FLAT) {
+      y.fetch_gates(A, sp.b, h0, nh, tid);
+      join(A.parts, sp.c0, sp.c1, sp.c0);
+    } else {
+      // many parts: each GROUP of CTAs joins its own, and the last group to do so the groups'
+      const int g0 = sp.c0 / GROUP, g1 = sp.c1 / GROUP;
+      join(A.parts, gi == g0 ? sp.c0 : gi * GROUP, gi == g1 ? sp.c1 : gi * GROUP + GROUP - 1, sp.c0);
+      y.keep(A.group_parts + ((long long)gi * 2 + (gi == g0)) * S::PART, tid);
+      __threadfence();
+      math_barrier<S>();
+      if (tid == 0) {
+        const bool all = atomicAdd(&A.counts[sp.c0], 1u) == (uint32_t)(g1 - g0);
+        if (all) A.counts[sp.c0] = 0;
+        s_flags[1 + i] = all;
+      }
+      math_barrier<S>();
+      if (!s_flags[1 + i]) continue;
+      __threadfence();
+      y.fetch_gates(A, sp.b, h0, nh, tid);
+      join(A.group_parts, g0, g1, g0);
+    }
+    y.finish(A, sp.b, h0, nh, vs, tid);
   }
 }
 
@@ -759,13 +939,13 @@ constexpr int SMEM_PER_CTA = 113 * 1024;      // two CTAs to an SM's 228 KB, of 
 
 template <class S>
 cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
-  static_assert(S::MISC + 1024 + CACHE_MAX_REQUESTS * 8 + 2 * S::STAGE <= SMEM_PER_CTA, "the ring needs two stages");
+  static_assert(S::MISC + 1024 + CACHE_MAX_REQUESTS * 4 + 2 * S::STAGE <= SMEM_PER_CTA, "the ring has two stages at least");
   CUtensorMap km, vm;
   cudaError_t e = pool_map<S>(c, A.a.k_cache, A.a.k_page_stride, &km);
   if (e == cudaSuccess) e = pool_map<S>(c, A.a.v_cache, A.a.v_page_stride, &vm);
   if (e != cudaSuccess) return e;
   A.head_tiles = (A.group + S::NH - 1) / S::NH;
-  const int other = S::MISC + 1024 + A.B * 8;
+  const int other = S::MISC + 1024 + A.B * 4;
   const int n = (SMEM_PER_CTA - other) / S::STAGE;
   A.n_stages = n > 32 ? 32 : n;
   static bool ready[64] = {};
@@ -776,7 +956,7 @@ cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
     if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev] = true;
   }
   if (e != cudaSuccess) return e;
-  k_cache_attend<S><<<ctas, THREADS, other + A.n_stages * S::STAGE, st>>>(A, km, vm);
+  k_cache_attend<S><<<ctas, S::THREADS, other + A.n_stages * S::STAGE, st>>>(A, km, vm);
   return cudaGetLastError();
 }
 
@@ -792,7 +972,11 @@ cudaError_t run_types(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t
 
 }  // namespace
 
-size_t cache_attend_workspace(int num_sms) { return ((size_t)2 * num_sms * 2 * (16 * 256 + 32) + COUNT_WORDS) * 4; }
+size_t cache_attend_workspace(int num_sms) {
+  const size_t ctas = 2 * (size_t)num_sms < MAX_CTAS ? 2 * (size_t)num_sms : MAX_CTAS;
+  const size_t groups = (ctas + GROUP - 1) / GROUP;
+  return ((ctas + groups) * 2 * PART_MAX + COUNT_WORDS) * 4;
+}
 
 cudaError_t cache_attend_launch(const CacheShape& S, const moe_cache_attend_t& a, const CacheAttendState& w,
                                 cudaStream_t st) {
@@ -806,9 +990,11 @@ cudaError_t cache_attend_launch(const CacheShape& S, const moe_cache_attend_t& a
   A.n_pages = S.n_pages;
   A.max_len = (long long)S.max_pages << S.page_log2;
   A.scale = (float)a.scale * LOG2E;
-  const int ctas = 2 * w.num_sms;
+  const int ctas = 2 * w.num_sms < MAX_CTAS ? 2 * w.num_sms : MAX_CTAS;
   A.counts = (uint32_t*)w.workspace;
+  A.group_counts = A.counts + MAX_CTAS;
   A.parts = (float*)w.workspace + COUNT_WORDS;
+  A.group_parts = A.parts + (size_t)ctas * 2 * PART_MAX;
   A.status = w.status;
   A.timeout_ns = w.timeout_ns;
   A.skip_copy = w.skip_copy;
