@@ -22,7 +22,7 @@ namespace moe {
 namespace {
 
 constexpr int GROUP = 10, FLAT = 20;              // CTAs whose parts are joined first; from FLAT + 1 parts on
-constexpr int MAX_CTAS = 2048, COUNT_WORDS = MAX_CTAS + MAX_CTAS / GROUP * 2;    // of the workspace
+constexpr int MAX_CTAS = 1024, COUNT_WORDS = MAX_CTAS + MAX_CTAS / GROUP * 2;    // of the workspace
 constexpr int PART_MAX = 16 * 256 + 32;           // floats of the largest part
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -45,8 +45,8 @@ struct Shape {
   static constexpr int D = D_, NT = NT_, NH = 8 * NT_;      // query heads of an item
   static constexpr bool BF16 = BF16_, E4M3 = E4M3_;
   static constexpr bool MMA_BF16 = BF16_ && !E4M3_;         // e4m3 is exact in fp16
-  static constexpr int WARPS = 4;                           // of the products
-  static constexpr int MATH = 32 * WARPS, THREADS = MATH + 32;
+  static constexpr int WARPS = 4, TEAMS = 2;                // math warps: the teams take the tiles in turn
+  static constexpr int MATH = 32 * WARPS, THREADS = TEAMS * (MATH + 32);   // and a warp to copy for each team
   static constexpr int RB = D * (E4M3 ? 1 : 2);             // bytes of a token's row
   static constexpr int CB = RB < 128 ? RB : 128, CH = RB / CB;
   static constexpr int TN = RB >= 512 ? 64 : 128;           // tokens of a tile
@@ -55,10 +55,13 @@ struct Shape {
   static constexpr int GPS = 16384 / (16 * RB) < KT ? 16384 / (16 * RB) : KT;   // 16-token groups of a stage
   static constexpr int GROUP_BYTES = 16 * RB, STAGE = GPS * GROUP_BYTES;
   static constexpr int MD = D / 16 / WARPS;                 // 16-row tiles of O per warp
+  static constexpr int EXTRA = 65536 / (2 * TN * RB) > 1 ? 65536 / (2 * TN * RB) : 1;   // units of an item, see there
   static constexpr int PP = TN + 8;                         // pitch of P: rows of 8 fall on different banks
   static constexpr int QP = D + 8;                          // pitch of queries and gates
   static constexpr int PART = NH * D + 2 * NH;              // floats of a partial result: O, maxima, sums
-  static constexpr int MISC = 1024 /* barriers */ + 2 * NH * QP * 2 + NH * PP * 2 + 2 * WARPS * NH * 4;
+  // of shared memory besides the rings and the lengths: barriers; queries and gates, twice; for each team P, maxima and sums;
+  // one's results on their way to the other
+  static constexpr int MISC = 1024 + 4 * NH * QP * 2 + TEAMS * (NH * PP * 2 + 2 * WARPS * NH * 4) + NH * D * 4 + (1 + WARPS) * NH * 4;
 };
 
 // ---- instructions ----
@@ -109,18 +112,23 @@ __device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* m, int x,
 __device__ __forceinline__ uint16_t* rows_at(const moe_rows_t& r, int b, int h, int d) {
   return (uint16_t*)r.p + b * r.row_stride + h * r.head_stride + d;
 }
+// named barriers: 1 and 2 of a team each, 3 and 4 of both
 template <class S>
-__device__ __forceinline__ void math_barrier() { named_bar(1, S::MATH); }
-// ---- the division of the work ----
-// Tiles are numbered request by request, within a request head by head; CTA c takes tiles c * share .. (c + 1) * share - 1.
-__host__ __device__ inline int even_share(int tiles, int ctas) {
-  return tiles > 0 ? (int)(((long long)tiles + ctas - 1) / ctas) : 1;
+__device__ __forceinline__ void team_barrier(int team) { named_bar(1 + team, S::MATH); }
+__device__ __forceinline__ void named_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// ---- the division of the work ----
+// Items come request by request, within a request head by head. An item of n tiles is n + EXTRA units long, for what its
+// beginning and end cost; CTA c takes units c * share .. (c + 1) * share - 1.
+__host__ __device__ inline int even_share(int units, int ctas) {
+  return units > 0 ? (int)(((long long)units + ctas - 1) / ctas) : 1;
+}
 template <class S>
 __device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + S::TN - 1) / S::TN); }
 
-// A place in the list of tiles: tile j of request b's head h (h: key-value head and its tile of query heads).
+// A place among the units: tile j of request b's head h (h: key-value head and its tile of query heads).
 struct Place {
   int b, h, j, n;      // n: tiles of each head of request b
   // to the first tile of the next item (which exists)
@@ -200,9 +208,34 @@ struct Split {
   int b, h, c0, c1;
 };
 
+// The parts of a split item, or of a group of CTAs where they are many, that have arrived when this CTA's does: their count
+// is in arrive's word, complete when the last one is there (and then set back).
+__device__ __forceinline__ uint32_t* count_of(const AttendArgs& A, const Split& sp, int* n) {
+  const int gi = blockIdx.x / GROUP;
+  if (sp.c1 - sp.c0 < FLAT) {
+    *n = sp.c1 - sp.c0 + 1;
+    return &A.counts[sp.c0];
+  }
+  const int from = sp.c0 > gi * GROUP ? sp.c0 : gi * GROUP, to = sp.c1 < gi * GROUP + GROUP ? sp.c1 : gi * GROUP + GROUP - 1;
+  *n = to - from + 1;
+  return &A.group_counts[2 * gi + (gi == sp.c0 / GROUP)];
+}
+__device__ __forceinline__ int arrive(const AttendArgs& A, const Split& sp) {
+  int n;
+  return (int)atomicAdd(count_of(A, sp, &n), 1u);
+}
+__device__ __forceinline__ bool complete(const AttendArgs& A, const Split& sp, int before) {
+  int n;
+  uint32_t* const count = count_of(A, sp, &n);
+  if (before != n - 1) return false;
+  *count = 0;
+  return true;
+}
+
 // The joined parts of a split item: NH * D / 4 groups of four d, PER of them to a thread.
 template <class S>
 struct Joined {
+  static constexpr int FEW = S::NT == 1 ? 4 : 2;
   static constexpr int NH = S::NH, D = S::D, VECS = NH * D / 4, PER = (VECS + S::MATH - 1) / S::MATH;
   static_assert(VECS % S::MATH == 0, "whole vectors for each thread");
   float4 y[PER];
@@ -219,7 +252,43 @@ struct Joined {
       sum[e] = 0.f;
     }
   }
-  // n further parts, from shared memory; the order of the sum is that of the parts. All math warps, in step.
+  // up to FEW parts, straight from L2 with every load on its way at once
+  __device__ __forceinline__ void few(const float* parts, int ia, int ib, int i0, int tid) {
+    float4 v[FEW][PER];
+    float m[FEW][PER], l[FEW][PER];
+#pragma unroll
+    for (int k = 0; k < FEW; ++k) {
+      const int i = ia + k < ib ? ia + k : ib;
+      const float* p = parts + ((long long)i * 2 + (i == i0 ? 1 : 0)) * S::PART;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const int at4 = (e * S::MATH + tid) * 4, he = at4 / D;
+        v[k][e] = __ldcg(reinterpret_cast<const float4*>(p + at4));
+        m[k][e] = __ldcg(p + NH * D + he);
+        l[k][e] = __ldcg(p + NH * D + NH + he);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      float x = m[0][e];
+#pragma unroll
+      for (int k = 1; k < FEW; ++k) x = fmaxf(x, m[k][e]);
+      const float base = x == -INFINITY ? 0.f : x;
+      y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      sum[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < FEW; ++k) {
+        if (ia + k > ib) break;
+        const float w = exp2_fast(m[k][e] - base);
+        sum[e] = fmaf(l[k][e], w, sum[e]);
+        y[e].x = fmaf(v[k][e].x, w, y[e].x);
+        y[e].y = fmaf(v[k][e].y, w, y[e].y);
+        y[e].z = fmaf(v[k][e].z, w, y[e].z);
+        y[e].w = fmaf(v[k][e].w, w, y[e].w);
+      }
+    }
+  }
+  // n further parts, from shared memory; the order of the sum is that of the parts. The first team, in step.
   // s_max: [WARPS][NH], s_w: [n][NH] weights beside weighted sums, and [NH] factors of what is there already
   __device__ __forceinline__ void add(const float* parts, int n, float* s_max, float2* s_w, int tid) {
     const int h = tid % NH, lane = tid & 31, warp = tid >> 5;
@@ -228,7 +297,7 @@ struct Joined {
 #pragma unroll
     for (int w = NH; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
     if (lane < NH) s_max[warp * NH + h] = x;
-    math_barrier<S>();
+    team_barrier<S>(0);
 #pragma unroll
     for (int w = 0; w < S::WARPS; ++w) x = fmaxf(x, s_max[w * NH + h]);
     const float base = x == -INFINITY ? 0.f : x;
@@ -238,7 +307,7 @@ struct Joined {
     }
     if (tid < NH) s_w[n * NH + h].x = exp2_fast(top - base);
     top = x;
-    math_barrier<S>();
+    team_barrier<S>(0);
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
       const int at4 = (e * S::MATH + tid) * 4, he = at4 / D;
@@ -301,44 +370,45 @@ struct Joined {
 };
 
 template <class S>
-__global__ void __launch_bounds__(S::THREADS, 2)
+__global__ void __launch_bounds__(S::THREADS, 1)
     k_cache_attend(const __grid_constant__ AttendArgs A, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
   constexpr int D = S::D, NT = S::NT, NH = S::NH, TN = S::TN, MT = S::MT, KT = S::KT, MD = S::MD, PP = S::PP, QP = S::QP;
-  constexpr int GPS = S::GPS, WARPS = S::WARPS;
+  constexpr int GPS = S::GPS, WARPS = S::WARPS, TEAMS = S::TEAMS, MATH = S::MATH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* const misc = ring + A.n_stages * S::STAGE;
-  uint64_t* const full = (uint64_t*)misc;            // [n_stages <= 32]
-  uint64_t* const empty = full + 32;
-  uint64_t* const rows_full = empty + 32;            // 0: queries, 1: gates
+  uint8_t* const misc = ring + TEAMS * A.n_stages * S::STAGE;
+  uint64_t* const full0 = (uint64_t*)misc;           // [TEAMS][n_stages <= 16]: every team has a ring of its own
+  uint64_t* const empty0 = full0 + 32;
+  uint64_t* const rows_full = empty0 + 32;            // [2]: an item's queries and gates, by turns
   uint64_t* const rows_empty = rows_full + 2;
   uint64_t* const join_full = rows_empty + 2;        // parts, when the ring is done with
-  volatile int* const s_flags = (int*)(join_full + 1);    // 0: a wait ran out; 1, 2: last to arrive
+  volatile int* const s_flags = (int*)(join_full + 1);    // 0: a wait ran out; 1, 2: last to arrive; 3: the first has
   int* const s_scan = (int*)(join_full + 1) + 4;     // [THREADS / 32]
   int* const s_place = s_scan + 16;                  // [3]
-  uint16_t* const s_q = (uint16_t*)(misc + 1024);    // [2][NH][QP]: queries, gates
-  uint16_t* const s_p = s_q + 2 * NH * QP;           // [NH][PP]
-  float* const s_max = (float*)(s_p + NH * PP);      // [WARPS][NH]
-  float* const s_sum = s_max + WARPS * NH;           // [WARPS][NH]
-  int* const s_len = (int*)(s_sum + WARPS * NH);     // [B]
+  uint16_t* const s_q = (uint16_t*)(misc + 1024);    // [2][2][NH][QP]: by turns, queries and gates
+  uint16_t* const s_p0 = s_q + 4 * NH * QP;          // [TEAMS][NH][PP]
+  float* const s_max0 = (float*)(s_p0 + TEAMS * NH * PP);   // [TEAMS][WARPS][NH]
+  float* const s_sum0 = s_max0 + TEAMS * WARPS * NH; // [TEAMS][WARPS][NH]
+  float* const s_x = s_sum0 + TEAMS * WARPS * NH;    // [NH * D], [NH] maxima, [WARPS][NH] sums
+  int* const s_len = (int*)(s_x + NH * D + NH + WARPS * NH);   // [B]
 
   const moe_cache_attend_t& a = A.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = A.Hkv * A.head_tiles;
 
   if (tid == 0) {
-    for (int s = 0; s < A.n_stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], WARPS);
+    for (int s = 0; s < TEAMS * 16; ++s) {
+      mbar_init(&full0[s], 1);
+      mbar_init(&empty0[s], WARPS);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&rows_full[s], 1);
-      mbar_init(&rows_empty[s], WARPS);
+      mbar_init(&rows_empty[s], TEAMS * WARPS);
     }
     mbar_init(join_full, 1);
     fence_mbar_init();
-    s_flags[0] = 0;
+    s_flags[0] = s_flags[1] = s_flags[2] = s_flags[3] = 0;
   }
   // lengths and the running number of tiles: a thread's requests lie side by side, so that all its loads are on their way
   // at once
@@ -353,7 +423,7 @@ __global__ void __launch_bounds__(S::THREADS, 2)
       len = len < 0 ? 0 : (int)A.max_len;
     }
     s_len[b] = len;
-    mine += tiles_of<S>(len);
+    mine += len ? tiles_of<S>(len) + S::EXTRA : 0;
   }
   // a wait ran out in an earlier call, or has in this one: the counts are off until the status is read
   const bool dead = tid == 0 && (*(volatile uint32_t*)A.status & CACHE_BAD_WAIT);
@@ -370,15 +440,17 @@ __global__ void __launch_bounds__(S::THREADS, 2)
     if (w < warp) upto += s_scan[w];
     carry += s_scan[w];
   }
-  const int tiles = carry * heads, share = even_share(tiles, gridDim.x);
-  const int first = (long long)share * blockIdx.x < tiles ? share * blockIdx.x : tiles;
-  const int last = share < tiles - first ? first + share : tiles;
+  const int units = carry * heads, share = even_share(units, gridDim.x);
+  const int first = (long long)share * blockIdx.x < units ? share * blockIdx.x : units;
+  const int last = share < units - first ? first + share : units;
   // where the CTA begins: found by the thread that holds the request
   if (first < last && (upto - mine) * heads <= first && first < upto * heads) {
-    int before = upto - mine, b = b_begin, n = tiles_of<S>(s_len[b]);
-    while ((before + n) * heads <= first) {
+    int before = upto - mine, b = b_begin - 1, n;
+    while (true) {
+      const int len = s_len[++b];
+      n = len ? tiles_of<S>(len) + S::EXTRA : 0;
+      if ((before + n) * heads > first) break;
       before += n;
-      n = tiles_of<S>(s_len[++b]);
     }
     const int in = first - before * heads;
     s_place[0] = b;
@@ -386,16 +458,29 @@ __global__ void __launch_bounds__(S::THREADS, 2)
     s_place[2] = in % n;
   }
   __syncthreads();
-  const Place begin = {s_place[0], s_place[1], s_place[2], first < last ? tiles_of<S>(s_len[s_place[0]]) : 0};
+  // begin: the first tile from unit `first` on, which is unit t0
+  Place begin = {0, 0, 0, 0};
+  int t0 = first;
+  if (first < last) {
+    begin = {s_place[0], s_place[1], s_place[2], tiles_of<S>(s_len[s_place[0]])};
+    if (begin.j >= begin.n) {
+      t0 += begin.n + S::EXTRA - begin.j;
+      if (t0 < last) begin.template next_item<S>(s_len, heads);
+    }
+  }
 
-  if (warp == WARPS) {
-    // ---------------------------------------------------------------- copies
+  if (warp >= TEAMS * WARPS) {
+    // ---------------------------------------------------------------- copies, for one team
+    const int team = warp - TEAMS * WARPS;
+    uint64_t* const full = full0 + team * 16;
+    uint64_t* const empty = empty0 + team * 16;
+    uint8_t* const my_ring = ring + team * A.n_stages * S::STAGE;
     int stage = 0;
-    uint32_t phase = 0, n_rows[2] = {0, 0};          // copies of queries and of gates so far
-    bool skip = A.skip_copy && blockIdx.x == 0;
+    uint32_t phase = 0, n_rows = 0;                  // n_rows: copies of rows so far, by the first team's warp
+    bool skip = A.skip_copy && blockIdx.x == 0 && team == 0;
     // Waits until a buffer is free. False: a wait ran out, here or in a math warp, which then no longer waits. Nothing
-    // more is copied then, and what is on its way is waited for (boundedly) before the CTA ends: earlier stages of this
-    // lap, later ones of the last, the rows.
+    // more is copied then, and what is on its way is waited for (boundedly) before the CTA ends: the ring's stages,
+    // earlier ones of this lap, later ones of the last, and the rows.
     auto free_to_fill = [&](uint64_t* bar, uint32_t parity) {
       if (!mbar_wait(bar, parity, A.timeout_ns)) {
         s_flags[0] = 1;
@@ -403,93 +488,102 @@ __global__ void __launch_bounds__(S::THREADS, 2)
       }
       __syncwarp();
       if (!s_flags[0]) return true;
-      int s = stage;
-      uint32_t ph = phase;
-      for (int i = 0; i < A.n_stages; ++i) {
-        if (s == 0) { s = A.n_stages; ph ^= 1; }
-        --s;
-        mbar_wait(&full[s], ph, A.timeout_ns);
-      }
-      for (int i = 0; i < 2; ++i)
-        if (n_rows[i]) mbar_wait(&rows_full[i], (n_rows[i] - 1) & 1, A.timeout_ns);
+      for (int s = 0; s < A.n_stages; ++s) mbar_wait(&full[s], s < stage ? phase : phase ^ 1, A.timeout_ns);
+      for (uint32_t i = n_rows > 2 ? n_rows - 2 : 0; i < n_rows; ++i) mbar_wait(&rows_full[i & 1], i >> 1 & 1, A.timeout_ns);
       return false;
     };
-    // the item's rows of queries (0) or gates (1), a head's D elements each
-    auto copy_rows = [&](int which, const Place& p) {
-      const uint32_t n = n_rows[which];
-      if (!free_to_fill(&rows_empty[which], (n & 1) ^ 1)) return false;
+    // the item's queries, and its gates where the whole item is this CTA's: rows of D elements
+    auto copy_rows = [&](const Place& p, bool gates) {
+      const uint32_t buf = n_rows & 1;
+      if (!free_to_fill(&rows_empty[buf], (n_rows >> 1 & 1) ^ 1)) return false;
       const int h_in = (p.h % A.head_tiles) * NH;
       const int h0 = (p.h / A.head_tiles) * A.group + h_in;
       const int nh = A.group - h_in < NH ? A.group - h_in : NH;
-      if (lane == 0) mbar_expect_tx(&rows_full[which], nh * D * 2);
+      if (lane == 0) mbar_expect_tx(&rows_full[buf], nh * D * 2 * (gates ? 2 : 1));
       __syncwarp();
-      if (lane < nh)
-        bulk_g2s(s_q + (which * NH + lane) * QP, rows_at(which ? a.gate : a.q, p.b, h0 + lane, 0), D * 2,
-                 &rows_full[which]);
-      n_rows[which] = n + 1;
+      const int which = lane / NH, h = lane % NH;
+      if (h < nh && (which == 0 || (which == 1 && gates)))
+        bulk_g2s(s_q + ((buf * 2 + which) * NH + h) * QP, rows_at(which ? a.gate : a.q, p.b, h0 + h, 0), D * 2,
+                 &rows_full[buf]);
+      ++n_rows;
       return true;
     };
-    // the page of group `lane` of a tile, one tile ahead of its copies
-    auto page_of = [&](const Place& p) {
+    // the pages of 32 groups of 16 tokens from a tile on, one to a lane; looked at only when they are used, which is while
+    // the next 32 are on their way
+    auto pages_from = [&](const Place& p) {
       const long long tok = (long long)p.j * TN + lane * 16;
-      if (lane >= KT || tok >= s_len[p.b]) return -1;
-      int page = __ldcg(a.tables + (long long)p.b * a.table_stride + (tok >> A.page_log2));
-      if (page < 0 || page >= A.n_pages) {
-        atomicOr(A.status, CACHE_BAD_PAGE);
-        page = A.n_pages;               // out of range: the copy reads zeros
-      }
-      return page;
+      return tok < s_len[p.b] ? __ldcg(a.tables + (long long)p.b * a.table_stride + (tok >> A.page_log2)) : 0;
     };
-    if (first >= last) return;
+    if (t0 >= last) return;
     Place at = begin;
-    int page = page_of(at), j_begin = at.j;
-    if (!copy_rows(0, at)) return;
-    for (int t = first; t < last; ++t) {
+    int pages = pages_from(at), j_begin = at.j, turn = team;   // turn: odd when the next tile is the other team's
+    for (int t = t0; t < last;) {
+      constexpr int TILES = 32 / KT;
+      int n_tiles = at.n - at.j < TILES ? at.n - at.j : TILES;
+      n_tiles = last - t < n_tiles ? last - t : n_tiles;
       Place nx = at;
-      const bool more = t + 1 < last, ends = at.j + 1 == at.n;
-      if (more) {
-        ++nx.j;
-        if (ends) nx.template next_item<S>(s_len, heads);
+      nx.j += n_tiles;
+      const bool ends = nx.j == nx.n;
+      const int t_next = t + n_tiles + (ends ? S::EXTRA : 0);
+      const bool more = t_next < last;
+      if (more && ends) nx.template next_item<S>(s_len, heads);
+      const int pages_next = more ? pages_from(nx) : 0;
+      if (team == 0 && at.j == j_begin && !copy_rows(at, a.gate.p && at.j == 0 && at.n <= last - t)) return;
+      if ((unsigned)pages >= (unsigned)A.n_pages) {
+        atomicOr(A.status, CACHE_BAD_PAGE);
+        pages = A.n_pages;                             // out of range: the copy reads zeros
       }
-      const int page_next = more ? page_of(nx) : -1;
-      const int left = s_len[at.b] - at.j * TN;
-      const int groups = left >= TN ? KT : (left + 15) >> 4;
       const int row0 = (at.h / A.head_tiles) << A.page_log2;
+      for (int i = turn & 1; i < n_tiles; i += TEAMS) {
+        const int tok0 = (at.j + i) * TN, left = s_len[at.b] - tok0;
+        const int groups = left >= TN ? KT : (left + 15) >> 4;
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
+        for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll 1
-        for (int g0 = 0; g0 < groups; g0 += GPS) {
-          if (!free_to_fill(&empty[stage], phase ^ 1)) return;
-          const int n = groups - g0 < GPS ? groups - g0 : GPS;
-          if (lane == 0) mbar_expect_tx(&full[stage], n * S::GROUP_BYTES);
-          const int grp = lane / S::CH, x = lane % S::CH;
-          const int pg = __shfl_sync(0xFFFFFFFFu, page, (g0 + grp) & 31);
-          if (grp < n && !skip)
-            tma_rows(ring + stage * S::STAGE + grp * S::GROUP_BYTES + x * 16 * S::CB, kv ? &vmap : &kmap,
-                     x * (D / S::CH), row0 + ((at.j * TN + (g0 + grp) * 16) & ((1 << A.page_log2) - 1)), pg,
-                     &full[stage]);
-          skip = false;
-          if (++stage == A.n_stages) { stage = 0; phase ^= 1; }
+          for (int g0 = 0; g0 < groups; g0 += GPS) {
+            if (!free_to_fill(&empty[stage], phase ^ 1)) return;
+            const int n = groups - g0 < GPS ? groups - g0 : GPS;
+            int page[GPS];
+#pragma unroll
+            for (int grp = 0; grp < GPS; ++grp) page[grp] = __shfl_sync(0xFFFFFFFFu, pages, (i * KT + g0 + grp) & 31);
+            uint8_t* const dst = my_ring + stage * S::STAGE;
+            const CUtensorMap* const map = kv ? &vmap : &kmap;
+            const int tok = tok0 + g0 * 16, in_page = (1 << A.page_log2) - 1;
+            if (elect_one()) {
+              mbar_expect_tx(&full[stage], n * S::GROUP_BYTES);
+#pragma unroll
+              for (int grp = 0; grp < GPS; ++grp)
+                if (grp < n && !skip)
+#pragma unroll
+                  for (int x = 0; x < S::CH; ++x)
+                    tma_rows(dst + grp * S::GROUP_BYTES + x * 16 * S::CB, map, x * (D / S::CH),
+                             row0 + ((tok + grp * 16) & in_page), page[grp], &full[stage]);
+            }
+            __syncwarp();
+            skip = false;
+            if (++stage == A.n_stages) { stage = 0; phase ^= 1; }
+          }
         }
       }
-      if (ends) {
-        // gates are wanted where the whole item is this CTA's, at its end
-        if (a.gate.p && j_begin == 0 && !copy_rows(1, at)) return;
-        if (more && !copy_rows(0, nx)) return;
-        j_begin = 0;
-      }
+      if (ends) j_begin = 0;
+      t = t_next;
+      turn += n_tiles;
       at = nx;
-      page = page_next;
+      pages = pages_next;
     }
     return;
   }
 
   // ------------------------------------------------------------------ products
   const int g = lane >> 2, t4 = lane & 3;
+  const int team = warp / WARPS, wt = warp % WARPS, ttid = tid % MATH;    // a warp and a thread within their team
+  uint16_t* const s_p = s_p0 + team * NH * PP;
+  float* const s_max = s_max0 + team * WARPS * NH;
+  float* const s_sum = s_sum0 + team * WARPS * NH;
   // requests of length 0
   for (int b = blockIdx.x; b < A.B; b += gridDim.x)
     if (s_len[b] == 0)
-      for (int i = tid; i < A.Hq * D / 8; i += S::MATH)
+      for (int i = tid; i < A.Hq * D / 8; i += TEAMS * MATH)
         *reinterpret_cast<uint4*>(rows_at(a.out, b, i / (D / 8), i % (D / 8) * 8)) = make_uint4(0, 0, 0, 0);
 
   // Where a lane's rows of a stage lie. 16-byte chunk c of row r of a group of 16 tokens is at
@@ -500,10 +594,12 @@ __global__ void __launch_bounds__(S::THREADS, 2)
     const int sw = S::CB == 128 ? r & 7 : (r >> 1) & 3;
     return (uint32_t)((c / PER) * (16 * S::CB) + r * S::CB + (((c % PER) ^ sw) << 4));
   };
-  const uint32_t ring0 = smem_u32(ring);
+  const uint32_t ring0 = smem_u32(ring) + team * A.n_stages * S::STAGE;
+  uint64_t* const full = full0 + team * 16;
+  uint64_t* const empty = empty0 + team * 16;
   const uint32_t k_lane = ring0 + in_group(lane & 15, lane >> 4);
-  const uint32_t v_lane = ring0 + (S::E4M3 ? (lane >> 4) * S::GROUP_BYTES + in_group(lane & 15, warp * MD)
-                                           : in_group((lane & 7) + ((lane >> 4) << 3), warp * MD * 2 + ((lane >> 3) & 1)));
+  const uint32_t v_lane = ring0 + (S::E4M3 ? (lane >> 4) * S::GROUP_BYTES + in_group(lane & 15, wt * MD)
+                                           : in_group((lane & 7) + ((lane >> 4) << 3), wt * MD * 2 + ((lane >> 3) & 1)));
   const uint32_t p_lane = smem_u32(s_p) + ((lane & 7) * PP + (lane >> 3) * 8) * 2;
   auto wait_full = [&](uint64_t* bar, uint32_t parity) {
     // once a wait has run out the outputs are lost: run to the end without waiting
@@ -519,11 +615,12 @@ __global__ void __launch_bounds__(S::THREADS, 2)
   };
 
   int stage = 0;
-  uint32_t phase = 0, rows_phase[2] = {0, 0};
-  if (first >= last) return;
-  int t = first;
+  uint32_t phase = 0, n_rows = 0;
+  if (t0 >= last) return;
+  int t = t0, done = 0;                                      // done: tiles of the CTA so far
   Place at = begin;
   Split split[2] = {{-1, 0, 0, 0}, {-1, 0, 0, 0}};           // of the first item and of the last
+  int head_before = -1;                                      // parts of the first item that had arrived before this CTA's
   while (t < last) {
     const int kvh = at.h / A.head_tiles, h_in = (at.h % A.head_tiles) * NH;
     const int h0 = kvh * A.group + h_in;                       // first query head of the item
@@ -536,12 +633,12 @@ __global__ void __launch_bounds__(S::THREADS, 2)
     // past nh hold whatever memory holds: no head's column reaches another's, and theirs are not written.
     uint32_t q[D / 16][NT][2];
     float sf[NT][2];                                           // what a product is multiplied by, for 2^x
-    wait_full(&rows_full[0], rows_phase[0]);
-    rows_phase[0] ^= 1;
+    wait_full(&rows_full[n_rows & 1], n_rows >> 1 & 1);
+    const uint16_t* const q_rows = s_q + (n_rows & 1) * 2 * NH * QP;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (S::E4M3) {
-        const uint16_t* src = s_q + (nt * 8 + g) * QP + 4 * t4;
+        const uint16_t* src = q_rows + (nt * 8 + g) * QP + 4 * t4;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint2 v = *reinterpret_cast<const uint2*>(src + ks * 16);
@@ -549,7 +646,7 @@ __global__ void __launch_bounds__(S::THREADS, 2)
           q[ks][nt][1] = v.y;
         }
       } else {
-        const uint32_t src = smem_u32(s_q + (nt * 8 + (lane & 7)) * QP + (lane >> 3) * 8);
+        const uint32_t src = smem_u32(q_rows + (nt * 8 + (lane & 7)) * QP + (lane >> 3) * 8);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ks += 2) {
           uint32_t r[4];
@@ -590,7 +687,6 @@ __global__ void __launch_bounds__(S::THREADS, 2)
       for (int i = 0; i < 2; ++i)
         sf[nt][i] = A.scale * (S::E4M3 ? a.k_scale[kvh] * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + i) * 4) : 1.f);
     }
-    release(&rows_empty[0]);
 
     float o[MD][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -606,7 +702,7 @@ __global__ void __launch_bounds__(S::THREADS, 2)
         for (int i = 0; i < 4; ++i) o[md][nt][i] = 0.f;
     }
 
-    for (int j = j0; j < j1; ++j) {
+    for (int j = j0 + ((done + team) & 1); j < j1; j += TEAMS) {
       const int left = len - j * TN;                           // tokens of the request from this tile on
       const int groups = left >= TN ? KT : (left + 15) >> 4;
       // ---- S^T = K Q^T for this warp's groups of 16 tokens; two chains of accumulators, as one would wait for each
@@ -620,11 +716,11 @@ __global__ void __launch_bounds__(S::THREADS, 2)
           for (int i = 0; i < 4; ++i) s[mt][nt][i] = s2[mt][nt][i] = 0.f;
 #pragma unroll 1
       for (int g0 = 0; g0 < groups; g0 += GPS) {
-        // every warp waits for every stage: one that went ahead could release a stage twice before the others once
+        // every warp of the team waits for every stage: one that went ahead could release a stage twice before the others once
         wait_full(&full[stage], phase);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const int gr = mt * WARPS + warp - g0;
+          const int gr = mt * WARPS + wt - g0;
           if (gr < 0 || gr >= GPS || g0 + gr >= groups) continue;
           const uint32_t from = k_lane + stage * S::STAGE + gr * S::GROUP_BYTES;
           if (S::E4M3) {
@@ -659,7 +755,7 @@ __global__ void __launch_bounds__(S::THREADS, 2)
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int tok = (mt * WARPS + warp) * 16;
+        const int tok = (mt * WARPS + wt) * 16;
         const bool edge = left < tok + 16;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -686,8 +782,8 @@ __global__ void __launch_bounds__(S::THREADS, 2)
       if (lane < 4)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          *reinterpret_cast<float2*>(&s_max[warp * NH + nt * 8 + 2 * t4]) = make_float2(top[nt][0], top[nt][1]);
-      math_barrier<S>();
+          *reinterpret_cast<float2*>(&s_max[wt * NH + nt * 8 + 2 * t4]) = make_float2(top[nt][0], top[nt][1]);
+      team_barrier<S>(team);
       bool moved = false;
       float c[NT][2];
 #pragma unroll
@@ -723,7 +819,7 @@ __global__ void __launch_bounds__(S::THREADS, 2)
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<uint32_t*>(&s_p[(nt * 8 + g) * PP + (mt * WARPS + warp) * 16 + 8 * r + 2 * t4]) =
+            *reinterpret_cast<uint32_t*>(&s_p[(nt * 8 + g) * PP + (mt * WARPS + wt) * 16 + 8 * r + 2 * t4]) =
                 transpose8x8(pack2<S::MMA_BF16>(s[mt][nt][2 * r], s[mt][nt][2 * r + 1]));
       }
       if (__any_sync(0xFFFFFFFFu, moved)) {
@@ -734,7 +830,7 @@ __global__ void __launch_bounds__(S::THREADS, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[md][nt][i] *= c[nt][i & 1];
       }
-      math_barrier<S>();
+      team_barrier<S>(team);
 
       // ---- O^T += V^T P^T for this warp's rows of d
 #pragma unroll 1
@@ -748,37 +844,85 @@ __global__ void __launch_bounds__(S::THREADS, 2)
       }
     }
 
-    // ---- the end of the item, or of the CTA's share of it
+    // ---- the end of the item, or of the CTA's share of it: the team with its last tile has the other's results added
+    const bool owner = ((done + j1 - 1 - j0) & 1) == team, alone = j1 - j0 == 1;
+    const bool whole = j0 == 0 && j1 == at.n;
+    auto put_sums = [&](float* to) {             // [WARPS][NH]
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = l[nt][i];
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
-        if (lane < 4) s_sum[warp * NH + nt * 8 + 2 * t4 + i] = x;
+        for (int i = 0; i < 2; ++i) {
+          float x = l[nt][i];
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
+          if (lane < 4) to[wt * NH + nt * 8 + 2 * t4 + i] = x;
+        }
+    };
+    if (!alone && !owner) {
+      named_bar(3, TEAMS * MATH);                // what lay here has been read
+      put_sums(s_x + NH * D + NH);
+#pragma unroll
+      for (int md = 0; md < MD; ++md)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          reinterpret_cast<float4*>(s_x)[(md * NT + nt) * MATH + ttid] =
+              make_float4(o[md][nt][0], o[md][nt][1], o[md][nt][2], o[md][nt][3]);
+      if (wt == 0 && g == 0)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) s_x[NH * D + nt * 8 + 2 * t4 + i] = m[nt][i];
+      named_arrive(4, TEAMS * MATH);
+    }
+    if (owner) {
+      put_sums(s_sum);
+      if (alone) {
+        team_barrier<S>(team);
+      } else {
+        named_arrive(3, TEAMS * MATH);
+        named_bar(4, TEAMS * MATH);
       }
-    math_barrier<S>();
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = 0.f;
+        for (int i = 0; i < 2; ++i) {
+          const int h = nt * 8 + 2 * t4 + i;
+          float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) x += s_sum[w * NH + nt * 8 + 2 * t4 + i];
-        l[nt][i] = x;
-      }
+          for (int w = 0; w < WARPS; ++w) x += s_sum[w * NH + h];
+          if (!alone) {
+            const float m1 = s_x[NH * D + h], nm = fmaxf(m[nt][i], m1), base = nm == -INFINITY ? 0.f : nm;
+            const float c0 = exp2_fast(m[nt][i] - base), c1 = exp2_fast(m1 - base);
+            float x1 = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) x1 += s_x[NH * D + NH + w * NH + h];
+            x = x * c0 + x1 * c1;
+            m[nt][i] = nm;
+#pragma unroll
+            for (int md = 0; md < MD; ++md)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                o[md][nt][2 * r + i] = o[md][nt][2 * r + i] * c0 + s_x[((md * NT + nt) * MATH + ttid) * 4 + 2 * r + i] * c1;
+          }
+          l[nt][i] = x;
+        }
+    }
     const float vs = S::E4M3 ? a.v_scale[kvh] : 1.f;
     // the rows of d that an accumulator's two halves hold
     auto d_of = [&](int md, int r) {
-      return S::E4M3 ? (warp * MD + md) * 16 + 2 * g + r : (warp * MD + md) * 16 + g + 8 * r;
+      return S::E4M3 ? (wt * MD + md) * 16 + 2 * g + r : (wt * MD + md) * 16 + g + 8 * r;
     };
-    if (j0 == 0 && j1 == at.n) {
-      if (a.gate.p) {
-        wait_full(&rows_full[1], rows_phase[1]);
-        rows_phase[1] ^= 1;
-      }
+    // a part is joined with the others once this CTA has nothing else to do: the item's tiles are those of CTAs c0 .. c1;
+    // c0 holds its part as the item it leaves, the others as the item they begin in the middle of
+    const int which = j0 == 0 ? 1 : 0;
+    if (!whole) {
+      const Split sp = {at.b, at.h, (t - j0) / share, (t - j0 + at.n - 1) / share};
+      if (which) split[1] = sp; else split[0] = sp;
+    }
+    if (!owner) {
+      release(&rows_empty[n_rows & 1]);
+    } else if (whole) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -793,18 +937,12 @@ __global__ void __launch_bounds__(S::THREADS, 2)
               float y = o[md][nt][2 * r + i] * f;
               const int d = d_of(md, r);
               if (a.gate.p) {
-                y = gated(y, unpack2<S::BF16>(s_q[(NH + h) * QP + d]).x);
+                y = gated(y, unpack2<S::BF16>(q_rows[(NH + h) * QP + d]).x);
               }
               *rows_at(a.out, at.b, h0 + h, d) = (uint16_t)pack2<S::BF16>(y, 0.f);
             }
         }
-      if (a.gate.p) release(&rows_empty[1]);
     } else {
-      // a part, joined with the others once this CTA has nothing else to do: the item's tiles are those of CTAs c0 .. c1;
-      // c0 holds its part as the item it leaves, the others as the item they begin in the middle of
-      const int which = j0 == 0 ? 1 : 0;
-      const Split sp = {at.b, at.h, (t - j0) / share, (t - j0 + at.n - 1) / share};
-      if (which) split[1] = sp; else split[0] = sp;
       float* part = A.parts + ((long long)blockIdx.x * 2 + which) * S::PART;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -815,38 +953,48 @@ __global__ void __launch_bounds__(S::THREADS, 2)
           for (int md = 0; md < MD; ++md)
 #pragma unroll
             for (int r = 0; r < 2; ++r) part[h * D + d_of(md, r)] = o[md][nt][2 * r + i];
-          if (warp == 0 && g == 0) {
+          if (wt == 0 && g == 0) {
             part[NH * D + h] = m[nt][i];
             part[NH * D + NH + h] = l[nt][i];
           }
         }
     }
-    t += j1 - j0;
+    if (owner) release(&rows_empty[n_rows & 1]);
+    ++n_rows;
+    if (owner && !whole && which == 0 && t + j1 - j0 < last) {
+      // the first item's part arrives now, while there are tiles to come; whether it was the last is looked at in the end
+      team_barrier<S>(team);
+      if (ttid == 0) {
+        __threadfence();
+        head_before = arrive(A, split[0]);
+      }
+    }
+    done += j1 - j0;
+    t += j1 - j0 + (j1 == at.n ? S::EXTRA : 0);
     if (t < last) at.template next_item<S>(s_len, heads);
   }
 
   // ---- joining the split items: the last of an item's parts to arrive joins them
   if (split[0].b < 0 && split[1].b < 0) return;
+  if (head_before >= 0) {
+    s_flags[3] = 1;
+    s_flags[1] = complete(A, split[0], head_before);
+  }
   __threadfence();
-  math_barrier<S>();
+  if (team) {
+    named_arrive(3, TEAMS * MATH);
+    return;
+  }
+  named_bar(3, TEAMS * MATH);
   const int gi = blockIdx.x / GROUP;
   if (lane == 0 && warp < 2) {
     const Split sp = warp ? split[1] : split[0];
-    bool all = false;
-    if (sp.b >= 0) {
-      const bool flat = sp.c1 - sp.c0 < FLAT;
-      uint32_t* const count = flat ? &A.counts[sp.c0] : &A.group_counts[2 * gi + (gi == sp.c0 / GROUP)];
-      const int from = flat || sp.c0 > gi * GROUP ? sp.c0 : gi * GROUP;
-      const int to = flat || sp.c1 < gi * GROUP + GROUP ? sp.c1 : gi * GROUP + GROUP - 1;
-      all = atomicAdd(count, 1u) == (uint32_t)(to - from);
-      if (all) *count = 0;
-    }
-    s_flags[1 + warp] = all;
+    if (sp.b >= 0 && !(warp == 0 && s_flags[3])) s_flags[1 + warp] = complete(A, sp, arrive(A, sp));
   }
-  math_barrier<S>();
+  team_barrier<S>(team);
   Joined<S> y;
   uint32_t join_phase = 0;
-  const int fit = A.n_stages * S::STAGE / (S::PART * 4);
+  const int fit = TEAMS * A.n_stages * S::STAGE / (S::PART * 4);
   const int at_once = fit < PP / 4 - 1 ? fit : PP / 4 - 1;      // the weights lie where P did
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
@@ -860,7 +1008,7 @@ __global__ void __launch_bounds__(S::THREADS, 2)
       y.clear();
       for (int k0 = ia; k0 <= ib; k0 += at_once) {
         const int n = ib - k0 + 1 < at_once ? ib - k0 + 1 : at_once;
-        math_barrier<S>();                       // what the ring held has been read
+        team_barrier<S>(team);                       // what the ring held has been read
         if (tid == 0) {
           fence_proxy_async_global();
           mbar_expect_tx(join_full, n * S::PART * 4);
@@ -877,20 +1025,21 @@ __global__ void __launch_bounds__(S::THREADS, 2)
     const int h0 = kvh * A.group + h_in;
     if (sp.c1 - sp.c0 < FLAT) {
       y.fetch_gates(A, sp.b, h0, nh, tid);
-      join(A.parts, sp.c0, sp.c1, sp.c0);
+      if (sp.c1 - sp.c0 < Joined<S>::FEW) y.few(A.parts, sp.c0, sp.c1, sp.c0, tid);
+      else join(A.parts, sp.c0, sp.c1, sp.c0);
     } else {
       // many parts: each GROUP of CTAs joins its own, and the last group to do so the groups'
       const int g0 = sp.c0 / GROUP, g1 = sp.c1 / GROUP;
       join(A.parts, gi == g0 ? sp.c0 : gi * GROUP, gi == g1 ? sp.c1 : gi * GROUP + GROUP - 1, sp.c0);
       y.keep(A.group_parts + ((long long)gi * 2 + (gi == g0)) * S::PART, tid);
       __threadfence();
-      math_barrier<S>();
+      team_barrier<S>(team);
       if (tid == 0) {
         const bool all = atomicAdd(&A.counts[sp.c0], 1u) == (uint32_t)(g1 - g0);
         if (all) A.counts[sp.c0] = 0;
         s_flags[1 + i] = all;
       }
-      math_barrier<S>();
+      team_barrier<S>(team);
       if (!s_flags[1 + i]) continue;
       __threadfence();
       y.fetch_gates(A, sp.b, h0, nh, tid);
@@ -935,19 +1084,19 @@ cudaError_t pool_map(const CacheShape& c, const void* pool, int64_t page_stride,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-constexpr int SMEM_PER_CTA = 113 * 1024;      // two CTAs to an SM's 228 KB, of which each costs one more
+constexpr int SMEM_PER_CTA = 227 * 1024;
 
 template <class S>
 cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
-  static_assert(S::MISC + 1024 + CACHE_MAX_REQUESTS * 4 + 2 * S::STAGE <= SMEM_PER_CTA, "the ring has two stages at least");
+  static_assert(S::MISC + 1024 + CACHE_MAX_REQUESTS * 4 + S::TEAMS * 2 * S::STAGE <= SMEM_PER_CTA, "the ring has two stages at least");
   CUtensorMap km, vm;
   cudaError_t e = pool_map<S>(c, A.a.k_cache, A.a.k_page_stride, &km);
   if (e == cudaSuccess) e = pool_map<S>(c, A.a.v_cache, A.a.v_page_stride, &vm);
   if (e != cudaSuccess) return e;
   A.head_tiles = (A.group + S::NH - 1) / S::NH;
   const int other = S::MISC + 1024 + A.B * 4;
-  const int n = (SMEM_PER_CTA - other) / S::STAGE;
-  A.n_stages = n > 32 ? 32 : n;
+  const int n = (SMEM_PER_CTA - other) / (S::TEAMS * S::STAGE);
+  A.n_stages = n > 16 ? 16 : n;
   static bool ready[64] = {};
   int dev = 0;
   e = cudaGetDevice(&dev);
@@ -956,7 +1105,7 @@ cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
     if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev] = true;
   }
   if (e != cudaSuccess) return e;
-  k_cache_attend<S><<<ctas, S::THREADS, other + A.n_stages * S::STAGE, st>>>(A, km, vm);
+  k_cache_attend<S><<<ctas, S::THREADS, other + S::TEAMS * A.n_stages * S::STAGE, st>>>(A, km, vm);
   return cudaGetLastError();
 }
 
@@ -973,7 +1122,7 @@ cudaError_t run_types(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t
 }  // namespace
 
 size_t cache_attend_workspace(int num_sms) {
-  const size_t ctas = 2 * (size_t)num_sms < MAX_CTAS ? 2 * (size_t)num_sms : MAX_CTAS;
+  const size_t ctas = num_sms < MAX_CTAS ? num_sms : MAX_CTAS;
   const size_t groups = (ctas + GROUP - 1) / GROUP;
   return ((ctas + groups) * 2 * PART_MAX + COUNT_WORDS) * 4;
 }
@@ -990,7 +1139,7 @@ cudaError_t cache_attend_launch(const CacheShape& S, const moe_cache_attend_t& a
   A.n_pages = S.n_pages;
   A.max_len = (long long)S.max_pages << S.page_log2;
   A.scale = (float)a.scale * LOG2E;
-  const int ctas = 2 * w.num_sms < MAX_CTAS ? 2 * w.num_sms : MAX_CTAS;
+  const int ctas = w.num_sms < MAX_CTAS ? w.num_sms : MAX_CTAS;       // one to an SM
   A.counts = (uint32_t*)w.workspace;
   A.group_counts = A.counts + MAX_CTAS;
   A.parts = (float*)w.workspace + COUNT_WORDS;
