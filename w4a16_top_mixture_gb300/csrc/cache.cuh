@@ -46,6 +46,30 @@ size_t cache_attend_workspace(int num_sms);
 cudaError_t cache_attend_launch(const CacheShape& S, const moe_cache_attend_t& a, const CacheAttendState& w,
                                 cudaStream_t st);
 
+// ---- launches ----
+// The three kernels are launched so that they may start while the kernel before them in the stream still ends
+// (programmatic dependent launch): each lets its successor start at once, and waits for its predecessor's end before it
+// reads or writes device memory. What a predecessor wrote is read past L1 (__ldcg, bulk copies): a line that another
+// kernel left in an SM's L1 could be older.
+__device__ __forceinline__ void follow_predecessor() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch_following(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // ---- 16-bit pairs ----
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {

@@ -21,6 +21,7 @@
 namespace moe {
 namespace {
 
+constexpr int SHORT = 4;                          // units of an item that is not split without need
 constexpr int GROUP = 10, FLAT = 20;              // CTAs whose parts are joined first; from FLAT + 1 parts on
 constexpr int MAX_CTAS = 1024, COUNT_WORDS = MAX_CTAS + MAX_CTAS / GROUP * 2;    // of the workspace
 constexpr int PART_MAX = 16 * 256 + 32;           // floats of the largest part
@@ -122,8 +123,11 @@ __device__ __forceinline__ void named_arrive(int id, int nthreads) {
 // ---- the division of the work ----
 // Items come request by request, within a request head by head. An item of n tiles is n + EXTRA units long, for what its
 // beginning and end cost; CTA c takes units c * share .. (c + 1) * share - 1.
-__host__ __device__ inline int even_share(int units, int ctas) {
-  return units > 0 ? (int)(((long long)units + ctas - 1) / ctas) : 1;
+// An even share; but while no item is longer than SHORT, a CTA takes whole items: a split one's parts take longer to join
+// than a few tiles to read (130 tokens of two 256-wide heads: 8.5 us whole, 10.5 us in six parts).
+__host__ __device__ inline int even_share(int units, int longest, int ctas) {
+  const int even = units > 0 ? (int)(((long long)units + ctas - 1) / ctas) : 1;
+  return longest <= SHORT && even < longest ? longest : even;
 }
 template <class S>
 __device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + S::TN - 1) / S::TN); }
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   uint64_t* const join_full = rows_empty + 2;        // parts, when the ring is done with
   volatile int* const s_flags = (int*)(join_full + 1);    // 0: a wait ran out; 1, 2: last to arrive; 3: the first has
   int* const s_scan = (int*)(join_full + 1) + 4;     // [THREADS / 32]
-  int* const s_place = s_scan + 16;                  // [3]
+  int* const s_place = s_scan + 32;                  // [3]
   uint16_t* const s_q = (uint16_t*)(misc + 1024);    // [2][2][NH][QP]: by turns, queries and gates
   uint16_t* const s_p0 = s_q + 4 * NH * QP;          // [TEAMS][NH][PP]
   float* const s_max0 = (float*)(s_p0 + TEAMS * NH * PP);   // [TEAMS][WARPS][NH]
@@ -410,11 +414,12 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     fence_mbar_init();
     s_flags[0] = s_flags[1] = s_flags[2] = s_flags[3] = 0;
   }
+  follow_predecessor();
   // lengths and the running number of tiles: a thread's requests lie side by side, so that all its loads are on their way
   // at once
   const int each = (A.B + S::THREADS - 1) / S::THREADS, b_begin = tid * each < A.B ? tid * each : A.B;
   const int b_end = b_begin + each < A.B ? b_begin + each : A.B;
-  int mine = 0;
+  int mine = 0, longest = 0;
 #pragma unroll 4
   for (int b = b_begin; b < b_end; ++b) {
     int len = __ldcg(a.lengths + b);
@@ -423,7 +428,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       len = len < 0 ? 0 : (int)A.max_len;
     }
     s_len[b] = len;
-    mine += len ? tiles_of<S>(len) + S::EXTRA : 0;
+    const int n = len ? tiles_of<S>(len) + S::EXTRA : 0;
+    mine += n;
+    longest = max(longest, n);
   }
   // a wait ran out in an earlier call, or has in this one: the counts are off until the status is read
   const bool dead = tid == 0 && (*(volatile uint32_t*)A.status & CACHE_BAD_WAIT);
@@ -433,14 +440,19 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
     if (lane >= o) upto += y;
   }
-  if (lane == 31) s_scan[warp] = upto;
+  const int wlongest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  if (lane == 31) {
+    s_scan[warp] = upto;
+    s_scan[16 + warp] = wlongest;
+  }
   if (__syncthreads_or(dead)) return;
   int carry = 0;
   for (int w = 0; w < S::THREADS / 32; ++w) {
     if (w < warp) upto += s_scan[w];
     carry += s_scan[w];
+    longest = max(longest, s_scan[16 + w]);
   }
-  const int units = carry * heads, share = even_share(units, gridDim.x);
+  const int units = carry * heads, share = even_share(units, longest, gridDim.x);
   const int first = (long long)share * blockIdx.x < units ? share * blockIdx.x : units;
   const int last = share < units - first ? first + share : units;
   // where the CTA begins: found by the thread that holds the request
@@ -685,7 +697,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        sf[nt][i] = A.scale * (S::E4M3 ? a.k_scale[kvh] * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + i) * 4) : 1.f);
+        sf[nt][i] = A.scale * (S::E4M3 ? __ldcg(a.k_scale + kvh) * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + i) * 4) : 1.f);
     }
 
     float o[MD][NT][4], m[NT][2], l[NT][2];
@@ -908,7 +920,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           l[nt][i] = x;
         }
     }
-    const float vs = S::E4M3 ? a.v_scale[kvh] : 1.f;
+    const float vs = S::E4M3 ? __ldcg(a.v_scale + kvh) : 1.f;
     // the rows of d that an accumulator's two halves hold
     auto d_of = [&](int md, int r) {
       return S::E4M3 ? (wt * MD + md) * 16 + 2 * g + r : (wt * MD + md) * 16 + g + 8 * r;
@@ -1003,7 +1015,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     const Split sp = i ? split[1] : split[0];
     const int kvh = sp.h / A.head_tiles, h_in = (sp.h % A.head_tiles) * NH;
     const int nh = A.group - h_in < NH ? A.group - h_in : NH;
-    const float vs = S::E4M3 ? a.v_scale[kvh] : 1.f;
+    const float vs = S::E4M3 ? __ldcg(a.v_scale + kvh) : 1.f;
     auto join = [&](const float* parts, int ia, int ib, int i0) {
       y.clear();
       for (int k0 = ia; k0 <= ib; k0 += at_once) {
@@ -1105,8 +1117,7 @@ cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
     if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev] = true;
   }
   if (e != cudaSuccess) return e;
-  k_cache_attend<S><<<ctas, S::THREADS, other + S::TEAMS * A.n_stages * S::STAGE, st>>>(A, km, vm);
-  return cudaGetLastError();
+  return launch_following(k_cache_attend<S>, ctas, S::THREADS, other + S::TEAMS * A.n_stages * S::STAGE, st, A, km, vm);
 }
 
 template <int D, bool BF16, bool E4M3>

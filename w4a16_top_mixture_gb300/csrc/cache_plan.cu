@@ -57,7 +57,8 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
   const int ps = 1 << a.page_log2;
   const long long max_len = (long long)a.max_pages << a.page_log2;
   const int tid = threadIdx.x, nth = blockDim.x;
-  int head = p.free_state[0], count = p.free_state[1];
+  follow_predecessor();
+  int head = __ldcg(p.free_state), count = __ldcg(p.free_state + 1);
   if (head < 0 || head >= a.n_pages || count < 0 || count > a.n_pages) {
     head = count = 0;
     if (tid == 0) atomicOr(a.status, CACHE_BAD_STATE);
@@ -69,8 +70,8 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
   for (int b0 = 0; b0 < a.B; b0 += nth) {
     const int b = b0 + tid;
     const bool in = b < a.B;
-    const int len = in ? p.lengths[b] : 0;
-    const int nw = in ? (p.new_tokens ? p.new_tokens[b] : 1) : 0;
+    const int len = in ? __ldcg(p.lengths + b) : 0;
+    const int nw = in ? (p.new_tokens ? __ldcg(p.new_tokens + b) : 1) : 0;
     const bool good = len >= 0 && len <= max_len;
     const bool done = nw < 0;
     const long long n = nw > 0 ? nw : 0;
@@ -112,11 +113,11 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
         const int held = (int)(((long long)len + ps - 1) >> a.page_log2);
         const int want = (int)(((long long)len + n + ps - 1) >> a.page_log2);
         for (int j = held + lane; j < want; j += 32)
-          row[j] = p.free_pages[((uint32_t)head + (uint32_t)at + (uint32_t)(j - held)) % (uint32_t)a.n_pages];
+          row[j] = __ldcg(p.free_pages + ((uint32_t)head + (uint32_t)at + (uint32_t)(j - held)) % (uint32_t)a.n_pages);
       } else if (at <= -2 && len > 0 && len <= max_len) {
         const int held = (int)(((long long)len + ps - 1) >> a.page_log2);
         const uint32_t to = (uint32_t)head + (uint32_t)count + (uint32_t)(-2 - at);
-        for (int j = lane; j < held; j += 32) p.free_pages[(to + (uint32_t)j) % (uint32_t)a.n_pages] = row[j];
+        for (int j = lane; j < held; j += 32) p.free_pages[(to + (uint32_t)j) % (uint32_t)a.n_pages] = __ldcg(row + j);
       }
     }
   }
@@ -133,9 +134,9 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
       pos = len + (int)(r - (lo ? s_end[lo - 1] : 0));
       const int held = (int)(((long long)len + ps - 1) >> a.page_log2), j = pos >> a.page_log2;
       // a page taken in this call is read where it comes from
-      const int page = j < held ? p.tables[(size_t)lo * p.table_stride + j]
-                                : p.free_pages[((uint32_t)head + (uint32_t)s_at[lo] + (uint32_t)(j - held)) %
-                                               (uint32_t)a.n_pages];
+      const int page = __ldcg(j < held ? p.tables + (size_t)lo * p.table_stride + j
+                                       : p.free_pages + ((uint32_t)head + (uint32_t)s_at[lo] + (uint32_t)(j - held)) %
+                                                            (uint32_t)a.n_pages);
       if (page >= 0 && page < a.n_pages) slot = (page << a.page_log2) + (pos & (ps - 1));
       else atomicOr(a.status, CACHE_BAD_PAGE);
     }
@@ -188,8 +189,7 @@ cudaError_t cache_plan_launch(const CacheShape& S, const moe_cache_plan_t& p, ui
   threads = threads < 128 ? 128 : threads > 1024 ? 1024 : threads;
   const long long want = ((long long)a.rows + threads - 1) / threads;
   const int grid = (int)(want < 1 ? 1 : want > num_sms ? num_sms : want);
-  k_cache_plan<<<grid, threads, (size_t)a.B * 12, st>>>(a);
-  return cudaGetLastError();
+  return launch_following(k_cache_plan, grid, threads, (size_t)a.B * 12, st, a);
 }
 
 }  // namespace moe

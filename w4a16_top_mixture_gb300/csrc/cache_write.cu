@@ -25,13 +25,14 @@ __global__ void __launch_bounds__(256) k_cache_write(const __grid_constant__ Wri
   const long long t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int half = a.rope / 2;
+  follow_predecessor();
   for (int i = threadIdx.x; i < half; i += 256) {
-    const double turns = (double)w.positions[t] * a.turns[i];
+    const double turns = (double)__ldcg(w.positions + t) * a.turns[i];
     float c, s;
     sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
     s_cs[i] = make_float2(c, s);
   }
-  const int slot = w.slots[t];
+  const int slot = __ldcg(w.slots + t);
   const bool put = slot >= 0 && slot < a.n_slots;
   if (slot >= a.n_slots && threadIdx.x == 0) atomicOr(a.status, CACHE_BAD_PAGE);
   const int page = slot >> a.page_log2, off = slot & ((1 << a.page_log2) - 1);
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(256) k_cache_write(const __grid_constant__ Wri
     const bool live = in && src.p != nullptr;
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (live)
-      raw = *reinterpret_cast<const uint4*>((const uint16_t*)src.p + t * src.row_stride + h * src.head_stride + 8 * l);
+      raw = __ldcg(reinterpret_cast<const uint4*>((const uint16_t*)src.p + t * src.row_stride + h * src.head_stride + 8 * l));
     float x[8];
     {
       const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(256) k_cache_write(const __grid_constant__ Wri
     for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     if (gamma) {
       const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-      const uint4 gr = *reinterpret_cast<const uint4*>((const uint16_t*)gamma + 8 * l);
+      const uint4 gr = __ldcg(reinterpret_cast<const uint4*>((const uint16_t*)gamma + 8 * l));
       const uint32_t g[4] = {gr.x, gr.y, gr.z, gr.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(256) k_cache_write(const __grid_constant__ Wri
                            ((long long)h << a.page_log2) * D + (long long)off * D + e;
       void* pool = kind == 1 ? w.k_cache : w.v_cache;
       if (E4M3) {
-        const float s = (kind == 1 ? w.k_scale : w.v_scale)[h];
+        const float s = __ldcg((kind == 1 ? w.k_scale : w.v_scale) + h);
         uint32_t c[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -115,12 +116,10 @@ __global__ void __launch_bounds__(256) k_cache_write(const __grid_constant__ Wri
 }
 
 template <int D>
-void launch(const WriteArgs& a, bool bf16, bool e4m3, cudaStream_t st) {
-  const dim3 grid((unsigned)a.w.n_rows);
-  if (bf16 && e4m3) k_cache_write<D, true, true><<<grid, 256, 0, st>>>(a);
-  else if (bf16) k_cache_write<D, true, false><<<grid, 256, 0, st>>>(a);
-  else if (e4m3) k_cache_write<D, false, true><<<grid, 256, 0, st>>>(a);
-  else k_cache_write<D, false, false><<<grid, 256, 0, st>>>(a);
+cudaError_t launch(const WriteArgs& a, bool bf16, bool e4m3, cudaStream_t st) {
+  auto* kernel = bf16 ? (e4m3 ? k_cache_write<D, true, true> : k_cache_write<D, true, false>)
+                      : (e4m3 ? k_cache_write<D, false, true> : k_cache_write<D, false, false>);
+  return launch_following(kernel, (unsigned)a.w.n_rows, 256, 0, st, a);
 }
 
 }  // namespace
@@ -138,10 +137,9 @@ cudaError_t cache_write_launch(const CacheShape& S, const moe_cache_write_t& w, 
   a.gamma_offset = S.gamma_offset;
   a.eps = S.eps;
   a.status = status;
-  if (S.D == 64) launch<64>(a, S.bf16, S.e4m3, st);
-  else if (S.D == 128) launch<128>(a, S.bf16, S.e4m3, st);
-  else launch<256>(a, S.bf16, S.e4m3, st);
-  return cudaGetLastError();
+  if (S.D == 64) return launch<64>(a, S.bf16, S.e4m3, st);
+  if (S.D == 128) return launch<128>(a, S.bf16, S.e4m3, st);
+  return launch<256>(a, S.bf16, S.e4m3, st);
 }
 
 }  // namespace moe
