@@ -289,7 +289,7 @@ typedef struct {
 } moe_cache_config_t;
 
 /* A [rows][heads][head_dim] tensor: strides in elements, the innermost 1. The pointer is 16-byte aligned and the
- * strides are multiples of 8. */
+ * strides are multiples of 8, below 2^40 (rows) and 2^30 (heads). */
 typedef struct {
   const void *p;
   int64_t row_stride, head_stride;
@@ -336,7 +336,7 @@ MOE_API int moe_cache_plan(moe_cache_t *cache, const moe_cache_plan_t *plan, voi
  * pools are 16-byte aligned, their page strides in elements, multiples of head_dim (n_kv_heads * page_size * head_dim
  * when the pool is dense). With an e4m3 cache
  * k / k_scale[head] and v / v_scale[head] are rounded to e4m3, values past its range to its largest. Computed in
- * fp32 (angles in fp64), rounded once. q may be NULL together with q_out. Slots past the pool write nothing and are
+ * fp32 (an angle's whole turns exactly), rounded once. q may be NULL together with q_out. Slots past the pool write nothing and are
  * reported by moe_cache_get_status. Rows with the same slot race. */
 typedef struct {
   moe_rows_t q, k, v;                          /* [T][n_heads | n_kv_heads][head_dim] */
@@ -346,7 +346,7 @@ typedef struct {
   void *k_cache, *v_cache;
   int64_t k_page_stride, v_page_stride;
   const float *k_scale, *v_scale;              /* [n_kv_heads]: both given with an e4m3 cache, NULL otherwise */
-  int64_t n_rows;                              /* T >= 0 */
+  int64_t n_rows;                              /* T: 0..2^24 */
 } moe_cache_write_t;
 
 MOE_API int moe_cache_write(moe_cache_t *cache, const moe_cache_write_t *write, void *stream);

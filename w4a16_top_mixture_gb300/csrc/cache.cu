@@ -16,7 +16,7 @@ struct moe_cache {
   int dev = 0, num_sms = 0;
   uint8_t* mem = nullptr;                // one allocation: control words, the frequencies (1 KB), the workspace
   uint32_t *status = nullptr, *arrivals = nullptr;
-  double* turns = nullptr;
+  uint64_t* turns = nullptr;
   uint8_t* workspace = nullptr;          // of the attention: counts, partial results
   size_t workspace_bytes = 0;
   uint64_t timeout_ns = 500ull * 1000 * 1000;
@@ -62,11 +62,10 @@ int check_config(const moe_cache_config_t& c, CacheShape* S) {
 }
 
 bool aligned(const void* p, int n) { return p && ((uintptr_t)p & (n - 1)) == 0; }
-// strides are bounded so that no row's byte offset can pass 63 bits
+// strides are bounded so that no row's byte offset can pass 63 bits, and a head's number times its stride 31 or so
 bool rows_ok(const moe_rows_t& r) {
-  constexpr int64_t most = (int64_t)1 << 40;
-  return aligned(r.p, 16) && r.row_stride % 8 == 0 && r.head_stride % 8 == 0 && llabs(r.row_stride) < most &&
-         llabs(r.head_stride) < most;
+  return aligned(r.p, 16) && r.row_stride % 8 == 0 && r.head_stride % 8 == 0 && llabs(r.row_stride) < (int64_t)1 << 40 &&
+         llabs(r.head_stride) < (int64_t)1 << 30;
 }
 // a pool: 16-byte aligned, pages that do not overlap, whole rows of D apart
 bool pool_ok(const CacheShape& S, const void* p, int64_t page_stride) {
@@ -93,7 +92,7 @@ int check_plan(const moe_cache_config_t& cfg, const moe_cache_plan_t& p) {
   return MOE_OK;
 }
 int check_write(const CacheShape& S, const moe_cache_write_t& w) {
-  if (w.n_rows < 0 || w.n_rows > INT32_MAX) return MOE_ERR_INVALID_ARG;
+  if (w.n_rows < 0 || w.n_rows > (int64_t)1 << 24) return MOE_ERR_INVALID_ARG;
   if (w.n_rows == 0) return MOE_OK;
   if ((w.q.p != nullptr) != (w.q_out.p != nullptr) || (w.q.p && (!rows_ok(w.q) || !rows_ok(w.q_out))) ||
       !rows_ok(w.k) || !rows_ok(w.v) || ((uintptr_t)w.q_gamma & 15) || ((uintptr_t)w.k_gamma & 15) ||
@@ -132,9 +131,9 @@ extern "C" int moe_cache_create(const moe_cache_config_t* cfg, moe_cache_t** out
   c->num_sms = prop.multiProcessorCount;
   c->workspace_bytes = cache_attend_workspace(c->num_sms);
   const size_t bytes = CTL_WORDS * 4 + 1024 + c->workspace_bytes;
-  double turns[128];
+  uint64_t turns[128];
   for (int i = 0; i < S.rope / 2; ++i)
-    turns[i] = pow(cfg->rope_theta, -2.0 * i / S.rope) / (2.0 * 3.14159265358979323846);
+    turns[i] = (uint64_t)ldexp(pow(cfg->rope_theta, -2.0 * i / S.rope) / (2.0 * 3.14159265358979323846), 64);
   cudaError_t e = cache_plan_init();
   if (e == cudaSuccess) e = cudaMalloc(&c->mem, bytes);
   if (e == cudaSuccess) e = cudaMemset(c->mem, 0, bytes);
@@ -148,7 +147,7 @@ extern "C" int moe_cache_create(const moe_cache_config_t* cfg, moe_cache_t** out
   }
   c->status = (uint32_t*)c->mem;
   c->arrivals = c->status + 1;
-  c->turns = (double*)(c->mem + CTL_WORDS * 4);
+  c->turns = (uint64_t*)(c->mem + CTL_WORDS * 4);
   c->workspace = c->mem + CTL_WORDS * 4 + 1024;
   *out = c;
   return MOE_OK;
@@ -186,7 +185,7 @@ extern "C" int moe_cache_write(moe_cache_t* c, const moe_cache_write_t* w, void*
   const int r = check_write(c->S, *w);
   if (r != MOE_OK || w->n_rows == 0) return r;
   c->last_stream = (cudaStream_t)stream;
-  const cudaError_t e = cache_write_launch(c->S, *w, c->turns, c->status, (cudaStream_t)stream);
+  const cudaError_t e = cache_write_launch(c->S, *w, c->turns, c->status, c->num_sms, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_write");
 }
 

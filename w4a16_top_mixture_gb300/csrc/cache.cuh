@@ -32,8 +32,8 @@ struct CacheShape {
 cudaError_t cache_plan_init();           // once per device: the kernel's shared-memory limit
 cudaError_t cache_plan_launch(const CacheShape& S, const moe_cache_plan_t& p, uint32_t* arrivals, uint32_t* status,
                               int num_sms, cudaStream_t st);
-cudaError_t cache_write_launch(const CacheShape& S, const moe_cache_write_t& w, const double* turns,
-                               uint32_t* status, cudaStream_t st);
+cudaError_t cache_write_launch(const CacheShape& S, const moe_cache_write_t& w, const uint64_t* turns,
+                               uint32_t* status, int num_sms, cudaStream_t st);
 
 struct CacheAttendState {
   void* workspace;                       // cache_attend_workspace bytes, 16-byte aligned, zeroed once

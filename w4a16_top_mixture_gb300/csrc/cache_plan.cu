@@ -13,93 +13,113 @@ namespace {
 struct PlanArgs {
   moe_cache_plan_t p;
   int B, rows, page_log2, n_pages, max_pages;
+  bool in_place;
   uint32_t *arrivals, *status;
 };
 
 // exclusive scan of one value per thread over the block; *total: the sum. ws: 33 words
-__device__ __forceinline__ long long block_scan(long long v, long long* ws, long long* total) {
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* ws,
+                                                         unsigned long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  long long x = v;
+  unsigned long long x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) ws[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    long long s = lane < nw ? ws[lane] : 0;
-    const long long mine = s;
+    unsigned long long s = lane < nw ? ws[lane] : 0;
+    const unsigned long long mine = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, s, o);
       if (lane >= o) s += y;
     }
     if (lane < nw) ws[lane] = s - mine;
     if (lane == 31) ws[32] = s;
   }
   __syncthreads();
-  const long long r = ws[warp] + x - v;
   *total = ws[32];
-  __syncthreads();
-  return r;
+  return ws[warp] + x - v;
 }
 
+// EACH: requests of a thread, side by side, so that all its loads are on their way at once and two scans do
+template <int EACH>
 __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
   extern __shared__ int sm[];
   // per request: the row after its last, its cached tokens, its first page's place among the pages taken (-1: not
   // admitted; -2 - place: its first page's place among the pages given back)
   int *s_end = sm, *s_len = sm + a.B, *s_at = sm + 2 * a.B;
-  __shared__ long long ws[33];
-  __shared__ int s_refused;
+  __shared__ unsigned long long ws[2][33];
+  __shared__ int s_refused, s_taken;
   __shared__ bool s_last;
   const moe_cache_plan_t& p = a.p;
   const int ps = 1 << a.page_log2;
   const long long max_len = (long long)a.max_pages << a.page_log2;
   const int tid = threadIdx.x, nth = blockDim.x;
+  if (tid == 0) s_refused = s_taken = 0;
   follow_predecessor();
   int head = __ldcg(p.free_state), count = __ldcg(p.free_state + 1);
+  int len[EACH], nw[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int b = tid * EACH + i;
+    len[i] = b < a.B ? __ldcg(p.lengths + b) : 0;
+    nw[i] = b < a.B ? (p.new_tokens ? __ldcg(p.new_tokens + b) : 1) : 0;
+  }
   if (head < 0 || head >= a.n_pages || count < 0 || count > a.n_pages) {
     head = count = 0;
     if (tid == 0) atomicOr(a.status, CACHE_BAD_STATE);
   }
-  if (tid == 0) s_refused = 0;
-  __syncthreads();
-
-  long long row0 = 0, need0 = 0, back0 = 0, taken_mine = 0;
-  for (int b0 = 0; b0 < a.B; b0 += nth) {
-    const int b = b0 + tid;
-    const bool in = b < a.B;
-    const int len = in ? __ldcg(p.lengths + b) : 0;
-    const int nw = in ? (p.new_tokens ? __ldcg(p.new_tokens + b) : 1) : 0;
-    const bool good = len >= 0 && len <= max_len;
-    const bool done = nw < 0;
-    const long long n = nw > 0 ? nw : 0;
-    long long total;
-    const long long end = row0 + block_scan(n, ws, &total) + n;
-    row0 += total;
-    const int held = good ? (int)(((long long)len + ps - 1) >> a.page_log2) : 0;
-    const bool fits = in && good && !done && len + n <= max_len && end <= a.rows;
-    const int need = fits ? (int)((len + n + ps - 1) >> a.page_log2) - held : 0;
-    const int back = in && done ? held : 0;
-    const long long need_at = need0 + block_scan(need, ws, &total);
-    need0 += total;
-    const long long back_at = back0 + block_scan(back, ws, &total);
-    back0 += total;
-    const bool ok = fits && (need == 0 || need_at + need <= count);
-    if (ok) taken_mine += need;
+  // where each request's rows end
+  unsigned long long sum = 0, total;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) sum += nw[i] > 0 ? nw[i] : 0;
+  unsigned long long end = block_scan(sum, ws[0], &total);
+  // the pages it needs (low half: those that fit take at most n_rows / 16 + B) and gives back (high half)
+  int held[EACH], need[EACH];
+  bool fits[EACH];
+  sum = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int b = tid * EACH + i;
+    const long long n = nw[i] > 0 ? nw[i] : 0;
+    end += n;
+    const bool in = b < a.B, good = len[i] >= 0 && len[i] <= max_len;
+    held[i] = good ? (int)(((long long)len[i] + ps - 1) >> a.page_log2) : 0;
+    fits[i] = in && good && nw[i] >= 0 && len[i] + n <= max_len && end <= (unsigned long long)a.rows;
+    need[i] = fits[i] ? (int)((len[i] + n + ps - 1) >> a.page_log2) - held[i] : 0;
+    sum += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(in && nw[i] < 0 ? held[i] : 0) << 32;
     if (in) {
       s_end[b] = (int)(end < 0x7FFFFFFF ? end : 0x7FFFFFFF);
-      s_len[b] = len;
-      // a place among the pages is below n_pages (taken) or max_requests * max_pages clamped (given back)
-      s_at[b] = ok ? (int)(need ? need_at : 0)
-                   : done ? (int)(-2 - (back_at < 0x3FFFFFFF ? back_at : 0x3FFFFFFF)) : -1;
-      if (!ok && !done) atomicAdd(&s_refused, 1);
+      s_len[b] = len[i];
       if (!good) atomicOr(a.status, CACHE_BAD_LENGTH);
     }
   }
-  long long taken;
-  block_scan(taken_mine, ws, &taken);
+  unsigned long long at = block_scan(sum, ws[1], &total);
+  const uint32_t back_total = (uint32_t)(total >> 32);
+  int refused = 0, taken = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int b = tid * EACH + i;
+    if (b < a.B) {
+      const uint32_t need_at = (uint32_t)at, back_at = (uint32_t)(at >> 32);
+      const bool done = nw[i] < 0, ok = fits[i] && (need[i] == 0 || need_at + (uint32_t)need[i] <= (uint32_t)count);
+      s_at[b] = ok ? (need[i] ? (int)need_at : 0) : done ? (int)(-2 - (int)(back_at < 0x3FFFFFFFu ? back_at : 0x3FFFFFFFu)) : -1;
+      if (ok) taken += need[i];
+      else if (!done) ++refused;
+      at += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(done ? held[i] : 0) << 32;
+    }
+  }
+  refused = __reduce_add_sync(0xFFFFFFFFu, refused);
+  taken = __reduce_add_sync(0xFFFFFFFFu, taken);
+  if ((tid & 31) == 0) {
+    if (refused) atomicAdd(&s_refused, refused);
+    if (taken) atomicAdd(&s_taken, taken);
+  }
+  __syncthreads();
 
   // the pages: a warp to a request
   {
@@ -143,8 +163,10 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
     p.slots[r] = slot;
     p.positions[r] = pos;
   }
-  // what may lie in place of the inputs: written once every CTA has read them
-  if (gridDim.x > 1) {
+  // the first CTA writes the rest; what lies in place of inputs, the last to have read them
+  if (!a.in_place) {
+    if (blockIdx.x) return;
+  } else if (gridDim.x > 1) {
     __syncthreads();
     if (tid == 0) {
       __threadfence();
@@ -160,18 +182,21 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
   }
   if (tid == 0) {
     p.starts[0] = 0;
-    p.free_state_out[0] = (int)((uint32_t)(head + taken) % (uint32_t)a.n_pages);
-    const long long left = count - taken + back0;
+    p.free_state_out[0] = (int)((uint32_t)(head + s_taken) % (uint32_t)a.n_pages);
+    const long long left = (long long)count - s_taken + back_total;
     p.free_state_out[1] = (int)(left < a.n_pages ? left : a.n_pages);
     p.free_state_out[2] = s_refused;
-    if (gridDim.x > 1) *a.arrivals = 0;
+    if (a.in_place && gridDim.x > 1) *a.arrivals = 0;
   }
 }
 
 }  // namespace
 
 cudaError_t cache_plan_init() {
-  return cudaFuncSetAttribute(k_cache_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, CACHE_MAX_REQUESTS * 12);
+  cudaError_t e = cudaSuccess;
+  for (auto* k : {k_cache_plan<1>, k_cache_plan<2>, k_cache_plan<4>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CACHE_MAX_REQUESTS * 12);
+  return e;
 }
 
 cudaError_t cache_plan_launch(const CacheShape& S, const moe_cache_plan_t& p, uint32_t* arrivals, uint32_t* status,
@@ -183,13 +208,17 @@ cudaError_t cache_plan_launch(const CacheShape& S, const moe_cache_plan_t& p, ui
   a.page_log2 = S.page_log2;
   a.n_pages = S.n_pages;
   a.max_pages = S.max_pages;
+  a.in_place = p.lengths == p.lengths_out || p.free_state == p.free_state_out;
   a.arrivals = arrivals;
   a.status = status;
-  int threads = (a.B + 31) & ~31;
-  threads = threads < 128 ? 128 : threads > 1024 ? 1024 : threads;
+  const int each = a.B <= 1024 ? 1 : a.B <= 2048 ? 2 : 4;
+  int threads = ((a.B + each - 1) / each + 31) & ~31;
+  threads = threads < 128 ? 128 : threads;
+  // a CTA for every row of each thread: rows are independent, and the scans cost every CTA alike
   const long long want = ((long long)a.rows + threads - 1) / threads;
   const int grid = (int)(want < 1 ? 1 : want > num_sms ? num_sms : want);
-  return launch_following(k_cache_plan, grid, threads, (size_t)a.B * 12, st, a);
+  return launch_following(each == 1 ? k_cache_plan<1> : each == 2 ? k_cache_plan<2> : k_cache_plan<4>, grid, threads,
+                          (size_t)a.B * 12, st, a);
 }
 
 }  // namespace moe
