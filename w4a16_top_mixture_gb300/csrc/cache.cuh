@@ -83,10 +83,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the low 
   else *reinterpret_cast<__half2*>(&r) = __floats2half2_rn(a, b);
   return r;
 }
-// two e4m3 codes (the lower one first) as a pair of fp16: exact
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
-  return (uint32_t)r.x | (uint32_t)r.y << 16;
+// four e4m3 codes as two pairs of fp16, the lower ones first: exact, NaN kept
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 
 }  // namespace moe

@@ -174,9 +174,11 @@ __device__ __forceinline__ void add_values(float (&o)[S::MD][S::NT][4], uint32_t
         ldsm4_t(v, (from ^ (md << 4)) + kt * S::GROUP_BYTES);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t y = __byte_perm(v[i], 0, 0x3120);
-          x[i][0] = e4m3x2_to_f16x2((uint16_t)y) & keep[i];
-          x[i][1] = e4m3x2_to_f16x2((uint16_t)(y >> 16)) & keep[i];
+          e4m3x4_to_f16x4(__byte_perm(v[i], 0, 0x3120), x[i][0], x[i][1]);
+          if (EDGE) {
+            x[i][0] &= keep[i];
+            x[i][1] &= keep[i];
+          }
         }
 #pragma unroll
         for (int nt = 0; nt < S::NT; ++nt) {
@@ -738,16 +740,14 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           if (S::E4M3) {
 #pragma unroll
             for (int c = 0; c < S::RB / 16; c += 2) {
-              uint32_t k[4];
+              uint32_t k[4], lo[4], hi[4];
               ldsm4(k, (from ^ (c % PER << 4)) + c / PER * (16 * S::CB));
 #pragma unroll
+              for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(k[i], lo[i], hi[i]);
+#pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma16816<false>(s[mt][nt], e4m3x2_to_f16x2((uint16_t)k[0]), e4m3x2_to_f16x2((uint16_t)k[1]),
-                                e4m3x2_to_f16x2((uint16_t)(k[0] >> 16)), e4m3x2_to_f16x2((uint16_t)(k[1] >> 16)),
-                                q[c][nt][0], q[c][nt][1]);
-                mma16816<false>(s2[mt][nt], e4m3x2_to_f16x2((uint16_t)k[2]), e4m3x2_to_f16x2((uint16_t)k[3]),
-                                e4m3x2_to_f16x2((uint16_t)(k[2] >> 16)), e4m3x2_to_f16x2((uint16_t)(k[3] >> 16)),
-                                q[c + 1][nt][0], q[c + 1][nt][1]);
+                mma16816<false>(s[mt][nt], lo[0], lo[1], hi[0], hi[1], q[c][nt][0], q[c][nt][1]);
+                mma16816<false>(s2[mt][nt], lo[2], lo[3], hi[2], hi[3], q[c + 1][nt][0], q[c + 1][nt][1]);
               }
             }
           } else {
