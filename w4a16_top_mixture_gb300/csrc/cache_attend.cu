@@ -15,6 +15,8 @@
 //   O be kept once.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "cache.cuh"
 #include "ptx.cuh"
 
@@ -1065,25 +1067,30 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-cudaError_t encode_fn(EncodeFn* out) {
-  static EncodeFn fn = nullptr;
-  if (!fn) {
+using ReplaceFn = CUresult (*)(CUtensorMap*, void*);
+
+template <class F>
+cudaError_t driver_fn(const char* name, std::atomic<F>& known, F* out) {
+  F f = known.load(std::memory_order_relaxed);
+  if (!f) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    const cudaError_t e = cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q);
     if (e != cudaSuccess) return e;
     if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
-    fn = reinterpret_cast<EncodeFn>(p);
+    known.store(f = reinterpret_cast<F>(p), std::memory_order_relaxed);
   }
-  *out = fn;
+  *out = f;
   return cudaSuccess;
 }
+std::atomic<EncodeFn> g_encode{nullptr};
+std::atomic<ReplaceFn> g_replace{nullptr};
 
 // a pool as rows of a head's D elements: [page][head, token][d], copied 16 tokens x CB bytes at a time
 template <class S>
 cudaError_t pool_map(const CacheShape& c, const void* pool, int64_t page_stride, CUtensorMap* m) {
   EncodeFn fn;
-  const cudaError_t e = encode_fn(&fn);
+  const cudaError_t e = driver_fn("cuTensorMapEncodeTiled", g_encode, &fn);
   if (e != cudaSuccess) return e;
   const int es = S::E4M3 ? 1 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)S::D, (cuuint64_t)c.Hkv << c.page_log2, (cuuint64_t)c.n_pages};
@@ -1103,18 +1110,28 @@ cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
   static_assert(S::MISC + 1024 + CACHE_MAX_REQUESTS * 4 + S::TEAMS * 2 * S::STAGE <= SMEM_PER_CTA, "the ring has two stages at least");
   CUtensorMap km, vm;
   cudaError_t e = pool_map<S>(c, A.a.k_cache, A.a.k_page_stride, &km);
-  if (e == cudaSuccess) e = pool_map<S>(c, A.a.v_cache, A.a.v_page_stride, &vm);
+  if (e == cudaSuccess && A.a.v_page_stride == A.a.k_page_stride) {
+    // the same map at another address: half the host's time for two
+    ReplaceFn replace;
+    e = driver_fn("cuTensorMapReplaceAddress", g_replace, &replace);
+    vm = km;
+    if (e == cudaSuccess && replace(&vm, (void*)A.a.v_cache) != CUDA_SUCCESS) e = cudaErrorInvalidValue;
+  } else if (e == cudaSuccess) {
+    e = pool_map<S>(c, A.a.v_cache, A.a.v_page_stride, &vm);
+  }
   if (e != cudaSuccess) return e;
   A.head_tiles = (A.group + S::NH - 1) / S::NH;
   const int other = S::MISC + 1024 + A.B * 4;
   const int n = (SMEM_PER_CTA - other) / (S::TEAMS * S::STAGE);
   A.n_stages = n > 16 ? 16 : n;
-  static bool ready[64] = {};
+  // the kernel's shared-memory limit, once per device
+  static std::atomic<uint64_t> ready{0};
   int dev = 0;
   e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev < 0 || dev >= 64 || !ready[dev])) {
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (e == cudaSuccess && !(ready.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(k_cache_attend<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_PER_CTA);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev] = true;
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   }
   if (e != cudaSuccess) return e;
   return launch_following(k_cache_attend<S>, ctas, S::THREADS, other + S::TEAMS * A.n_stages * S::STAGE, st, A, km, vm);

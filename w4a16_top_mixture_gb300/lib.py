@@ -469,15 +469,16 @@ class PagedCache:
 
     def _rows(self, t, heads, rows):
         """(pointer, row stride, head stride) of a [rows, heads, head_dim] tensor of the activations' type."""
-        if t.dtype is not self.dtype or t.shape != (rows, heads, self.head_dim) or t.get_device() != self._dev or t.stride(2) != 1:
+        r, h, d = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if d != 1 or t.dtype is not self.dtype or t.shape != (rows, heads, self.head_dim) or t.get_device() != self._dev:
             raise ValueError(f"want {self.dtype} [{rows}, {heads}, {self.head_dim}] on {self.device}, innermost stride 1; "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-        return t.data_ptr(), t.stride(0) if rows > 1 else 0, t.stride(1) if heads > 1 else 0
+        return t.data_ptr(), r if rows > 1 else 0, h if heads > 1 else 0
 
     def _vector(self, t, n, dtype):
-        if t.dtype is not dtype or t.shape != (n,) or t.get_device() != self._dev or not t.is_contiguous():
-            raise ValueError(f"want a contiguous {dtype} [{n}] on {self.device}; got {t.dtype} {tuple(t.shape)} on {t.device}")
-        return t.data_ptr()
+        if t.dtype is dtype and t.shape == (n,) and t.get_device() == self._dev and t.is_contiguous():
+            return t.data_ptr()
+        raise ValueError(f"want a contiguous {dtype} [{n}] on {self.device}; got {t.dtype} {tuple(t.shape)} on {t.device}")
 
     def _table(self, t, rows):
         if (t.dtype is not self._i32 or t.shape != (rows, self.max_pages) or t.get_device() != self._dev
@@ -513,16 +514,20 @@ class PagedCache:
         """Block tables and slot maps of a step (moe_cache_plan): lengths, new_tokens int32 [B] (new_tokens may be None:
         one each), tables int32 [B, max_pages] and free_pages int32 [n_pages] (both updated in place), free_state
         int32 [3]. out: a CachePlan to write into, whose lengths and free_state may be the inputs themselves."""
-        B = lengths.shape[0]
+        B, i32, vec = lengths.shape[0], self._i32, self._vector
         if out is None:
-            out = CachePlan(*self._empty((2 * n_rows + 2 * B + 4,), self._i32, stream).split(
-                (n_rows, n_rows, B + 1, B, 3)))
-        i32 = self._i32
+            buf = self._empty((2 * n_rows + 2 * B + 4,), i32, stream)
+            out = CachePlan._make(buf.split((n_rows, n_rows, B + 1, B, 3)))
+            slots = buf.data_ptr()
+            positions, starts = slots + 4 * n_rows, slots + 8 * n_rows
+            lengths_out = starts + 4 * (B + 1)
+            state_out = lengths_out + 4 * B
+        else:
+            slots, positions = vec(out.slots, n_rows, i32), vec(out.positions, n_rows, i32)
+            starts, lengths_out, state_out = vec(out.starts, B + 1, i32), vec(out.lengths, B, i32), vec(out.free_state, 3, i32)
         args = CACHE_PLAN.pack(
-            self._vector(lengths, B, i32), self._vector(new_tokens, B, i32) if new_tokens is not None else 0,
-            *self._table(tables, B), self._vector(free_pages, self.n_pages, i32), self._vector(free_state, 3, i32),
-            self._vector(out.free_state, 3, i32), self._vector(out.lengths, B, i32), self._vector(out.starts, B + 1, i32),
-            self._vector(out.slots, n_rows, i32), self._vector(out.positions, n_rows, i32), B, n_rows)
+            vec(lengths, B, i32), vec(new_tokens, B, i32) if new_tokens is not None else 0, *self._table(tables, B),
+            vec(free_pages, self.n_pages, i32), vec(free_state, 3, i32), state_out, lengths_out, starts, slots, positions, B, n_rows)
         self._call(self.lib.moe_cache_plan, args, stream, "moe_cache_plan")
         return out
 
@@ -531,18 +536,22 @@ class PagedCache:
         """RMSNorm and rotary embedding of q and k, and k, v into the pools by slot (moe_cache_write). q [T, n_heads,
         head_dim] (or None), k and v [T, n_kv_heads, head_dim], views of a projection's output among them; returns
         the new q (q_out, which may be q itself)."""
-        T = k.shape[0]
+        T, heads, i32 = k.shape[0], self.n_heads, self._i32
+        out_rows = (0, 0, 0)
         if q is not None and q_out is None:
-            q_out = self._empty((T, self.n_heads, self.head_dim), self.dtype, stream)
+            q_out = self._empty((T, heads, self.head_dim), self.dtype, stream)
+            out_rows = q_out.data_ptr(), heads * self.head_dim, self.head_dim
+        elif q is not None:
+            out_rows = self._rows(q_out, heads, T)
         kc, ks = self._pool(k_cache)
         vc, vs = self._pool(v_cache)
         args = CACHE_WRITE.pack(
-            *(self._rows(q, self.n_heads, T) if q is not None else (0, 0, 0)), *self._rows(k, self.n_kv_heads, T),
-            *self._rows(v, self.n_kv_heads, T), *(self._rows(q_out, self.n_heads, T) if q is not None else (0, 0, 0)),
+            *(self._rows(q, heads, T) if q is not None else (0, 0, 0)), *self._rows(k, self.n_kv_heads, T),
+            *self._rows(v, self.n_kv_heads, T), *out_rows,
             self._vector(q_gamma, self.head_dim, self.dtype) if q_gamma is not None else 0,
             self._vector(k_gamma, self.head_dim, self.dtype) if k_gamma is not None else 0,
-            self._vector(positions, T, self._i32), self._vector(slots, T, self._i32), kc, vc, ks, vs,
-            *self._scales(k_scale, v_scale), T)
+            self._vector(positions, T, i32), self._vector(slots, T, i32), kc, vc, ks, vs,
+            *(self._scales(k_scale, v_scale) if k_scale is not None or v_scale is not None else (0, 0)), T)
         self._call(self.lib.moe_cache_write, args, stream, "moe_cache_write")
         return q_out
 
@@ -551,15 +560,19 @@ class PagedCache:
         """Attention of one token of each request over its pages (moe_cache_attend): q [B, n_heads, head_dim], tables
         int32 [B, max_pages], lengths int32 [B], gate None or like q (the output is multiplied by its sigmoid), scale
         1 / sqrt(head_dim) unless given."""
-        B = q.shape[0]
+        B, heads = q.shape[0], self.n_heads
         if out is None:
-            out = self._empty((B, self.n_heads, self.head_dim), self.dtype, stream)
+            out = self._empty((B, heads, self.head_dim), self.dtype, stream)
+            out_rows = out.data_ptr(), heads * self.head_dim, self.head_dim
+        else:
+            out_rows = self._rows(out, heads, B)
         kc, ks = self._pool(k_cache)
         vc, vs = self._pool(v_cache)
         args = CACHE_ATTEND.pack(
-            *self._rows(q, self.n_heads, B), *(self._rows(gate, self.n_heads, B) if gate is not None else (0, 0, 0)),
-            *self._rows(out, self.n_heads, B), *self._table(tables, B), self._vector(lengths, B, self._i32), kc, vc, ks, vs,
-            *self._scales(k_scale, v_scale), B, scale if scale is not None else self.head_dim ** -0.5)
+            *self._rows(q, heads, B), *(self._rows(gate, heads, B) if gate is not None else (0, 0, 0)), *out_rows,
+            *self._table(tables, B), self._vector(lengths, B, self._i32), kc, vc, ks, vs,
+            *(self._scales(k_scale, v_scale) if k_scale is not None or v_scale is not None else (0, 0)), B,
+            scale if scale is not None else self.head_dim ** -0.5)
         self._call(self.lib.moe_cache_attend, args, stream, "moe_cache_attend")
         return out
 
