@@ -23,7 +23,7 @@
 namespace moe {
 namespace {
 
-constexpr int SHORT = 4;                          // units of an item that is not split without need
+constexpr int SHORT = 5;                          // units of an item that is not split without need
 constexpr int GROUP = 10, FLAT = 20;              // CTAs whose parts are joined first; from FLAT + 1 parts on
 constexpr int MAX_CTAS = 1024, COUNT_WORDS = MAX_CTAS + MAX_CTAS / GROUP * 2;    // of the workspace
 constexpr int PART_MAX = 16 * 256 + 32;           // floats of the largest part
@@ -58,7 +58,7 @@ struct Shape {
   static constexpr int GPS = 16384 / (16 * RB) < KT ? 16384 / (16 * RB) : KT;   // 16-token groups of a stage
   static constexpr int GROUP_BYTES = 16 * RB, STAGE = GPS * GROUP_BYTES;
   static constexpr int MD = D / 16 / WARPS;                 // 16-row tiles of O per warp
-  static constexpr int EXTRA = 65536 / (2 * TN * RB) > 1 ? 65536 / (2 * TN * RB) : 1;   // units of an item, see there
+  static constexpr int EXTRA = RB >= 128 ? 2 : 4;           // units of an item, see the division of the work
   static constexpr int PP = TN + 8;                         // pitch of P: rows of 8 fall on different banks
   static constexpr int QP = D + 8;                          // pitch of queries and gates
   static constexpr int PART = NH * D + 2 * NH;              // floats of a partial result: O, maxima, sums
@@ -405,19 +405,18 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = A.Hkv * A.head_tiles;
 
-  if (tid == 0) {
-    for (int s = 0; s < TEAMS * 16; ++s) {
-      mbar_init(&full0[s], 1);
-      mbar_init(&empty0[s], WARPS);
-    }
+  if (tid < TEAMS * 16) {
+    mbar_init(&full0[tid], 1);
+    mbar_init(&empty0[tid], WARPS);
+  } else if (tid == TEAMS * 16) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&rows_full[s], 1);
       mbar_init(&rows_empty[s], TEAMS * WARPS);
     }
     mbar_init(join_full, 1);
-    fence_mbar_init();
     s_flags[0] = s_flags[1] = s_flags[2] = s_flags[3] = 0;
   }
+  if (tid <= TEAMS * 16) fence_mbar_init();
   follow_predecessor();
   // lengths and the running number of tiles: a thread's requests lie side by side, so that all its loads are on their way
   // at once
@@ -994,7 +993,6 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     s_flags[3] = 1;
     s_flags[1] = complete(A, split[0], head_before);
   }
-  __threadfence();
   if (team) {
     named_arrive(3, TEAMS * MATH);
     return;
@@ -1003,7 +1001,11 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   const int gi = blockIdx.x / GROUP;
   if (lane == 0 && warp < 2) {
     const Split sp = warp ? split[1] : split[0];
-    if (sp.b >= 0 && !(warp == 0 && s_flags[3])) s_flags[1 + warp] = complete(A, sp, arrive(A, sp));
+    if (sp.b >= 0 && !(warp == 0 && s_flags[3])) {
+      __threadfence();               // the barrier's threads' parts before the count, and the others' parts after it
+      s_flags[1 + warp] = complete(A, sp, arrive(A, sp));
+    }
+    __threadfence();
   }
   team_barrier<S>(team);
   Joined<S> y;
@@ -1013,7 +1015,6 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     if (!s_flags[1 + i]) continue;
-    __threadfence();
     const Split sp = i ? split[1] : split[0];
     const int kvh = sp.h / A.head_tiles, h_in = (sp.h % A.head_tiles) * NH;
     const int nh = A.group - h_in < NH ? A.group - h_in : NH;
@@ -1046,16 +1047,16 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       const int g0 = sp.c0 / GROUP, g1 = sp.c1 / GROUP;
       join(A.parts, gi == g0 ? sp.c0 : gi * GROUP, gi == g1 ? sp.c1 : gi * GROUP + GROUP - 1, sp.c0);
       y.keep(A.group_parts + ((long long)gi * 2 + (gi == g0)) * S::PART, tid);
-      __threadfence();
       team_barrier<S>(team);
       if (tid == 0) {
+        __threadfence();
         const bool all = atomicAdd(&A.counts[sp.c0], 1u) == (uint32_t)(g1 - g0);
         if (all) A.counts[sp.c0] = 0;
         s_flags[1 + i] = all;
+        __threadfence();
       }
       team_barrier<S>(team);
       if (!s_flags[1 + i]) continue;
-      __threadfence();
       y.fetch_gates(A, sp.b, h0, nh, tid);
       join(A.group_parts, g0, g1, g0);
     }
