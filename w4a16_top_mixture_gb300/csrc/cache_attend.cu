@@ -240,28 +240,21 @@ __device__ __forceinline__ bool complete(const AttendArgs& A, const Split& sp, i
   return true;
 }
 
-// The joined parts of a split item: NH * D / 4 groups of four d, PER of them to a thread.
+// The joined parts of a split item: NH * D / 4 groups of four d, PER of them to each math thread.
 template <class S>
 struct Joined {
-  static constexpr int FEW = S::NT == 1 ? 4 : 2;
-  static constexpr int NH = S::NH, D = S::D, VECS = NH * D / 4, PER = (VECS + S::MATH - 1) / S::MATH;
-  static_assert(VECS % S::MATH == 0, "whole vectors for each thread");
+  static constexpr int NH = S::NH, D = S::D, VECS = NH * D / 4, STEP = S::TEAMS * S::MATH, PER = (VECS + STEP - 1) / STEP;
+  static constexpr int FEW = 16 / PER < 8 ? 16 / PER : 8;
+  static_assert(VECS % STEP == 0 || PER == 1, "whole vectors for each thread, or one for some");
   float4 y[PER];
-  float sum[PER];
+  float sum[PER], top[PER];
   uint2 gate[PER];
 
-  float top;               // of head tid % NH
-
-  __device__ __forceinline__ void clear() {
-    top = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      sum[e] = 0.f;
-    }
-  }
-  // up to FEW parts, straight from L2 with every load on its way at once
+  __device__ __forceinline__ static bool mine(int tid) { return VECS >= STEP || tid < VECS; }
+  // Part i of ia .. ib lies in slot 2 i + (i == i0): i0 is where the item begins. Up to FEW of them come straight from L2,
+  // every load on its way at once; the order of the sum is that of the parts.
   __device__ __forceinline__ void few(const float* parts, int ia, int ib, int i0, int tid) {
+    if (!mine(tid)) return;
     float4 v[FEW][PER];
     float m[FEW][PER], l[FEW][PER];
 #pragma unroll
@@ -270,97 +263,87 @@ struct Joined {
       const float* p = parts + ((long long)i * 2 + (i == i0 ? 1 : 0)) * S::PART;
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
-        const int at4 = (e * S::MATH + tid) * 4, he = at4 / D;
+        const int at4 = (e * STEP + tid) * 4, h = at4 / D;
         v[k][e] = __ldcg(reinterpret_cast<const float4*>(p + at4));
-        m[k][e] = __ldcg(p + NH * D + he);
-        l[k][e] = __ldcg(p + NH * D + NH + he);
+        m[k][e] = __ldcg(p + NH * D + h);
+        l[k][e] = __ldcg(p + NH * D + NH + h);
       }
     }
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
       float x = m[0][e];
 #pragma unroll
-      for (int k = 1; k < FEW; ++k) x = fmaxf(x, m[k][e]);
+      for (int k = 1; k < FEW; ++k) x = fmaxf(x, m[k][e]);     // the last part again does not matter
       const float base = x == -INFINITY ? 0.f : x;
-      y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      sum[e] = 0.f;
+      top[e] = x;
 #pragma unroll
-      for (int k = 0; k < FEW; ++k) {
-        if (ia + k > ib) break;
-        const float w = exp2_fast(m[k][e] - base);
-        sum[e] = fmaf(l[k][e], w, sum[e]);
-        y[e].x = fmaf(v[k][e].x, w, y[e].x);
-        y[e].y = fmaf(v[k][e].y, w, y[e].y);
-        y[e].z = fmaf(v[k][e].z, w, y[e].z);
-        y[e].w = fmaf(v[k][e].w, w, y[e].w);
+      for (int k = 0; k < FEW; ++k)
+        if (ia + k <= ib) put(e, v[k][e], l[k][e], exp2_fast(m[k][e] - base));
+    }
+  }
+  // n further parts, from shared memory. All math warps, in step.
+  __device__ __forceinline__ void add(const float* parts, int n, int tid) {
+    if (!mine(tid)) return;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int at4 = (e * STEP + tid) * 4, h = at4 / D;
+      float x = top[e];
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) x = fmaxf(x, parts[k * S::PART + NH * D + h]);
+      const float base = x == -INFINITY ? 0.f : x, c = exp2_fast(top[e] - base);
+      top[e] = x;
+      sum[e] *= c;
+      y[e] = make_float4(y[e].x * c, y[e].y * c, y[e].z * c, y[e].w * c);
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float* p = parts + k * S::PART;
+        put(e, *reinterpret_cast<const float4*>(p + at4), p[NH * D + NH + h], exp2_fast(p[NH * D + h] - base));
       }
     }
   }
-  // n further parts, from shared memory; the order of the sum is that of the parts. The first team, in step.
-  // s_max: [WARPS][NH], s_w: [n][NH] weights beside weighted sums, and [NH] factors of what is there already
-  __device__ __forceinline__ void add(const float* parts, int n, float* s_max, float2* s_w, int tid) {
-    const int h = tid % NH, lane = tid & 31, warp = tid >> 5;
-    float x = top;
-    for (int k = tid / NH; k < n; k += S::MATH / NH) x = fmaxf(x, parts[k * S::PART + NH * D + h]);
-#pragma unroll
-    for (int w = NH; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
-    if (lane < NH) s_max[warp * NH + h] = x;
-    team_barrier<S>(0);
-#pragma unroll
-    for (int w = 0; w < S::WARPS; ++w) x = fmaxf(x, s_max[w * NH + h]);
-    const float base = x == -INFINITY ? 0.f : x;
-    for (int k = tid / NH; k < n; k += S::MATH / NH) {
-      const float w = exp2_fast(parts[k * S::PART + NH * D + h] - base);
-      s_w[k * NH + h] = make_float2(w, w * parts[k * S::PART + NH * D + NH + h]);
-    }
-    if (tid < NH) s_w[n * NH + h].x = exp2_fast(top - base);
-    top = x;
-    team_barrier<S>(0);
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int at4 = (e * S::MATH + tid) * 4, he = at4 / D;
-      const float c = s_w[n * NH + he].x;
-      y[e] = make_float4(y[e].x * c, y[e].y * c, y[e].z * c, y[e].w * c);
-      sum[e] *= c;
+      y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      sum[e] = 0.f;
+      top[e] = -INFINITY;
     }
-#pragma unroll 4
-    for (int k = 0; k < n; ++k)
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        const int at4 = (e * S::MATH + tid) * 4, he = at4 / D;
-        const float4 v = *reinterpret_cast<const float4*>(parts + k * S::PART + at4);
-        const float2 w = s_w[k * NH + he];
-        y[e].x = fmaf(v.x, w.x, y[e].x);
-        y[e].y = fmaf(v.y, w.x, y[e].y);
-        y[e].z = fmaf(v.z, w.x, y[e].z);
-        y[e].w = fmaf(v.w, w.x, y[e].w);
-        sum[e] += w.y;
-      }
+  }
+  __device__ __forceinline__ void put(int e, float4 v, float l, float w) {
+    sum[e] = fmaf(l, w, sum[e]);
+    y[e].x = fmaf(v.x, w, y[e].x);
+    y[e].y = fmaf(v.y, w, y[e].y);
+    y[e].z = fmaf(v.z, w, y[e].z);
+    y[e].w = fmaf(v.w, w, y[e].w);
   }
   // as a part of its own
   __device__ __forceinline__ void keep(float* part, int tid) {
+    if (!mine(tid)) return;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int at4 = (e * S::MATH + tid) * 4;
+      const int at4 = (e * STEP + tid) * 4;
       *reinterpret_cast<float4*>(part + at4) = y[e];
-      if (at4 % D == 0) part[NH * D + NH + at4 / D] = sum[e];
+      if (at4 % D == 0) {
+        part[NH * D + at4 / D] = top[e];
+        part[NH * D + NH + at4 / D] = sum[e];
+      }
     }
-    if (tid < NH) part[NH * D + tid] = top;
   }
   // the gates, on their way while the parts are joined
   __device__ __forceinline__ void fetch_gates(const AttendArgs& A, int b, int h0, int nh, int tid) {
-    if (!A.a.gate.p) return;
+    if (!A.a.gate.p || !mine(tid)) return;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int at4 = (e * S::MATH + tid) * 4, h = at4 / D, d = at4 % D;
+      const int at4 = (e * STEP + tid) * 4, h = at4 / D, d = at4 % D;
       gate[e] = h < nh ? __ldcg(reinterpret_cast<const uint2*>(rows_at(A.a.gate, b, h0 + h, d))) : make_uint2(0, 0);
     }
   }
   // as the output
   __device__ __forceinline__ void finish(const AttendArgs& A, int b, int h0, int nh, float vs, int tid) {
+    if (!mine(tid)) return;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int at4 = (e * S::MATH + tid) * 4, h = at4 / D, d = at4 % D;
+      const int at4 = (e * STEP + tid) * 4, h = at4 / D, d = at4 % D;
       if (h >= nh) continue;
       const float f = vs / sum[e];
       float x[4] = {y[e].x * f, y[e].y * f, y[e].z * f, y[e].w * f};
@@ -390,9 +373,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   uint64_t* const empty0 = full0 + 32;
   uint64_t* const rows_full = empty0 + 32;            // [2]: an item's queries and gates, by turns
   uint64_t* const rows_empty = rows_full + 2;
-  uint64_t* const join_full = rows_empty + 2;        // parts, when the ring is done with
-  volatile int* const s_flags = (int*)(join_full + 1);    // 0: a wait ran out; 1, 2: last to arrive; 3: the first has
-  int* const s_scan = (int*)(join_full + 1) + 4;     // [THREADS / 32]
+  uint64_t* const join_full = rows_empty + 2;        // parts, when the rings are done with
+  volatile int* const s_flags = (int*)(join_full + 2);    // 0: a wait ran out; 1, 2: last to arrive; 3: the first has
+  int* const s_scan = (int*)(join_full + 2) + 4;     // [THREADS / 32]
   int* const s_place = s_scan + 32;                  // [3]
   uint16_t* const s_q = (uint16_t*)(misc + 1024);    // [2][2][NH][QP]: by turns, queries and gates
   uint16_t* const s_p0 = s_q + 4 * NH * QP;          // [TEAMS][NH][PP]
@@ -993,12 +976,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     s_flags[3] = 1;
     s_flags[1] = complete(A, split[0], head_before);
   }
-  if (team) {
-    named_arrive(3, TEAMS * MATH);
-    return;
-  }
   named_bar(3, TEAMS * MATH);
-  const int gi = blockIdx.x / GROUP;
   if (lane == 0 && warp < 2) {
     const Split sp = warp ? split[1] : split[0];
     if (sp.b >= 0 && !(warp == 0 && s_flags[3])) {
@@ -1007,47 +985,51 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     }
     __threadfence();
   }
-  team_barrier<S>(team);
+  named_bar(3, TEAMS * MATH);
   Joined<S> y;
   uint32_t join_phase = 0;
-  const int fit = TEAMS * A.n_stages * S::STAGE / (S::PART * 4);
-  const int at_once = fit < PP / 4 - 1 ? fit : PP / 4 - 1;      // the weights lie where P did
+  auto join = [&](const float* parts, int ia, int ib, int i0) {
+    y.clear();
+    if (ib - ia < Joined<S>::FEW) {
+      y.few(parts, ia, ib, i0, tid);
+      return;
+    }
+    // more than FEW by bulk copies, to where the rings were
+    static_assert(TEAMS * 2 * S::STAGE >= S::PART * 4, "the rings hold a part at least");
+    const int at_once = TEAMS * A.n_stages * S::STAGE / (S::PART * 4);
+    for (int k0 = ia; k0 <= ib; k0 += at_once) {
+      const int n = ib - k0 + 1 < at_once ? ib - k0 + 1 : at_once;
+      named_bar(3, TEAMS * MATH);                // what lay there has been read
+      if (warp == 0) {
+        if (lane == 0) mbar_expect_tx(join_full, n * S::PART * 4);
+        __syncwarp();
+        fence_proxy_async_global();
+        for (int k = lane; k < n; k += 32)
+          bulk_g2s(ring + k * S::PART * 4, parts + ((long long)(k0 + k) * 2 + (k0 + k == i0 ? 1 : 0)) * S::PART,
+                   S::PART * 4, join_full);
+      }
+      wait_full(join_full, join_phase);
+      if (s_flags[0]) mbar_wait(join_full, join_phase, A.timeout_ns);      // lost; the copies must not outlive the CTA
+      join_phase ^= 1;
+      y.add((const float*)ring, n, tid);
+    }
+  };
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     if (!s_flags[1 + i]) continue;
     const Split sp = i ? split[1] : split[0];
-    const int kvh = sp.h / A.head_tiles, h_in = (sp.h % A.head_tiles) * NH;
+    const int kvh = sp.h / A.head_tiles, h_in = (sp.h % A.head_tiles) * NH, h0 = kvh * A.group + h_in;
     const int nh = A.group - h_in < NH ? A.group - h_in : NH;
     const float vs = S::E4M3 ? __ldcg(a.v_scale + kvh) : 1.f;
-    auto join = [&](const float* parts, int ia, int ib, int i0) {
-      y.clear();
-      for (int k0 = ia; k0 <= ib; k0 += at_once) {
-        const int n = ib - k0 + 1 < at_once ? ib - k0 + 1 : at_once;
-        team_barrier<S>(team);                       // what the ring held has been read
-        if (tid == 0) {
-          fence_proxy_async_global();
-          mbar_expect_tx(join_full, n * S::PART * 4);
-          for (int k = 0; k < n; ++k)
-            bulk_g2s(ring + k * S::PART * 4, parts + ((long long)(k0 + k) * 2 + (k0 + k == i0 ? 1 : 0)) * S::PART,
-                     S::PART * 4, join_full);
-        }
-        wait_full(join_full, join_phase);
-        if (s_flags[0]) mbar_wait(join_full, join_phase, A.timeout_ns);   // lost; the copies must not outlive the CTA
-        join_phase ^= 1;
-        y.add((const float*)ring, n, s_max, reinterpret_cast<float2*>(s_p), tid);
-      }
-    };
-    const int h0 = kvh * A.group + h_in;
+    y.fetch_gates(A, sp.b, h0, nh, tid);
     if (sp.c1 - sp.c0 < FLAT) {
-      y.fetch_gates(A, sp.b, h0, nh, tid);
-      if (sp.c1 - sp.c0 < Joined<S>::FEW) y.few(A.parts, sp.c0, sp.c1, sp.c0, tid);
-      else join(A.parts, sp.c0, sp.c1, sp.c0);
+      join(A.parts, sp.c0, sp.c1, sp.c0);
     } else {
       // many parts: each GROUP of CTAs joins its own, and the last group to do so the groups'
-      const int g0 = sp.c0 / GROUP, g1 = sp.c1 / GROUP;
+      const int g0 = sp.c0 / GROUP, g1 = sp.c1 / GROUP, gi = blockIdx.x / GROUP;
       join(A.parts, gi == g0 ? sp.c0 : gi * GROUP, gi == g1 ? sp.c1 : gi * GROUP + GROUP - 1, sp.c0);
       y.keep(A.group_parts + ((long long)gi * 2 + (gi == g0)) * S::PART, tid);
-      team_barrier<S>(team);
+      named_bar(3, TEAMS * MATH);
       if (tid == 0) {
         __threadfence();
         const bool all = atomicAdd(&A.counts[sp.c0], 1u) == (uint32_t)(g1 - g0);
@@ -1055,9 +1037,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         s_flags[1 + i] = all;
         __threadfence();
       }
-      team_barrier<S>(team);
+      named_bar(3, TEAMS * MATH);
       if (!s_flags[1 + i]) continue;
-      y.fetch_gates(A, sp.b, h0, nh, tid);
       join(A.group_parts, g0, g1, g0);
     }
     y.finish(A, sp.b, h0, nh, vs, tid);
