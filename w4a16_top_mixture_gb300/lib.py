@@ -481,19 +481,24 @@ class PagedCache:
         raise ValueError(f"want a contiguous {dtype} [{n}] on {self.device}; got {t.dtype} {tuple(t.shape)} on {t.device}")
 
     def _table(self, t, rows):
-        if (t.dtype is not self._i32 or t.shape != (rows, self.max_pages) or t.get_device() != self._dev
-                or (t.stride(1) != 1 and rows and self.max_pages > 1) or (rows > 1 and t.stride(0) < self.max_pages)):
-            raise ValueError(f"want tables int32 [{rows}, {self.max_pages}] on {self.device}, rows apart; got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
-        return t.data_ptr(), max(t.stride(0), self.max_pages)
+        n = self.max_pages
+        if t.dtype is self._i32 and t.shape == (rows, n) and t.get_device() == self._dev:
+            if t.is_contiguous():
+                return t.data_ptr(), n
+            row, one = t.stride()
+            if (one == 1 or n == 1) and (row >= n or rows == 1):
+                return t.data_ptr(), max(row, n)
+        raise ValueError(f"want tables int32 [{rows}, {n}] on {self.device}, rows apart; got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
     def _pool(self, t):
-        st, (_, _, p, d) = t.stride(), self.pool_shape
-        if (t.dtype is not self.cache_dtype or t.shape != self.pool_shape or t.get_device() != self._dev or st[3] != 1
-                or st[2] != d or (st[1] != p * d and self.n_kv_heads > 1)):
-            raise ValueError(f"want a pool {self.cache_dtype} {self.pool_shape} on {self.device}, dense within a page; got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
-        return t.data_ptr(), max(st[0], self.n_kv_heads * p * d)
+        if t.dtype is self.cache_dtype and t.shape == self.pool_shape and t.get_device() == self._dev:
+            page, head, row, one = t.stride()
+            _, heads, p, d = self.pool_shape
+            if one == 1 and row == d and (head == p * d or heads == 1):
+                return t.data_ptr(), max(page, heads * p * d)
+        raise ValueError(f"want a pool {self.cache_dtype} {self.pool_shape} on {self.device}, dense within a page; got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
     def _scales(self, k, v):
         return (self._vector(k, self.n_kv_heads, self._f32) if k is not None else 0,
@@ -517,7 +522,7 @@ class PagedCache:
         B, i32, vec = lengths.shape[0], self._i32, self._vector
         if out is None:
             buf = self._empty((2 * n_rows + 2 * B + 4,), i32, stream)
-            out = CachePlan._make(buf.split((n_rows, n_rows, B + 1, B, 3)))
+            out = CachePlan._make(buf.split_with_sizes((n_rows, n_rows, B + 1, B, 3)))
             slots = buf.data_ptr()
             positions, starts = slots + 4 * n_rows, slots + 8 * n_rows
             lengths_out = starts + 4 * (B + 1)
