@@ -262,7 +262,8 @@ MOE_API int moe_router_topk_noalloc(const uint8_t *router_q, const uint16_t *rou
  * The pages of request b are tables[b][0 ..], in the order of its tokens: token p lies in slot
  *   tables[b][p / page_size] * page_size + p % page_size.
  * A moe_cache_t holds what the calls need besides: the shape, the rotary frequencies and the workspace. One handle
- * serves every layer of a model. The pointers of the calls are device memory; a call is asynchronous on `stream`,
+ * serves every layer of a model, on the device that was current when it was made. The pointers of the calls are device
+ * memory; a call is asynchronous on `stream`,
  * allocates nothing, makes no host synchronisation and can be captured in a CUDA graph. Calls on one handle must
  * not overlap in time, on the device either.
  *
@@ -375,7 +376,8 @@ typedef struct {
 MOE_API int moe_cache_attend(moe_cache_t *cache, const moe_cache_attend_t *attend, void *stream);
 
 /* Waits for the stream of the handle's last call and returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side
- * wait of an attend call ran out: its outputs are wrong) or MOE_ERR_INVALID_ARG (a call met a value on the device
+ * wait of an attend call ran out: its outputs are wrong, and later attend calls leave theirs unwritten until this call
+ * has reported it) or MOE_ERR_INVALID_ARG (a call met a value on the device
  * that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits: 1 a wait ran out,
  * 2 a length, 4 a page id or slot, 8 a free_state out of range. */
 MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);

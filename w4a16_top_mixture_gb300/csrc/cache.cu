@@ -160,6 +160,12 @@ extern "C" void moe_cache_destroy(moe_cache_t* c) {
   delete c;
 }
 
+// a handle works on the device that was current when it was made
+static bool on_device(const moe_cache* c) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == c->dev;
+}
+
 extern "C" int moe_debug_cache_check(const moe_cache_config_t* cfg, const moe_cache_plan_t* p,
                                      const moe_cache_write_t* w, const moe_cache_attend_t* a) {
   if (!cfg) return MOE_ERR_INVALID_ARG;
@@ -175,6 +181,7 @@ extern "C" int moe_cache_plan(moe_cache_t* c, const moe_cache_plan_t* p, void* s
   if (!c || !p) return MOE_ERR_INVALID_ARG;
   const int r = check_plan(c->cfg, *p);
   if (r != MOE_OK) return r;
+  if (!on_device(c)) return MOE_ERR_INVALID_ARG;
   c->last_stream = (cudaStream_t)stream;
   const cudaError_t e = cache_plan_launch(c->S, *p, c->arrivals, c->status, c->num_sms, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_plan");
@@ -184,6 +191,7 @@ extern "C" int moe_cache_write(moe_cache_t* c, const moe_cache_write_t* w, void*
   if (!c || !w) return MOE_ERR_INVALID_ARG;
   const int r = check_write(c->S, *w);
   if (r != MOE_OK || w->n_rows == 0) return r;
+  if (!on_device(c)) return MOE_ERR_INVALID_ARG;
   c->last_stream = (cudaStream_t)stream;
   const cudaError_t e = cache_write_launch(c->S, *w, c->turns, c->status, c->num_sms, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_write");
@@ -193,6 +201,7 @@ extern "C" int moe_cache_attend(moe_cache_t* c, const moe_cache_attend_t* a, voi
   if (!c || !a) return MOE_ERR_INVALID_ARG;
   const int r = check_attend(c->cfg, c->S, *a);
   if (r != MOE_OK || a->n_requests == 0) return r;
+  if (!on_device(c)) return MOE_ERR_INVALID_ARG;
   c->last_stream = (cudaStream_t)stream;
   const CacheAttendState w{c->workspace, c->status, c->num_sms, c->timeout_ns, c->skip_copy};
   c->skip_copy = 0;
