@@ -280,7 +280,8 @@ typedef struct {
   int page_size;      /* tokens per page: 16, 32, 64, 128 or 256 */
   int n_pages;        /* pages of a pool: n_pages * page_size < 2^31 */
   int max_requests;   /* largest B any call will pass: 1..4096 */
-  int max_pages;      /* entries of a table row: max_pages * page_size < 2^31, times max_requests and n_heads at most 2^36 */
+  int max_pages;      /* entries of a table row: max_pages * page_size < 2^31,
+                       * max_pages * page_size * max_requests * n_heads <= 2^36 */
   int act_dtype;      /* q, k, v, gate, out: MOE_DTYPE_F16 or MOE_DTYPE_BF16 */
   int cache_dtype;    /* act_dtype, or MOE_DTYPE_E4M3 with fp32 scales per key-value head */
   int rope_dim;       /* R: elements of a head that are rotated, a multiple of 16 up to head_dim; 0 for none */

@@ -50,7 +50,7 @@ def test_well_formed_calls_pass(L):
     dict(n_heads=15), dict(n_heads=0), dict(n_heads=256, n_kv_heads=2), dict(n_kv_heads=0), dict(n_kv_heads=257, n_heads=257),
     dict(head_dim=96), dict(head_dim=0), dict(page_size=8), dict(page_size=24), dict(page_size=512), dict(page_size=0),
     dict(n_pages=0), dict(n_pages=1 << 27), dict(max_pages=0), dict(max_pages=1 << 27), dict(max_requests=0),
-    dict(max_requests=4097), dict(act_dtype=2), dict(act_dtype=1), dict(cache_dtype=3), dict(rope_dim=8), dict(rope_dim=272),
+    dict(max_requests=4097), dict(max_requests=4096, max_pages=1 << 17), dict(act_dtype=2), dict(act_dtype=1), dict(cache_dtype=3), dict(rope_dim=8), dict(rope_dim=272),
     dict(rope_dim=-16), dict(rope_theta=1.0), dict(rope_theta=float("nan")), dict(norm_eps=-1.0), dict(norm_eps=float("inf")),
     dict(gamma_offset=float("nan"))], ids=str)
 def test_shapes_without_a_kernel_are_unsupported(L, change):
@@ -69,9 +69,10 @@ def test_plan_refuses(L, change):
 
 
 @pytest.mark.parametrize("change", [
-    dict(q=0), dict(o=0), dict(q=P + 8), dict(k=0), dict(v=P + 2), dict(q_row=4100), dict(k_head=4), dict(v_row=1 << 40),
+    dict(q=0), dict(o=0), dict(q=P + 8), dict(k=0), dict(v=P + 2), dict(q_row=4100), dict(k_head=4), dict(v_row=1 << 40), dict(k_head=1 << 30),
     dict(q_gamma=P + 8), dict(k_gamma=P + 2), dict(positions=0), dict(slots=P + 1), dict(k_cache=0), dict(v_cache=P + 8),
-    dict(k_page=DENSE - 8), dict(v_page=DENSE + 4), dict(k_scale=P), dict(v_scale=P), dict(n_rows=-1)], ids=str)
+    dict(k_page=DENSE - 8), dict(v_page=DENSE + 4), dict(k_scale=P), dict(v_scale=P), dict(n_rows=-1),
+    dict(n_rows=(1 << 24) + 1)], ids=str)
 def test_write_refuses(L, change):
     assert status(L, write=change) == -1
 

@@ -56,7 +56,8 @@ __device__ __forceinline__ void follow_predecessor() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 template <class... P, class... A>
-cudaError_t launch_following(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, const A&... args) {
+cudaError_t launch_following(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                             const A&... args) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(grid);
   c.blockDim = dim3(block);

@@ -1,18 +1,31 @@
 // Attention of one new token of each request over the paged cache (moe_cache_attend).
 //
 // Every cached key and value is read once from HBM and meets only the query heads of its group, so the bytes of the
-// cache bound the kernel; all else is arranged to keep them coming.
+// cache bound the kernel; all else is arranged to keep them coming. One CTA to an SM.
 //   Work. The tokens of a request and key-value head (an item) are cut into tiles of TN. The tiles of all items, one
 //   after another, are divided evenly over the CTAs, whatever the requests' lengths are: a CTA walks its range, and an
 //   item that crosses a CTA's border is split. Nobody waits: every CTA of a split item leaves its partial sums in the
-//   workspace, and the one that counts itself last joins them, in the order of the tiles (in two steps where they are many).
-//   Copies. One warp walks the block table ahead of the rest and brings 16 tokens x 128 bytes at a time with TMA into a
-//   ring of stages, keys and values in stages of their own, across the borders of items; queries and gates of the next
-//   item with it.
+//   workspace, and the one that counts itself last joins them, in the order of the tiles (in two steps where they are
+//   many). It does so when it has nothing else to do: joining between two items stalled the copies by 5 to 10 us.
+//   Copies. For each of two teams of math warps a warp walks the block table ahead of it and brings 16 tokens x 128
+//   bytes at a time with TMA into the team's ring of 16 KB stages, keys and values in stages of their own, across the
+//   borders of items; queries and gates of the next item with it. One copying warp for both teams issued too slowly
+//   (188 us where two take 183, and 114 against 101 with an e4m3 cache).
 //   Products. Heads are the narrow side of the tensor cores' m16n8k16: S^T[tokens x heads] = K Q^T and
-//   O^T[d x heads] = V^T P^T, so that eight query heads fill a tile. The math warps share a tile: each takes 16 tokens
-//   (or 32) of S and then its share of the rows d of O. One maximum for all of them, exchanged through shared memory, lets
-//   O be kept once.
+//   O^T[d x heads] = V^T P^T, so that eight query heads fill a tile (tcgen05's 128 rows would leave its results in
+// tensor
+//   memory, a round trip away from the softmax between the products; mma.sync needs a tenth of the tensor cores' time
+//   here). The teams take the tiles in turn, so that one's softmax hides behind the other's products. The four warps of
+//   a team share a tile: each takes 16 tokens (or 32) of S and then its share of the rows d of O. One maximum for the
+//   four, exchanged through shared memory, lets O be kept once.
+// Measured (16 query over 2 key-value heads of 256): 128 requests of 512 to 16000 tokens, 1.19 GB: 179 us, 6.6 TB/s (a
+// plain copy runs at 6.8); 256 requests over an e4m3 cache, 445 MB: 75 us, where a tile's conversions and products
+// leave
+// less slack; one request of 130 tokens: 7.4 us, of which the chain lengths - table - keys takes 3, the launch 2.
+// What is
+// left in between: 5 us until the first keys arrive, up to 8 us of joining, and SMs that do not all get the same
+// bandwidth
+// (on equal shares 48 of them end 10 % later; smaller shares for whoever is done first cost more than they won).
 #include <cuda.h>
 
 #include <atomic>
@@ -25,7 +38,8 @@ namespace {
 
 constexpr int SHORT = 5;                          // units of an item that is not split without need
 constexpr int GROUP = 10, FLAT = 20;              // CTAs whose parts are joined first; from FLAT + 1 parts on
-constexpr int MAX_CTAS = 1024, COUNT_WORDS = MAX_CTAS + MAX_CTAS / GROUP * 2;    // of the workspace
+constexpr int MAX_CTAS = 1024, COUNT_WORDS = 2048;                               // of the workspace
+static_assert(COUNT_WORDS >= MAX_CTAS + 2 * ((MAX_CTAS + GROUP - 1) / GROUP) && COUNT_WORDS % 4 == 0, "all counts");
 constexpr int PART_MAX = 16 * 256 + 32;           // floats of the largest part
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -62,9 +76,11 @@ struct Shape {
   static constexpr int PP = TN + 8;                         // pitch of P: rows of 8 fall on different banks
   static constexpr int QP = D + 8;                          // pitch of queries and gates
   static constexpr int PART = NH * D + 2 * NH;              // floats of a partial result: O, maxima, sums
-  // of shared memory besides the rings and the lengths: barriers; queries and gates, twice; for each team P, maxima and sums;
+  // of shared memory besides the rings and the lengths: barriers; queries and gates, twice; for each team P,
+  // maxima and sums;
   // one's results on their way to the other
-  static constexpr int MISC = 1024 + 4 * NH * QP * 2 + TEAMS * (NH * PP * 2 + 2 * WARPS * NH * 4) + NH * D * 4 + (1 + WARPS) * NH * 4;
+  static constexpr int MISC = 1024 + 4 * NH * QP * 2 + TEAMS * (NH * PP * 2 + 2 * WARPS * NH * 4) + NH * D * 4 +
+                              (1 + WARPS) * NH * 4;
 };
 
 // ---- instructions ----
@@ -125,9 +141,11 @@ __device__ __forceinline__ void named_arrive(int id, int nthreads) {
 }
 
 // ---- the division of the work ----
-// Items come request by request, within a request head by head. An item of n tiles is n + EXTRA units long, for what its
+// Items come request by request, within a request head by head. An item of n tiles is n + EXTRA units long, for
+// what its
 // beginning and end cost; CTA c takes units c * share .. (c + 1) * share - 1.
-// An even share; but while no item is longer than SHORT, a CTA takes whole items: a split one's parts take longer to join
+// An even share; but while no item is longer than SHORT, a CTA takes whole items: a split one's parts take longer
+// to join
 // than a few tiles to read (130 tokens of two 256-wide heads: 8.5 us whole, 10.5 us in six parts).
 __host__ __device__ inline int even_share(int units, int longest, int ctas) {
   const int even = units > 0 ? (int)(((long long)units + ctas - 1) / ctas) : 1;
@@ -150,7 +168,8 @@ struct Place {
   }
 };
 
-// o += V^T P^T over the groups of 16 tokens of one stage, from group g0 of the tile on; the first `left` tokens of the tile
+// o += V^T P^T over the groups of 16 tokens of one stage, from group g0 of the tile on; the first `left` tokens of
+// the tile
 // count (EDGE). from: the lane's address in the stage, pbase: in P.
 template <class S, bool EDGE>
 __device__ __forceinline__ void add_values(float (&o)[S::MD][S::NT][4], uint32_t from, uint32_t pbase, int g0, int left,
@@ -218,7 +237,8 @@ struct Split {
   int b, h, c0, c1;
 };
 
-// The parts of a split item, or of a group of CTAs where they are many, that have arrived when this CTA's does: their count
+// The parts of a split item, or of a group of CTAs where they are many, that have arrived when this CTA's does:
+// their count
 // is in arrive's word, complete when the last one is there (and then set back).
 __device__ __forceinline__ uint32_t* count_of(const AttendArgs& A, const Split& sp, int* n) {
   const int gi = blockIdx.x / GROUP;
@@ -226,7 +246,8 @@ __device__ __forceinline__ uint32_t* count_of(const AttendArgs& A, const Split& 
     *n = sp.c1 - sp.c0 + 1;
     return &A.counts[sp.c0];
   }
-  const int from = sp.c0 > gi * GROUP ? sp.c0 : gi * GROUP, to = sp.c1 < gi * GROUP + GROUP ? sp.c1 : gi * GROUP + GROUP - 1;
+  const int from = sp.c0 > gi * GROUP ? sp.c0 : gi * GROUP;
+  const int to = sp.c1 < gi * GROUP + GROUP ? sp.c1 : gi * GROUP + GROUP - 1;
   *n = to - from + 1;
   return &A.group_counts[2 * gi + (gi == sp.c0 / GROUP)];
 }
@@ -245,7 +266,8 @@ __device__ __forceinline__ bool complete(const AttendArgs& A, const Split& sp, i
 // The joined parts of a split item: NH * D / 4 groups of four d, PER of them to each math thread.
 template <class S>
 struct Joined {
-  static constexpr int NH = S::NH, D = S::D, VECS = NH * D / 4, STEP = S::TEAMS * S::MATH, PER = (VECS + STEP - 1) / STEP;
+  static constexpr int NH = S::NH, D = S::D, VECS = NH * D / 4;
+  static constexpr int STEP = S::TEAMS * S::MATH, PER = (VECS + STEP - 1) / STEP;
   static constexpr int FEW = 16 / PER < 8 ? 16 / PER : 8;
   static_assert(VECS % STEP == 0 || PER == 1, "whole vectors for each thread, or one for some");
   float4 y[PER];
@@ -253,7 +275,8 @@ struct Joined {
   uint2 gate[PER];
 
   __device__ __forceinline__ static bool mine(int tid) { return VECS >= STEP || tid < VECS; }
-  // Part i of ia .. ib lies in slot 2 i + (i == i0): i0 is where the item begins. Up to FEW of them come straight from L2,
+  // Part i of ia .. ib lies in slot 2 i + (i == i0): i0 is where the item begins. Up to FEW of them come
+  // straight from L2,
   // every load on its way at once; the order of the sum is that of the parts.
   __device__ __forceinline__ void few(const float* parts, int ia, int ib, int i0, int tid) {
     if (!mine(tid)) return;
@@ -366,7 +389,8 @@ template <class S>
 __global__ void __launch_bounds__(S::THREADS, 1)
     k_cache_attend(const __grid_constant__ AttendArgs A, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
-  constexpr int D = S::D, NT = S::NT, NH = S::NH, TN = S::TN, MT = S::MT, KT = S::KT, MD = S::MD, PP = S::PP, QP = S::QP;
+  constexpr int D = S::D, NT = S::NT, NH = S::NH, TN = S::TN, MT = S::MT, KT = S::KT, MD = S::MD;
+  constexpr int PP = S::PP, QP = S::QP;
   constexpr int GPS = S::GPS, WARPS = S::WARPS, TEAMS = S::TEAMS, MATH = S::MATH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -403,7 +427,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   }
   if (tid <= TEAMS * 16) fence_mbar_init();
   follow_predecessor();
-  // lengths and the running number of tiles: a thread's requests lie side by side, so that all its loads are on their way
+  // lengths and the running number of tiles: a thread's requests lie side by side, so that all its loads are on
+  // their way
   // at once
   const int each = (A.B + S::THREADS - 1) / S::THREADS, b_begin = tid * each < A.B ? tid * each : A.B;
   const int b_end = b_begin + each < A.B ? b_begin + each : A.B;
@@ -477,7 +502,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     uint8_t* const my_ring = ring + team * A.n_stages * S::STAGE;
     int stage = 0;
     uint32_t phase = 0, n_rows = 0;                  // n_rows: copies of rows so far, by the first team's warp
-    // keys and values are read once, so they leave L2 first (256 requests over an e4m3 cache: 74.9 us, 79.5 us without);
+    // keys and values are read once, so they leave L2 first (256 requests over an e4m3 cache: 74.9 us, 79.5 us
+    // without);
     // twice or more where a group's heads are several items
     const uint64_t policy = A.head_tiles == 1 ? policy_evict_first() : policy_evict_normal();
     bool skip = A.skip_copy && blockIdx.x == 0 && team == 0;
@@ -492,7 +518,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       __syncwarp();
       if (!s_flags[0]) return true;
       for (int s = 0; s < A.n_stages; ++s) mbar_wait(&full[s], s < stage ? phase : phase ^ 1, A.timeout_ns);
-      for (uint32_t i = n_rows > 2 ? n_rows - 2 : 0; i < n_rows; ++i) mbar_wait(&rows_full[i & 1], i >> 1 & 1, A.timeout_ns);
+      for (uint32_t i = n_rows > 2 ? n_rows - 2 : 0; i < n_rows; ++i)
+        mbar_wait(&rows_full[i & 1], i >> 1 & 1, A.timeout_ns);
       return false;
     };
     // the item's queries, and its gates where the whole item is this CTA's: rows of D elements
@@ -511,7 +538,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       ++n_rows;
       return true;
     };
-    // the pages of 32 groups of 16 tokens from a tile on, one to a lane; looked at only when they are used, which is while
+    // the pages of 32 groups of 16 tokens from a tile on, one to a lane; looked at only when they are used,
+    // which is while
     // the next 32 are on their way
     auto pages_from = [&](const Place& p) {
       const long long tok = (long long)p.j * TN + lane * 16;
@@ -601,8 +629,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   uint64_t* const full = full0 + team * 16;
   uint64_t* const empty = empty0 + team * 16;
   const uint32_t k_lane = ring0 + in_group(lane & 15, lane >> 4);
-  const uint32_t v_lane = ring0 + (S::E4M3 ? (lane >> 4) * S::GROUP_BYTES + in_group(lane & 15, wt * MD)
-                                           : in_group((lane & 7) + ((lane >> 4) << 3), wt * MD * 2 + ((lane >> 3) & 1)));
+  const uint32_t v_lane =
+      ring0 + (S::E4M3 ? (lane >> 4) * S::GROUP_BYTES + in_group(lane & 15, wt * MD)
+                       : in_group((lane & 7) + ((lane >> 4) << 3), wt * MD * 2 + ((lane >> 3) & 1)));
   const uint32_t p_lane = smem_u32(s_p) + ((lane & 7) * PP + (lane >> 3) * 8) * 2;
   auto wait_full = [&](uint64_t* bar, uint32_t parity) {
     // once a wait has run out the outputs are lost: run to the end without waiting
@@ -623,7 +652,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   int t = t0, done = 0;                                      // done: tiles of the CTA so far
   Place at = begin;
   Split split[2] = {{-1, 0, 0, 0}, {-1, 0, 0, 0}};           // of the first item and of the last
-  int head_before = -1;                                      // parts of the first item that had arrived before this CTA's
+  // parts of the first item that had arrived before this CTA's
+  int head_before = -1;
   while (t < last) {
     const int kvh = at.h / A.head_tiles, h_in = (at.h % A.head_tiles) * NH;
     const int h0 = kvh * A.group + h_in;                       // first query head of the item
@@ -636,6 +666,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     // past nh hold whatever memory holds: no head's column reaches another's, and theirs are not written.
     uint32_t q[D / 16][NT][2];
     float sf[NT][2];                                           // what a product is multiplied by, for 2^x
+    const float ks = S::E4M3 ? __ldcg(a.k_scale + kvh) : 1.f;
     wait_full(&rows_full[n_rows & 1], n_rows >> 1 & 1);
     const uint16_t* const q_rows = s_q + (n_rows & 1) * 2 * NH * QP;
 #pragma unroll
@@ -688,7 +719,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        sf[nt][i] = A.scale * (S::E4M3 ? __ldcg(a.k_scale + kvh) * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + i) * 4) : 1.f);
+        sf[nt][i] = A.scale * (S::E4M3 ? ks * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + i) * 4) : 1.f);
     }
 
     float o[MD][NT][4], m[NT][2], l[NT][2];
@@ -719,7 +750,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           for (int i = 0; i < 4; ++i) s[mt][nt][i] = s2[mt][nt][i] = 0.f;
 #pragma unroll 1
       for (int g0 = 0; g0 < groups; g0 += GPS) {
-        // every warp of the team waits for every stage: one that went ahead could release a stage twice before the others once
+        // every warp of the team waits for every stage: one that went ahead could release a stage twice
+        // before the others once
         wait_full(&full[stage], phase);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -904,7 +936,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             for (int md = 0; md < MD; ++md)
 #pragma unroll
               for (int r = 0; r < 2; ++r)
-                o[md][nt][2 * r + i] = o[md][nt][2 * r + i] * c0 + s_x[((md * NT + nt) * MATH + ttid) * 4 + 2 * r + i] * c1;
+                o[md][nt][2 * r + i] =
+                    o[md][nt][2 * r + i] * c0 + s_x[((md * NT + nt) * MATH + ttid) * 4 + 2 * r + i] * c1;
           }
           l[nt][i] = x;
         }
@@ -914,7 +947,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     auto d_of = [&](int md, int r) {
       return S::E4M3 ? (wt * MD + md) * 16 + 2 * g + r : (wt * MD + md) * 16 + g + 8 * r;
     };
-    // a part is joined with the others once this CTA has nothing else to do: the item's tiles are those of CTAs c0 .. c1;
+    // a part is joined with the others once this CTA has nothing else to do: the item's tiles are those of
+    // CTAs c0 .. c1;
     // c0 holds its part as the item it leaves, the others as the item they begin in the middle of
     const int which = j0 == 0 ? 1 : 0;
     if (!whole) {
@@ -963,7 +997,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     if (owner) release(&rows_empty[n_rows & 1]);
     ++n_rows;
     if (owner && !whole && which == 0 && t + j1 - j0 < last) {
-      // the first item's part arrives now, while there are tiles to come; whether it was the last is looked at in the end
+      // the first item's part arrives now, while there are tiles to come; whether it was the last is looked
+      // at in the end
       team_barrier<S>(team);
       if (ttid == 0) {
         __threadfence();
@@ -1050,8 +1085,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   }
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 using ReplaceFn = CUresult (*)(CUtensorMap*, void*);
@@ -1083,8 +1118,8 @@ cudaError_t pool_map(const CacheShape& c, const void* pool, int64_t page_stride,
   const cuuint64_t dims[3] = {(cuuint64_t)S::D, (cuuint64_t)c.Hkv << c.page_log2, (cuuint64_t)c.n_pages};
   const cuuint64_t strides[2] = {(cuuint64_t)S::RB, (cuuint64_t)page_stride * es};
   const cuuint32_t box[3] = {(cuuint32_t)(S::CB / es), 16, 1}, ones[3] = {1, 1, 1};
-  const CUresult r = fn(m, S::E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, (void*)pool, dims,
-                        strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUtensorMapDataType type = S::E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+  const CUresult r = fn(m, type, 3, (void*)pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         S::CB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -1094,7 +1129,8 @@ constexpr int SMEM_PER_CTA = 227 * 1024;
 
 template <class S>
 cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
-  static_assert(S::MISC + 1024 + CACHE_MAX_REQUESTS * 4 + S::TEAMS * 2 * S::STAGE <= SMEM_PER_CTA, "the ring has two stages at least");
+  static_assert(S::MISC + 1024 + CACHE_MAX_REQUESTS * 4 + S::TEAMS * 2 * S::STAGE <= SMEM_PER_CTA,
+                "a ring has two stages at least");
   CUtensorMap km, vm;
   cudaError_t e = pool_map<S>(c, A.a.k_cache, A.a.k_page_stride, &km);
   if (e == cudaSuccess && A.a.v_page_stride == A.a.k_page_stride) {

@@ -107,7 +107,8 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
     if (b < a.B) {
       const uint32_t need_at = (uint32_t)at, back_at = (uint32_t)(at >> 32);
       const bool done = nw[i] < 0, ok = fits[i] && (need[i] == 0 || need_at + (uint32_t)need[i] <= (uint32_t)count);
-      s_at[b] = ok ? (need[i] ? (int)need_at : 0) : done ? (int)(-2 - (int)(back_at < 0x3FFFFFFFu ? back_at : 0x3FFFFFFFu)) : -1;
+      const int back_to = (int)(back_at < 0x3FFFFFFFu ? back_at : 0x3FFFFFFFu);
+      s_at[b] = ok ? (need[i] ? (int)need_at : 0) : done ? -2 - back_to : -1;
       if (ok) taken += need[i];
       else if (!done) ++refused;
       at += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(done ? held[i] : 0) << 32;
@@ -195,7 +196,8 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
 cudaError_t cache_plan_init() {
   cudaError_t e = cudaSuccess;
   for (auto* k : {k_cache_plan<1>, k_cache_plan<2>, k_cache_plan<4>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CACHE_MAX_REQUESTS * 12);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CACHE_MAX_REQUESTS * 12);
   return e;
 }
 

@@ -67,15 +67,21 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
 }
 __device__ __forceinline__ uint32_t quantize4(const pair x[2], float s, float r) {
   const float2 f0 = split(x[0]), f1 = split(x[1]);
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(quotient(f0.x, s, r), quotient(f0.y, s, r)), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(quotient(f1.x, s, r), quotient(f1.y, s, r)), __NV_SATFINITE, __NV_E4M3);
+  const float2 a = make_float2(quotient(f0.x, s, r), quotient(f0.y, s, r));
+  const float2 b = make_float2(quotient(f1.x, s, r), quotient(f1.y, s, r));
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
 
-// A warp to a row, or to a slice of its heads where there are few rows. A head's D elements lie over D / 8 lanes, 8 to a
-// lane, so a step of a warp is 256 / D heads of q, of k or of v. A lane among the first R / 8 holds elements 4l .. 4l+3 and
-// their partners R/2 further on, so that the rotation needs no exchange; the others hold 8 in a row. Each lane makes its
-// four cosines and sines once for all heads: the angle in turns is position times frequency modulo 1, exactly, as integers
+// A warp to a row, or to a slice of its heads where there are few rows. A head's D elements lie over D / 8 lanes,
+// 8 to a
+// lane, so a step of a warp is 256 / D heads of q, of k or of v. A lane among the first R / 8 holds elements 4l ..
+// 4l+3 and
+// their partners R/2 further on, so that the rotation needs no exchange; the others hold 8 in a row. Each lane
+// makes its
+// four cosines and sines once for all heads: the angle in turns is position times frequency modulo 1, exactly, as
+// integers
 // (fp32 loses its fraction), and its upper 32 bits are the argument. What bounds the kernel is the bytes, then the
 // instructions and whole waves of warps: the loads of three steps are on their way while three others are worked on,
 // nothing synchronises, and a row is cut in two where that fills the last wave. 8192 rows of 32 + 2 x 8 heads of 128
@@ -99,7 +105,8 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const
   const uint16_t* const q0 = (const uint16_t*)w.q.p + t * w.q.row_stride + sub * w.q.head_stride + e0;
   const uint16_t* const k0 = (const uint16_t*)w.k.p + t * w.k.row_stride + sub * w.k.head_stride + e0;
   const uint16_t* const v0 = (const uint16_t*)w.v.p + t * w.v.row_stride + sub * w.v.head_stride + e0;
-  const int qs = PER_WARP * (int)w.q.head_stride, ks = PER_WARP * (int)w.k.head_stride, vs = PER_WARP * (int)w.v.head_stride;
+  const int qs = PER_WARP * (int)w.q.head_stride, ks = PER_WARP * (int)w.k.head_stride;
+  const int vs = PER_WARP * (int)w.v.head_stride;
   auto load = [&](uint2 (&raw)[WRITE_AHEAD][2], int s0) {
 #pragma unroll
     for (int i = 0; i < WRITE_AHEAD; ++i) {
@@ -163,7 +170,8 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const
     unpack4<BF16>(raw[0], x[0]);
     unpack4<BF16>(raw[1], x[1]);
     if (norm) {
-      const float2 sum = split(fma2(x[0][0], x[0][0], fma2(x[0][1], x[0][1], fma2(x[1][0], x[1][0], mul2(x[1][1], x[1][1])))));
+      const pair upper = fma2(x[1][0], x[1][0], mul2(x[1][1], x[1][1]));
+      const float2 sum = split(fma2(x[0][0], x[0][0], fma2(x[0][1], x[0][1], upper)));
       float ss = sum.x + sum.y;
       // a head's lanes lie in one warp
 #pragma unroll

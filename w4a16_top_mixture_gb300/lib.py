@@ -441,8 +441,8 @@ class PagedCache:
         import torch
         self.lib = load_library()
         cache_dtype = cache_dtype or dtype
-        self.cfg = CacheConfig(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests, max_pages, DTYPES[dtype],
-                               CACHE_DTYPES[cache_dtype], rope_dim, rope_theta, gamma_offset, eps)
+        self.cfg = CacheConfig(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests, max_pages,
+                               DTYPES[dtype], CACHE_DTYPES[cache_dtype], rope_dim, rope_theta, gamma_offset, eps)
         h = ctypes.c_void_p()
         _check(self.lib.moe_cache_create(ctypes.byref(self.cfg), ctypes.byref(h)), "moe_cache_create")
         self.h = h
@@ -470,15 +470,17 @@ class PagedCache:
     def _rows(self, t, heads, rows):
         """(pointer, row stride, head stride) of a [rows, heads, head_dim] tensor of the activations' type."""
         r, h, d = t.stride() if t.dim() == 3 else (0, 0, 0)
-        if d != 1 or t.dtype is not self.dtype or t.shape != (rows, heads, self.head_dim) or t.get_device() != self._dev:
-            raise ValueError(f"want {self.dtype} [{rows}, {heads}, {self.head_dim}] on {self.device}, innermost stride 1; "
-                             f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+        if (d != 1 or t.dtype is not self.dtype or t.shape != (rows, heads, self.head_dim)
+                or t.get_device() != self._dev):
+            raise ValueError(f"want {self.dtype} [{rows}, {heads}, {self.head_dim}] on {self.device}, innermost stride "
+                             f"1; got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
         return t.data_ptr(), r if rows > 1 else 0, h if heads > 1 else 0
 
     def _vector(self, t, n, dtype):
         if t.dtype is dtype and t.shape == (n,) and t.get_device() == self._dev and t.is_contiguous():
             return t.data_ptr()
-        raise ValueError(f"want a contiguous {dtype} [{n}] on {self.device}; got {t.dtype} {tuple(t.shape)} on {t.device}")
+        raise ValueError(f"want a contiguous {dtype} [{n}] on {self.device}; got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
 
     def _table(self, t, rows):
         n = self.max_pages
@@ -529,10 +531,12 @@ class PagedCache:
             state_out = lengths_out + 4 * B
         else:
             slots, positions = vec(out.slots, n_rows, i32), vec(out.positions, n_rows, i32)
-            starts, lengths_out, state_out = vec(out.starts, B + 1, i32), vec(out.lengths, B, i32), vec(out.free_state, 3, i32)
+            starts, lengths_out = vec(out.starts, B + 1, i32), vec(out.lengths, B, i32)
+            state_out = vec(out.free_state, 3, i32)
         args = CACHE_PLAN.pack(
             vec(lengths, B, i32), vec(new_tokens, B, i32) if new_tokens is not None else 0, *self._table(tables, B),
-            vec(free_pages, self.n_pages, i32), vec(free_state, 3, i32), state_out, lengths_out, starts, slots, positions, B, n_rows)
+            vec(free_pages, self.n_pages, i32), vec(free_state, 3, i32), state_out, lengths_out, starts,
+            slots, positions, B, n_rows)
         self._call(self.lib.moe_cache_plan, args, stream, "moe_cache_plan")
         return out
 
