@@ -93,6 +93,14 @@ def test_an_8_bit_cache_needs_its_scales_and_whole_16_byte_pages(L):
     assert status(L, cfg=cfg, attend=dict(both, k_page=DENSE + 8)) == -1
 
 
+def test_pages_are_whole_lines_apart(L):
+    narrow = dict(cache_dtype=2, head_dim=64, rope_dim=64)
+    both = dict(k_scale=P, v_scale=P)
+    for change, want in ((dict(), 0), (dict(k_page=DENSE + 128), 0), (dict(v_page=DENSE + 64), -1), (dict(k_page=DENSE + 192), -1)):
+        assert status(L, cfg=narrow, attend=dict(both, **change)) == want, change
+        assert status(L, cfg=narrow, write=dict(both, **change)) == want, change
+
+
 def test_null_handles_and_no_device(L):
     import torch
     h = ctypes.c_void_p()

@@ -356,6 +356,23 @@ def test_attend_matches_the_oracle(lengths, Hq, Hkv, D, page, act, cache, gate):
     assert torch.equal(out, again)                            # sums in a fixed order
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("D,act,cache,Hq,Hkv", [(64, "f16", "e4m3", 9, 3), (64, "bf16", "bf16", 7, 1), (128, "bf16", "e4m3", 6, 2)])
+def test_attend_copies_of_several_rows(D, act, cache, Hq, Hkv, page):
+    """Rows of a line or less, copied by as much of a page as a stage holds: ends within a copy, within a page."""
+    lengths = EDGES + [240, 241, 255, 256, 272, 273, 511, 513, 529]
+    d, n_pages, width = attend_case(lengths, Hq, Hkv, D, page, act, cache, page + D, True)
+    c = lib.PagedCache(Hq, Hkv, D, page, n_pages, len(lengths), width, dtype=act, cache_dtype=cache)
+    out = c.attend(**d)
+    assert c.status() == (0, 0)
+    attend_check(d, out, Hq, Hkv, D, act, cache)
+    long = lengths.index(529)
+    d["tables"][long, 0], d["tables"][long, 1] = n_pages, -5  # read as zeros, whole copies of them
+    out = c.attend(**d)
+    assert c.status() == (-1, 4)
+    attend_check(d, out, Hq, Hkv, D, act, cache)
+
+
 def test_attend_calls_of_alternating_shapes_on_one_handle():
     torch = torch_()
     cases = [attend_case(n, 16, 2, 256, 16, "f16", "f16", 50 + i, width=400) for i, n in enumerate(([5000, 3, 700], [64] * 90, [1], [6000]))]

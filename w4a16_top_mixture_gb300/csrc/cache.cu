@@ -67,10 +67,11 @@ bool rows_ok(const moe_rows_t& r) {
   return aligned(r.p, 16) && r.row_stride % 8 == 0 && r.head_stride % 8 == 0 &&
          llabs(r.row_stride) < (int64_t)1 << 40 && llabs(r.head_stride) < (int64_t)1 << 30;
 }
-// a pool: 16-byte aligned, pages that do not overlap, whole rows of D apart
+// a pool: 16-byte aligned, pages that do not overlap, whole rows of D and whole lines of 128 bytes apart
 bool pool_ok(const CacheShape& S, const void* p, int64_t page_stride) {
   return aligned(p, 16) && page_stride >= ((int64_t)S.Hkv << S.page_log2) * S.D && page_stride < (int64_t)1 << 38 &&
-         page_stride % S.D == 0;
+         page_stride % S.D == 0 &&
+         (S.e4m3 ? page_stride : 2 * page_stride) % 128 == 0;
 }
 bool scales_ok(const CacheShape& S, const float* k, const float* v) {
   return S.e4m3 ? aligned(k, 4) && aligned(v, 4) : !k && !v;

@@ -46,6 +46,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 struct AttendArgs {
   moe_cache_attend_t a;
   int B, Hq, Hkv, group, head_tiles, page_log2, n_pages, n_stages;
+  int box;                   // groups of 16 tokens to a copy: a power of two
   long long max_len;
   float scale;
   float* parts;              // [CTA][2][part floats]: the item a CTA begins in the middle of, the one it leaves so
@@ -65,14 +66,15 @@ struct Shape {
   static constexpr int WARPS = 4, TEAMS = 2;                // math warps: the teams take the tiles in turn
   static constexpr int MATH = 32 * WARPS, THREADS = TEAMS * (MATH + 32);   // and a warp to copy for each team
   static constexpr int RB = D * (E4M3 ? 1 : 2);             // bytes of a token's row
-  static constexpr int CB = RB < 128 ? RB : 128, CH = RB / CB;
-  static constexpr int TN = RB >= 512 ? 64 : 128;           // tokens of a tile
+  // copies are of lines of 128 bytes: CH of them to a row, or LT tokens to a line
+  static constexpr int CB = 128, CH = RB < CB ? 1 : RB / CB, LT = RB < CB ? CB / RB : 1;
+  static constexpr int TN = RB >= 512 ? 64 : RB >= 128 ? 128 : 256;   // tokens of a tile
   static constexpr int MT = TN / 16 / WARPS;                // 16-token tiles of S per warp
   static constexpr int KT = TN / 16;
   static constexpr int GPS = 16384 / (16 * RB) < KT ? 16384 / (16 * RB) : KT;   // 16-token groups of a stage
   static constexpr int GROUP_BYTES = 16 * RB, STAGE = GPS * GROUP_BYTES;
   static constexpr int MD = D / 16 / WARPS;                 // 16-row tiles of O per warp
-  static constexpr int EXTRA = RB >= 128 ? 2 : 4;           // units of an item, see the division of the work
+  static constexpr int EXTRA = 2;                           // units of an item, see the division of the work
   static constexpr int PP = TN + 8;                         // pitch of P: rows of 8 fall on different banks
   static constexpr int QP = D + 8;                          // pitch of queries and gates
   static constexpr int PART = NH * D + 2 * NH;              // floats of a partial result: O, maxima, sums
@@ -581,14 +583,14 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             const CUtensorMap* const map = kv ? &vmap : &kmap;
             const int tok = tok0 + g0 * 16, in_page = (1 << A.page_log2) - 1;
             if (elect_one()) {
-              mbar_expect_tx(&full[stage], n * S::GROUP_BYTES);
+              mbar_expect_tx(&full[stage], ((n + A.box - 1) & -A.box) * S::GROUP_BYTES);
 #pragma unroll
               for (int grp = 0; grp < GPS; ++grp)
-                if (grp < n && !skip)
+                if (grp < n && (grp & (A.box - 1)) == 0 && !skip)
 #pragma unroll
                   for (int x = 0; x < S::CH; ++x)
                     tma_rows(dst + grp * S::GROUP_BYTES + x * 16 * S::CB, map, x * (D / S::CH),
-                             row0 + ((tok + grp * 16) & in_page), page[grp], &full[stage], policy);
+                             (row0 + ((tok + grp * 16) & in_page)) / S::LT, page[grp], &full[stage], policy);
             }
             __syncwarp();
             skip = false;
@@ -618,12 +620,13 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         *reinterpret_cast<uint4*>(rows_at(a.out, b, i / (D / 8), i % (D / 8) * 8)) = make_uint4(0, 0, 0, 0);
 
   // Where a lane's rows of a stage lie. 16-byte chunk c of row r of a group of 16 tokens is at
-  //   c / PER * 16 * CB + r * CB + ((c % PER) ^ swizzle(r)) * 16,      PER = CB / 16,
-  // so with chunks that differ in a constant's bits alone, the address differs by an exclusive or with 16 * constant.
+  //   c / PER * 16 * CB + r * CB + ((c % PER) ^ (r % 8)) * 16,      PER = CB / 16,
+  // and where a line holds LT rows, their chunks follow one another in it. With chunks that differ in a constant's bits
+  // alone, the address differs by an exclusive or with 16 * constant.
   constexpr int PER = S::CB / 16;
   auto in_group = [](int r, int c) {
-    const int sw = S::CB == 128 ? r & 7 : (r >> 1) & 3;
-    return (uint32_t)((c / PER) * (16 * S::CB) + r * S::CB + (((c % PER) ^ sw) << 4));
+    const int line = r / S::LT, at = r % S::LT * (PER / S::LT) + c % PER;
+    return (uint32_t)((c / PER) * (16 * S::CB) + line * S::CB + ((at ^ (line & 7)) << 4));
   };
   const uint32_t ring0 = smem_u32(ring) + team * A.n_stages * S::STAGE;
   uint64_t* const full = full0 + team * 16;
@@ -1108,19 +1111,21 @@ cudaError_t driver_fn(const char* name, std::atomic<F>& known, F* out) {
 std::atomic<EncodeFn> g_encode{nullptr};
 std::atomic<ReplaceFn> g_replace{nullptr};
 
-// a pool as rows of a head's D elements: [page][head, token][d], copied 16 tokens x CB bytes at a time
+// a pool as rows of a head's D elements, LT of them together: [page][head, token][d], copied `groups` of 16 tokens x
+// CB bytes at a time
 template <class S>
-cudaError_t pool_map(const CacheShape& c, const void* pool, int64_t page_stride, CUtensorMap* m) {
+cudaError_t pool_map(const CacheShape& c, const void* pool, int64_t page_stride, int groups, CUtensorMap* m) {
   EncodeFn fn;
   const cudaError_t e = driver_fn("cuTensorMapEncodeTiled", g_encode, &fn);
   if (e != cudaSuccess) return e;
   const int es = S::E4M3 ? 1 : 2;
-  const cuuint64_t dims[3] = {(cuuint64_t)S::D, (cuuint64_t)c.Hkv << c.page_log2, (cuuint64_t)c.n_pages};
-  const cuuint64_t strides[2] = {(cuuint64_t)S::RB, (cuuint64_t)page_stride * es};
-  const cuuint32_t box[3] = {(cuuint32_t)(S::CB / es), 16, 1}, ones[3] = {1, 1, 1};
+  const cuuint64_t rows = ((cuuint64_t)c.Hkv << c.page_log2) / S::LT;
+  const cuuint64_t dims[3] = {(cuuint64_t)S::D * S::LT, rows, (cuuint64_t)c.n_pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)S::RB * S::LT, (cuuint64_t)page_stride * es};
+  const cuuint32_t box[3] = {(cuuint32_t)(S::CB / es), (cuuint32_t)(16 * groups / S::LT), 1}, ones[3] = {1, 1, 1};
   const CUtensorMapDataType type = S::E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
   const CUresult r = fn(m, type, 3, (void*)pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        S::CB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -1131,8 +1136,14 @@ template <class S>
 cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
   static_assert(S::MISC + 1024 + CACHE_MAX_REQUESTS * 4 + S::TEAMS * 2 * S::STAGE <= SMEM_PER_CTA,
                 "a ring has two stages at least");
+  // where a row is a line or less, a copy takes as much of a page as fits a stage (64 requests, 540 MB: rows of 64
+  // bytes come at 3.7, 4.4, 4.7 and 5.1 TB/s from pages of 16, 32, 64 and 256 tokens, which are copies of 1, 2, 4 and
+  // 16 KB; rows of 128 bytes at 5.6 to 6.2). Copies of longer rows are of 2 KB and more as they are: larger ones won
+  // nothing (84.5 and 84.1 us for heads of 256)
+  A.box = 1;
+  while (S::CH == 1 && 2 * A.box <= S::GPS && 32 * A.box <= 1 << c.page_log2) A.box *= 2;
   CUtensorMap km, vm;
-  cudaError_t e = pool_map<S>(c, A.a.k_cache, A.a.k_page_stride, &km);
+  cudaError_t e = pool_map<S>(c, A.a.k_cache, A.a.k_page_stride, A.box, &km);
   if (e == cudaSuccess && A.a.v_page_stride == A.a.k_page_stride) {
     // the same map at another address: half the host's time for two
     ReplaceFn replace;
@@ -1140,7 +1151,7 @@ cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
     vm = km;
     if (e == cudaSuccess && replace(&vm, (void*)A.a.v_cache) != CUDA_SUCCESS) e = cudaErrorInvalidValue;
   } else if (e == cudaSuccess) {
-    e = pool_map<S>(c, A.a.v_cache, A.a.v_page_stride, &vm);
+    e = pool_map<S>(c, A.a.v_cache, A.a.v_page_stride, A.box, &vm);
   }
   if (e != cudaSuccess) return e;
   A.head_tiles = (A.group + S::NH - 1) / S::NH;
