@@ -269,6 +269,27 @@ def test_write_reports_slots_past_the_pool():
     assert set(changed.flatten().nonzero()[:, 0].tolist()) == {int(d["slots"][0]), int(d["slots"][3])}
 
 
+def test_write_heads_far_apart():
+    """Head strides of 2^29 elements: a step over a warp's heads passes 31 bits."""
+    torch = torch_()
+    T, H, D, far = 3, 5, 64, 1 << 29
+    buf = torch.empty((H - 1) * far + T * D, dtype=torch.float16, device="cuda")
+    g = gen_of(18)
+    x = randn(g, (3, T, H, D), "f16")
+    apart = buf.as_strided((T, H, D), (D, far, 1))
+    c = lib.PagedCache(H, H, D, 16, 1, 1, 1, rope_dim=0)
+    slots, positions = ints([0, 5, 15]), ints([0, 1, 2])
+    kc, vc = randn(g, (1, H, 16, D), "f16"), randn(g, (1, H, 16, D), "f16")
+    for far_q, far_k, far_v in ((1, 0, 0), (0, 1, 0), (0, 0, 1)):
+        apart.copy_(x[0] if far_q else x[1] if far_k else x[2])
+        q = c.write(apart if far_q else x[0], apart if far_k else x[1], apart if far_v else x[2], positions, slots, kc, vc,
+                    q_out=apart if far_q else None)
+        assert torch.equal(q, x[0])
+        for t, slot in enumerate([0, 5, 15]):
+            assert torch.equal(kc[0, :, slot], x[1, t]) and torch.equal(vc[0, :, slot], x[2, t])
+    assert c.status() == (0, 0)
+
+
 def test_write_far_positions():
     """Angles of positions up to 2^31 - 1 keep their fraction of a turn."""
     torch = torch_()

@@ -62,7 +62,7 @@ int check_config(const moe_cache_config_t& c, CacheShape* S) {
 }
 
 bool aligned(const void* p, int n) { return p && ((uintptr_t)p & (n - 1)) == 0; }
-// strides are bounded so that no row's byte offset can pass 63 bits, and a head's number times its stride 31 or so
+// strides are bounded so that no row's byte offset can pass 63 bits
 bool rows_ok(const moe_rows_t& r) {
   return aligned(r.p, 16) && r.row_stride % 8 == 0 && r.head_stride % 8 == 0 &&
          llabs(r.row_stride) < (int64_t)1 << 40 && llabs(r.head_stride) < (int64_t)1 << 30;

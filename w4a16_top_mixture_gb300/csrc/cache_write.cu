@@ -74,18 +74,14 @@ __device__ __forceinline__ uint32_t quantize4(const pair x[2], float s, float r)
   return lo | hi << 16;
 }
 
-// A warp to a row, or to a slice of its heads where there are few rows. A head's D elements lie over D / 8 lanes,
-// 8 to a
-// lane, so a step of a warp is 256 / D heads of q, of k or of v. A lane among the first R / 8 holds elements 4l ..
-// 4l+3 and
-// their partners R/2 further on, so that the rotation needs no exchange; the others hold 8 in a row. Each lane
-// makes its
-// four cosines and sines once for all heads: the angle in turns is position times frequency modulo 1, exactly, as
-// integers
-// (fp32 loses its fraction), and its upper 32 bits are the argument. What bounds the kernel is the bytes, then the
-// instructions and whole waves of warps: the loads of three steps are on their way while three others are worked on,
-// nothing synchronises, and a row is cut in two where that fills the last wave. 8192 rows of 32 + 2 x 8 heads of 128
-// (201 MB): 41 us, 4.9 TB/s; with four steps ahead and four CTAs to an SM 64 us, with whole rows 43 us.
+// A warp to a row, or to a slice of its heads where there are few rows. A head's D elements lie over D / 8 lanes, 8 to
+// a lane, so a step of a warp is 256 / D heads of q, of k or of v. A lane among the first R / 8 holds elements 4l ..
+// 4l+3 and their partners R/2 further on, so that the rotation needs no exchange; the others hold 8 in a row. Each lane
+// makes its four cosines and sines once for all heads: the angle in turns is position times frequency modulo 1,
+// exactly, as integers (fp32 loses its fraction), and its upper 32 bits are the argument. What bounds the kernel is the
+// bytes, then the instructions and whole waves of warps: the loads of three steps are on their way while three others
+// are worked on, nothing synchronises, and a row is cut in two where that fills the last wave. 8192 rows of 32 + 2 x 8
+// heads of 128 (201 MB): 41 us, 4.9 TB/s; with four steps ahead and four CTAs to an SM 64 us, with whole rows 43 us.
 template <int D, bool BF16, bool E4M3>
 __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const __grid_constant__ WriteArgs a) {
   constexpr int LANES = D / 8, PER_WARP = 32 / LANES;
@@ -105,8 +101,7 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const
   const uint16_t* const q0 = (const uint16_t*)w.q.p + t * w.q.row_stride + sub * w.q.head_stride + e0;
   const uint16_t* const k0 = (const uint16_t*)w.k.p + t * w.k.row_stride + sub * w.k.head_stride + e0;
   const uint16_t* const v0 = (const uint16_t*)w.v.p + t * w.v.row_stride + sub * w.v.head_stride + e0;
-  const int qs = PER_WARP * (int)w.q.head_stride, ks = PER_WARP * (int)w.k.head_stride;
-  const int vs = PER_WARP * (int)w.v.head_stride;
+  const int64_t qs = PER_WARP * w.q.head_stride, ks = PER_WARP * w.k.head_stride, vs = PER_WARP * w.v.head_stride;
   auto load = [&](uint2 (&raw)[WRITE_AHEAD][2], int s0) {
 #pragma unroll
     for (int i = 0; i < WRITE_AHEAD; ++i) {
@@ -115,13 +110,13 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const
       const uint16_t* p;
       bool in;
       if (st < q_steps) {
-        p = q0 + (long long)st * qs;
+        p = q0 + st * qs;
         in = st * PER_WARP + sub < a.Hq;
       } else if (st < q_steps + kv_steps) {
-        p = k0 + (long long)(st - q_steps) * ks;
+        p = k0 + (st - q_steps) * ks;
         in = (st - q_steps) * PER_WARP + sub < a.Hkv;
       } else {
-        p = v0 + (long long)(st - q_steps - kv_steps) * vs;
+        p = v0 + (st - q_steps - kv_steps) * vs;
         in = (st - q_steps - kv_steps) * PER_WARP + sub < a.Hkv;
       }
       if (in) {
@@ -147,7 +142,7 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const
   const long long v_at = (slot >> a.page_log2) * w.v_page_stride + in_page;
   const int pool_step = PER_WARP * D << a.page_log2;
   uint16_t* const o0 = (uint16_t*)w.q_out.p + t * w.q_out.row_stride + sub * w.q_out.head_stride + e0;
-  const int os = PER_WARP * (int)w.q_out.head_stride;
+  const int64_t os = PER_WARP * w.q_out.head_stride;
   pair c[2], s[2], ns[2];
   {
     float cf[4] = {1.f, 1.f, 1.f, 1.f}, sf[4] = {0.f, 0.f, 0.f, 0.f};
@@ -200,7 +195,7 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const
       if (st < q_steps) {
         turned(raw[i], w.q_gamma != nullptr, gq, x);
         if (st * PER_WARP + sub < a.Hq) {
-          uint16_t* const p = o0 + (long long)st * os;
+          uint16_t* const p = o0 + st * os;
           *reinterpret_cast<uint2*>(p) = pack4<BF16>(x[0]);
           *reinterpret_cast<uint2*>(p + (e1 - e0)) = pack4<BF16>(x[1]);
         }
