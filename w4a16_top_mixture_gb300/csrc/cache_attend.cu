@@ -8,24 +8,21 @@
 //   workspace, and the one that counts itself last joins them, in the order of the tiles (in two steps where they are
 //   many). It does so when it has nothing else to do: joining between two items stalled the copies by 5 to 10 us.
 //   Copies. For each of two teams of math warps a warp walks the block table ahead of it and brings 16 tokens x 128
-//   bytes at a time with TMA into the team's ring of 16 KB stages, keys and values in stages of their own, across the
-//   borders of items; queries and gates of the next item with it. One copying warp for both teams issued too slowly
-//   (188 us where two take 183, and 114 against 101 with an e4m3 cache).
+//   bytes at a time (more tokens where their rows are short) with TMA into the team's ring of 16 KB stages, keys and
+//   values in stages of their own, across the borders of items; queries and gates of the next item with it. One copying
+//   warp for both teams issued too slowly (188 us where two take 183, and 114 against 101 with an e4m3 cache).
 //   Products. Heads are the narrow side of the tensor cores' m16n8k16: S^T[tokens x heads] = K Q^T and
 //   O^T[d x heads] = V^T P^T, so that eight query heads fill a tile (tcgen05's 128 rows would leave its results in
-// tensor
-//   memory, a round trip away from the softmax between the products; mma.sync needs a tenth of the tensor cores' time
-//   here). The teams take the tiles in turn, so that one's softmax hides behind the other's products. The four warps of
-//   a team share a tile: each takes 16 tokens (or 32) of S and then its share of the rows d of O. One maximum for the
-//   four, exchanged through shared memory, lets O be kept once.
+//   tensor memory, a round trip away from the softmax between the products; mma.sync needs a tenth of the tensor cores'
+//   time here). The teams take the tiles in turn, so that one's softmax hides behind the other's products. The four
+//   warps of a team share a tile: each takes 16 tokens (or 32, or 64) of S and then its share of the rows d of O. One
+//   maximum for the four, exchanged through shared memory, lets O be kept once.
 // Measured (16 query over 2 key-value heads of 256): 128 requests of 512 to 16000 tokens, 1.19 GB: 179 us, 6.6 TB/s (a
 // plain copy runs at 6.8); 256 requests over an e4m3 cache, 445 MB: 75 us, where a tile's conversions and products
-// leave
-// less slack; one request of 130 tokens: 7.4 us, of which the chain lengths - table - keys takes 3, the launch 2.
-// What is
-// left in between: 5 us until the first keys arrive, up to 8 us of joining, and SMs that do not all get the same
-// bandwidth
-// (on equal shares 48 of them end 10 % later; smaller shares for whoever is done first cost more than they won).
+// leave less slack; one request of 130 tokens: 7.4 us, of which the chain lengths - table - keys takes 3, the launch 2.
+// What is left in between: 5 us until the first keys arrive, up to 8 us of joining, and SMs that do not all get the
+// same bandwidth (on equal shares 48 of them end 10 % later; smaller shares for whoever is done first cost more than
+// they won).
 #include <cuda.h>
 
 #include <atomic>
@@ -78,9 +75,8 @@ struct Shape {
   static constexpr int PP = TN + 8;                         // pitch of P: rows of 8 fall on different banks
   static constexpr int QP = D + 8;                          // pitch of queries and gates
   static constexpr int PART = NH * D + 2 * NH;              // floats of a partial result: O, maxima, sums
-  // of shared memory besides the rings and the lengths: barriers; queries and gates, twice; for each team P,
-  // maxima and sums;
-  // one's results on their way to the other
+  // of shared memory besides the rings and the lengths: barriers; queries and gates, twice; for each team P, maxima and
+  // sums; one's results on their way to the other
   static constexpr int MISC = 1024 + 4 * NH * QP * 2 + TEAMS * (NH * PP * 2 + 2 * WARPS * NH * 4) + NH * D * 4 +
                               (1 + WARPS) * NH * 4;
 };
@@ -143,12 +139,10 @@ __device__ __forceinline__ void named_arrive(int id, int nthreads) {
 }
 
 // ---- the division of the work ----
-// Items come request by request, within a request head by head. An item of n tiles is n + EXTRA units long, for
-// what its
-// beginning and end cost; CTA c takes units c * share .. (c + 1) * share - 1.
-// An even share; but while no item is longer than SHORT, a CTA takes whole items: a split one's parts take longer
-// to join
-// than a few tiles to read (130 tokens of two 256-wide heads: 8.5 us whole, 10.5 us in six parts).
+// Items come request by request, within a request head by head. An item of n tiles is n + EXTRA units long, for what
+// its beginning and end cost; CTA c takes units c * share .. (c + 1) * share - 1.
+// An even share; but while no item is longer than SHORT, a CTA takes whole items: a split one's parts take longer to
+// join than a few tiles to read (130 tokens of two 256-wide heads: 8.5 us whole, 10.5 us in six parts).
 __host__ __device__ inline int even_share(int units, int longest, int ctas) {
   const int even = units > 0 ? (int)(((long long)units + ctas - 1) / ctas) : 1;
   return longest <= SHORT && even < longest ? longest : even;
@@ -170,9 +164,8 @@ struct Place {
   }
 };
 
-// o += V^T P^T over the groups of 16 tokens of one stage, from group g0 of the tile on; the first `left` tokens of
-// the tile
-// count (EDGE). from: the lane's address in the stage, pbase: in P.
+// o += V^T P^T over the groups of 16 tokens of one stage, from group g0 of the tile on; the first `left` tokens of the
+// tile count (EDGE). from: the lane's address in the stage, pbase: in P.
 template <class S, bool EDGE>
 __device__ __forceinline__ void add_values(float (&o)[S::MD][S::NT][4], uint32_t from, uint32_t pbase, int g0, int left,
                                            int t4) {
@@ -239,9 +232,8 @@ struct Split {
   int b, h, c0, c1;
 };
 
-// The parts of a split item, or of a group of CTAs where they are many, that have arrived when this CTA's does:
-// their count
-// is in arrive's word, complete when the last one is there (and then set back).
+// The parts of a split item, or of a group of CTAs where they are many, that have arrived when this CTA's does: their
+// count is in arrive's word, complete when the last one is there (and then set back).
 __device__ __forceinline__ uint32_t* count_of(const AttendArgs& A, const Split& sp, int* n) {
   const int gi = blockIdx.x / GROUP;
   if (sp.c1 - sp.c0 < FLAT) {
@@ -277,9 +269,8 @@ struct Joined {
   uint2 gate[PER];
 
   __device__ __forceinline__ static bool mine(int tid) { return VECS >= STEP || tid < VECS; }
-  // Part i of ia .. ib lies in slot 2 i + (i == i0): i0 is where the item begins. Up to FEW of them come
-  // straight from L2,
-  // every load on its way at once; the order of the sum is that of the parts.
+  // Part i of ia .. ib lies in slot 2 i + (i == i0): i0 is where the item begins. Up to FEW of them come straight from
+  // L2, every load on its way at once; the order of the sum is that of the parts.
   __device__ __forceinline__ void few(const float* parts, int ia, int ib, int i0, int tid) {
     if (!mine(tid)) return;
     float4 v[FEW][PER];
@@ -429,9 +420,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   }
   if (tid <= TEAMS * 16) fence_mbar_init();
   follow_predecessor();
-  // lengths and the running number of tiles: a thread's requests lie side by side, so that all its loads are on
-  // their way
-  // at once
+  // lengths and the running number of tiles: a thread's requests lie side by side, so that all its loads are on their
+  // way at once
   const int each = (A.B + S::THREADS - 1) / S::THREADS, b_begin = tid * each < A.B ? tid * each : A.B;
   const int b_end = b_begin + each < A.B ? b_begin + each : A.B;
   int mine = 0, longest = 0;
@@ -505,8 +495,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, n_rows = 0;                  // n_rows: copies of rows so far, by the first team's warp
     // keys and values are read once, so they leave L2 first (256 requests over an e4m3 cache: 74.9 us, 79.5 us
-    // without);
-    // twice or more where a group's heads are several items
+    // without); twice or more where a group's heads are several items
     const uint64_t policy = A.head_tiles == 1 ? policy_evict_first() : policy_evict_normal();
     bool skip = A.skip_copy && blockIdx.x == 0 && team == 0;
     // Waits until a buffer is free. False: a wait ran out, here or in a math warp, which then no longer waits. Nothing
@@ -540,9 +529,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       ++n_rows;
       return true;
     };
-    // the pages of 32 groups of 16 tokens from a tile on, one to a lane; looked at only when they are used,
-    // which is while
-    // the next 32 are on their way
+    // the pages of 32 groups of 16 tokens from a tile on, one to a lane; looked at only when they are used, which is
+    // while the next 32 are on their way
     auto pages_from = [&](const Place& p) {
       const long long tok = (long long)p.j * TN + lane * 16;
       return tok < s_len[p.b] ? __ldcg(a.tables + (long long)p.b * a.table_stride + (tok >> A.page_log2)) : 0;
@@ -950,9 +938,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     auto d_of = [&](int md, int r) {
       return S::E4M3 ? (wt * MD + md) * 16 + 2 * g + r : (wt * MD + md) * 16 + g + 8 * r;
     };
-    // a part is joined with the others once this CTA has nothing else to do: the item's tiles are those of
-    // CTAs c0 .. c1;
-    // c0 holds its part as the item it leaves, the others as the item they begin in the middle of
+    // a part is joined with the others once this CTA has nothing else to do: the item's tiles are those of CTAs c0 ..
+    // c1; c0 holds its part as the item it leaves, the others as the item they begin in the middle of
     const int which = j0 == 0 ? 1 : 0;
     if (!whole) {
       const Split sp = {at.b, at.h, (t - j0) / share, (t - j0 + at.n - 1) / share};
@@ -1016,6 +1003,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   // ---- joining the split items: the last of an item's parts to arrive joins them
   if (split[0].b < 0 && split[1].b < 0) return;
   if (head_before >= 0) {
+    __threadfence();                 // the others' parts after the count that told of them
     s_flags[3] = 1;
     s_flags[1] = complete(A, split[0], head_before);
   }
@@ -1089,8 +1077,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 using ReplaceFn = CUresult (*)(CUtensorMap*, void*);
 
