@@ -394,6 +394,23 @@ def test_attend_copies_of_several_rows(D, act, cache, Hq, Hkv, page):
     attend_check(d, out, Hq, Hkv, D, act, cache)
 
 
+@pytest.mark.parametrize("lengths", [EDGES, [9000, 0, 20011, 1, 16], [70001]], ids=["edges", "split", "one"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,act,cache,gate", [
+    (32, 1, 128, 16, "bf16", "e4m3", True), (40, 2, 128, 32, "f16", "f16", True), (64, 1, 128, 64, "bf16", "bf16", False),
+    (33, 1, 64, 16, "f16", "e4m3", True), (34, 2, 64, 128, "bf16", "bf16", True), (16, 1, 256, 16, "bf16", "e4m3", True),
+    (24, 2, 256, 64, "f16", "f16", True), (48, 1, 256, 16, "f16", "e4m3", False)])
+def test_attend_wide_groups(lengths, Hq, Hkv, D, page, act, cache, gate):
+    """More query heads to a key-value head than a tile of eight."""
+    torch = torch_()
+    d, n_pages, width = attend_case(lengths, Hq, Hkv, D, page, act, cache, Hq + D, gate)
+    c = lib.PagedCache(Hq, Hkv, D, page, n_pages, len(lengths), width, dtype=act, cache_dtype=cache)
+    out = c.attend(**d)
+    again = c.attend(**d)
+    assert c.status() == (0, 0)
+    attend_check(d, out, Hq, Hkv, D, act, cache)
+    assert torch.equal(out, again)
+
+
 def test_attend_calls_of_alternating_shapes_on_one_handle():
     torch = torch_()
     cases = [attend_case(n, 16, 2, 256, 16, "f16", "f16", 50 + i, width=400) for i, n in enumerate(([5000, 3, 700], [64] * 90, [1], [6000]))]

@@ -37,7 +37,7 @@ constexpr int SHORT = 5;                          // units of an item that is no
 constexpr int GROUP = 10, FLAT = 20;              // CTAs whose parts are joined first; from FLAT + 1 parts on
 constexpr int MAX_CTAS = 1024, COUNT_WORDS = 2048;                               // of the workspace
 static_assert(COUNT_WORDS >= MAX_CTAS + 2 * ((MAX_CTAS + GROUP - 1) / GROUP) && COUNT_WORDS % 4 == 0, "all counts");
-constexpr int PART_MAX = 16 * 256 + 32;           // floats of the largest part
+constexpr int PART_MAX = 32 * 256 + 2 * 32;       // floats of the largest part
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -65,7 +65,12 @@ struct Shape {
   static constexpr int RB = D * (E4M3 ? 1 : 2);             // bytes of a token's row
   // copies are of lines of 128 bytes: CH of them to a row, or LT tokens to a line
   static constexpr int CB = 128, CH = RB < CB ? 1 : RB / CB, LT = RB < CB ? CB / RB : 1;
-  static constexpr int TN = RB >= 512 ? 64 : RB >= 128 ? 128 : 256;   // tokens of a tile
+  static constexpr int TN = RB >= 512 ? 64 : RB >= 128 || NT > 2 ? 128 : 256;   // tokens of a tile
+  // queries as fragments in shared memory, a copy for each team, where registers do not hold them beside the rest (16
+  // heads of 256 over an e4m3 cache of 400 MB: 81 us in registers, 73 us so; of 128: 81.7 and 82.9)
+  static constexpr bool QS = NT > 2 || NT * D >= 512;
+  static constexpr int ROWS = NT * D > 512 ? 1 : 2;         // rows of D copied for each head: q; the gate, if it fits
+  static constexpr int QF = QS ? D / 16 * NT * 32 : 0;      // uint2 of a team's
   static constexpr int MT = TN / 16 / WARPS;                // 16-token tiles of S per warp
   static constexpr int KT = TN / 16;
   static constexpr int GPS = 16384 / (16 * RB) < KT ? 16384 / (16 * RB) : KT;   // 16-token groups of a stage
@@ -77,8 +82,8 @@ struct Shape {
   static constexpr int PART = NH * D + 2 * NH;              // floats of a partial result: O, maxima, sums
   // of shared memory besides the rings and the lengths: barriers; queries and gates, twice; for each team P, maxima and
   // sums; one's results on their way to the other
-  static constexpr int MISC = 1024 + 4 * NH * QP * 2 + TEAMS * (NH * PP * 2 + 2 * WARPS * NH * 4) + NH * D * 4 +
-                              (1 + WARPS) * NH * 4;
+  static constexpr int MISC = 1024 + 2 * ROWS * NH * QP * 2 + TEAMS * QF * 8 +
+                              TEAMS * (NH * PP * 2 + 2 * WARPS * NH * 4) + NH * D * 4 + (1 + WARPS) * NH * 4;
 };
 
 // ---- instructions ----
@@ -396,8 +401,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   volatile int* const s_flags = (int*)(join_full + 2);    // 0: a wait ran out; 1, 2: last to arrive; 3: the first has
   int* const s_scan = (int*)(join_full + 2) + 4;     // [THREADS / 32]
   int* const s_place = s_scan + 32;                  // [3]
-  uint16_t* const s_q = (uint16_t*)(misc + 1024);    // [2][2][NH][QP]: by turns, queries and gates
-  uint16_t* const s_p0 = s_q + 4 * NH * QP;          // [TEAMS][NH][PP]
+  uint16_t* const s_q = (uint16_t*)(misc + 1024);    // [2][ROWS][NH][QP]: by turns, queries and gates
+  uint2* const s_qf0 = (uint2*)(s_q + 2 * S::ROWS * NH * QP);  // [TEAMS][D / 16][NT / 2][lane][2], if QS
+  uint16_t* const s_p0 = (uint16_t*)(s_qf0 + TEAMS * S::QF);   // [TEAMS][NH][PP]
   float* const s_max0 = (float*)(s_p0 + TEAMS * NH * PP);   // [TEAMS][WARPS][NH]
   float* const s_sum0 = s_max0 + TEAMS * WARPS * NH; // [TEAMS][WARPS][NH]
   float* const s_x = s_sum0 + TEAMS * WARPS * NH;    // [NH * D], [NH] maxima, [WARPS][NH] sums
@@ -520,12 +526,15 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       const int h_in = (p.h % A.head_tiles) * NH;
       const int h0 = (p.h / A.head_tiles) * A.group + h_in;
       const int nh = A.group - h_in < NH ? A.group - h_in : NH;
-      if (lane == 0) mbar_expect_tx(&rows_full[buf], nh * D * 2 * (gates ? 2 : 1));
+      if (lane == 0) mbar_expect_tx(&rows_full[buf], nh * D * 2 * (gates && S::ROWS == 2 ? 2 : 1));
       __syncwarp();
-      const int which = lane / NH, h = lane % NH;
-      if (h < nh && (which == 0 || (which == 1 && gates)))
-        bulk_g2s(s_q + ((buf * 2 + which) * NH + h) * QP, rows_at(which ? a.gate : a.q, p.b, h0 + h, 0), D * 2,
-                 &rows_full[buf]);
+#pragma unroll
+      for (int i = lane; i < S::ROWS * NH; i += 32) {
+        const int which = i / NH, h = i % NH;
+        if (h < nh && (which == 0 || gates))
+          bulk_g2s(s_q + ((buf * S::ROWS + which) * NH + h) * QP, rows_at(which ? a.gate : a.q, p.b, h0 + h, 0), D * 2,
+                   &rows_full[buf]);
+      }
       ++n_rows;
       return true;
     };
@@ -600,6 +609,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   const int team = warp / WARPS, wt = warp % WARPS, ttid = tid % MATH;    // a warp and a thread within their team
   uint16_t* const s_p = s_p0 + team * NH * PP;
   float* const s_max = s_max0 + team * WARPS * NH;
+  uint2* const s_qf = s_qf0 + team * S::QF;
   float* const s_sum = s_sum0 + team * WARPS * NH;
   // requests of length 0
   for (int b = blockIdx.x; b < A.B; b += gridDim.x)
@@ -659,7 +669,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     float sf[NT][2];                                           // what a product is multiplied by, for 2^x
     const float ks = S::E4M3 ? __ldcg(a.k_scale + kvh) : 1.f;
     wait_full(&rows_full[n_rows & 1], n_rows >> 1 & 1);
-    const uint16_t* const q_rows = s_q + (n_rows & 1) * 2 * NH * QP;
+    const uint16_t* const q_rows = s_q + (n_rows & 1) * S::ROWS * NH * QP;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (S::E4M3) {
@@ -708,10 +718,40 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             q[ks][nt][i] = pack2<false>(f.x * down, f.y * down);
           }
       }
+      if (S::QS) {
+        // the last tile's barriers are behind every reader of the item before
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          if (ks % WARPS == wt)
+            s_qf[((ks * (NT / 2) + nt / 2) * 32 + lane) * 2 + nt % 2] = make_uint2(q[ks][nt][0], q[ks][nt][1]);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         sf[nt][i] = A.scale * (S::E4M3 ? ks * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + i) * 4) : 1.f);
     }
+
+    if (S::QS) team_barrier<S>(team);
+    // the queries' fragments of step ks
+    auto queries = [&](int ks, uint32_t (&f)[NT][2]) {
+      if (S::QS) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt += 2) {
+          const uint4 v = reinterpret_cast<const uint4*>(s_qf)[(ks * (NT / 2) + nt / 2) * 32 + lane];
+          f[nt][0] = v.x;
+          f[nt][1] = v.y;
+          if (nt + 1 < NT) {
+            f[nt + 1][0] = v.z;
+            f[nt + 1][1] = v.w;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          f[nt][0] = q[ks][nt][0];
+          f[nt][1] = q[ks][nt][1];
+        }
+      }
+    };
 
     float o[MD][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -730,8 +770,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     for (int j = j0 + ((done + team) & 1); j < j1; j += TEAMS) {
       const int left = len - j * TN;                           // tokens of the request from this tile on
       const int groups = left >= TN ? KT : (left + 15) >> 4;
-      // ---- S^T = K Q^T for this warp's groups of 16 tokens; two chains of accumulators, as one would wait for each
-      // product's latency
+      // ---- S^T = K Q^T for this warp's groups of 16 tokens; two chains of accumulators for one or two tiles of heads,
+      // as one would wait for each product's latency
       float s[MT][NT][4], s2[MT][NT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -756,10 +796,13 @@ __global__ void __launch_bounds__(S::THREADS, 1)
               ldsm4(k, (from ^ (c % PER << 4)) + c / PER * (16 * S::CB));
 #pragma unroll
               for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(k[i], lo[i], hi[i]);
+              uint32_t f0[NT][2], f1[NT][2];
+              queries(c, f0);
+              queries(c + 1, f1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma16816<false>(s[mt][nt], lo[0], lo[1], hi[0], hi[1], q[c][nt][0], q[c][nt][1]);
-                mma16816<false>(s2[mt][nt], lo[2], lo[3], hi[2], hi[3], q[c + 1][nt][0], q[c + 1][nt][1]);
+                mma16816<false>(s[mt][nt], lo[0], lo[1], hi[0], hi[1], f0[nt][0], f0[nt][1]);
+                mma16816<false>(NT > 2 ? s[mt][nt] : s2[mt][nt], lo[2], lo[3], hi[2], hi[3], f1[nt][0], f1[nt][1]);
               }
             }
           } else {
@@ -767,10 +810,12 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             for (int ks = 0; ks < D / 16; ++ks) {
               uint32_t k[4];
               ldsm4(k, (from ^ (2 * ks % PER << 4)) + 2 * ks / PER * (16 * S::CB));
+              uint32_t f[NT][2];
+              queries(ks, f);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma16816<S::MMA_BF16>(ks & 1 ? s2[mt][nt] : s[mt][nt], k[0], k[1], k[2], k[3], q[ks][nt][0],
-                                      q[ks][nt][1]);
+                mma16816<S::MMA_BF16>(NT <= 2 && ks & 1 ? s2[mt][nt] : s[mt][nt], k[0], k[1], k[2], k[3], f[nt][0],
+                                      f[nt][1]);
             }
           }
         }
@@ -785,7 +830,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float x = (s[mt][nt][i] + s2[mt][nt][i]) * sf[nt][i & 1];
+            const float x = (NT > 2 ? s[mt][nt][i] : s[mt][nt][i] + s2[mt][nt][i]) * sf[nt][i & 1];
             s[mt][nt][i] = edge && tok + g + (i >> 1) * 8 >= left ? -INFINITY : x;
           }
       }
@@ -962,7 +1007,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
               float y = o[md][nt][2 * r + i] * f;
               const int d = d_of(md, r);
               if (a.gate.p) {
-                y = gated(y, unpack2<S::BF16>(q_rows[(NH + h) * QP + d]).x);
+                y = gated(y, unpack2<S::BF16>(S::ROWS == 2 ? q_rows[(NH + h) * QP + d]
+                                                           : __ldcg(rows_at(a.gate, at.b, h0 + h, d))).x);
               }
               *rows_at(a.out, at.b, h0 + h, d) = (uint16_t)pack2<S::BF16>(y, 0.f);
             }
@@ -1161,7 +1207,11 @@ cudaError_t run(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
 
 template <int D, bool BF16, bool E4M3>
 cudaError_t run_heads(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
-  return A.group <= 8 ? run<Shape<D, BF16, E4M3, 1>>(c, A, ctas, st) : run<Shape<D, BF16, E4M3, 2>>(c, A, ctas, st);
+  // the fewest heads to an item that keep a group in one, up to 32: an item more reads the cache once more, from L2 (32
+  // over 1 heads of 128, 400 MB: 74 us as one item, 124 as two; of 256: 85 and 124, over an e4m3 cache 117 and 136)
+  if (A.group <= 8) return run<Shape<D, BF16, E4M3, 1>>(c, A, ctas, st);
+  if (A.group <= 16) return run<Shape<D, BF16, E4M3, 2>>(c, A, ctas, st);
+  return run<Shape<D, BF16, E4M3, 4>>(c, A, ctas, st);
 }
 template <int D>
 cudaError_t run_types(const CacheShape& c, AttendArgs& A, int ctas, cudaStream_t st) {
