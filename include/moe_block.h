@@ -357,10 +357,11 @@ MOE_API int moe_cache_write(moe_cache_t *cache, const moe_cache_write_t *write, 
  * moe_cache_write has put it there): with g = the key-value head of query head h (h / (n_heads / n_kv_heads)),
  *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j[g]) v_j[g]  * sigmoid(gate[b][h])       (gate.p NULL: no gate)
  * and 0 for a request of length 0. Values of an e4m3 cache are multiplied by k_scale and v_scale. Softmax statistics
- * and sums are fp32; the weights of the second product are rounded to act_dtype (fp16 with an e4m3 cache), the output
- * once to act_dtype. What lies in a page past the request's end has no effect, NaN included. Table entries past the
- * request's pages are not read. A page id outside the pool reads as zeros, and a length outside
- * 0 .. max_pages * page_size as the nearest of the two; both are reported by moe_cache_get_status. */
+ * and sums are fp32; the weights of the second product are rounded to act_dtype, or to fp16 with an e4m3 cache (in fp16
+ * weights below 2^-29 of the highest lose bits and those below 2^-40 count as none), the output once to act_dtype.
+ * What lies in a page past the request's end has no effect, NaN included. Table entries past the request's pages are
+ * not read. A page id outside the pool reads as zeros, and a length outside 0 .. max_pages * page_size as the nearest
+ * of the two; both are reported by moe_cache_get_status. */
 typedef struct {
   moe_rows_t q, gate;                          /* [B][n_heads][head_dim] */
   moe_rows_t out;                              /* written; may be q or gate itself */

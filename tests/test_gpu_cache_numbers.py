@@ -1,0 +1,94 @@
+"""Numbers at the edges of the paged cache's formats, against the float64 oracle: long flat tails under one high score,
+scores so large that fp32 cannot hold a step between them.
+
+Bounds. As in test_gpu_cache.py: a score is off by d = D 2^-23 sum|q k| scale, a weight by its rounding u(p), the sum over n
+tokens by (n / 16 + 32) 2^-23, all relative to S = sum p |v|; the output by u(out) |out|. Weights of the second product are
+fp16, as high as 2^15 for the highest score, unless the cache is bf16: those below 2^-14 have a half step of 2^-25, which is
+2^-40 of the highest, so each value adds 2^-40 |v| times the highest weight, which is less than 1."""
+import numpy as np
+import pytest
+
+import oracle.cache_oracle as O
+from tests.test_gpu_cache import U, dt, f64, gen_of, ints, randn, torch_
+from w4a16_top_mixture_gb300 import build, lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    lib.load_library()
+
+
+def one_request(k, v, act, cache, page=16):
+    """A handle, and tables, lengths and pools of one request with the keys and values k, v [n, Hkv, D]."""
+    torch = torch_()
+    n, Hkv, D = k.shape
+    pages = -(-n // page)
+
+    def pool(x):
+        x = torch.cat([x, torch.zeros(pages * page - n, Hkv, D, device="cuda")])
+        return x.view(pages, page, Hkv, D).transpose(1, 2).contiguous().to(dt(cache))
+    d = dict(tables=torch.arange(pages, dtype=torch.int32, device="cuda")[None], lengths=ints([n]), k_cache=pool(k), v_cache=pool(v))
+    if cache == "e4m3":
+        d["k_scale"], d["v_scale"] = torch.ones(Hkv, device="cuda"), torch.ones(Hkv, device="cuda")
+    return d, lambda Hq: lib.PagedCache(Hq, Hkv, D, page, pages, 1, pages, dtype=act, cache_dtype=cache)
+
+
+def reference(d, q, scale, gate=None):
+    k, v = f64(d["k_cache"]), f64(d["v_cache"])
+    if "k_scale" in d:
+        k, v = k * f64(d["k_scale"])[:, None, None], v * f64(d["v_scale"])[:, None, None]
+    return O.attend(f64(q), d["tables"].cpu().numpy(), d["lengths"].tolist(), k, v, scale, f64(gate))
+
+
+TAILS = [(n, gap, sink, D, Hq, act, cache) for n, gap, sink in ((30000, 18.0, 0), (20000, 16.0, 19999), (20000, 20.0, 9000), (700, 14.0, 0))
+         for D, Hq, act, cache in ((64, 8, "f16", "f16"), (64, 8, "bf16", "e4m3"), (64, 32, "f16", "e4m3"), (128, 16, "f16", "f16"),
+                                   (128, 8, "bf16", "e4m3"), (128, 24, "bf16", "bf16"), (256, 4, "f16", "f16"), (256, 16, "bf16", "e4m3"))]
+
+
+@pytest.mark.parametrize("n,gap,sink,D,Hq,act,cache", TAILS + [(131071, 18.0, 0, 64, 2, "f16", "f16"), (131071, 18.0, 0, 64, 2, "bf16", "e4m3")])
+def test_attend_keeps_the_tail_under_one_high_score(n, gap, sink, D, Hq, act, cache):
+    """One key `gap` above all others with a value of 0, so that the others make the whole output."""
+    torch = torch_()
+    g = gen_of(n + D + Hq)
+    k, v = torch.randn(n, 1, D, generator=g, device="cuda") * 0.5, torch.randn(n, 1, D, generator=g, device="cuda") * 8 + 64
+    k[..., 0] = 0
+    k[sink], v[sink] = 0, 0
+    k[sink, 0, 0] = gap
+    d, handle = one_request(k, v, act, cache)
+    scale = 0.125
+    q = torch.randn(1, Hq, D, generator=g, device="cuda") * (0.5 * (64 / D) ** 0.5)
+    q[..., 0] = 8                                             # scale * q . k = gap for the high key
+    q = q.to(dt(act))
+    c = handle(Hq)
+    out = c.attend(q, scale=scale, **d)
+    assert c.status() == (0, 0)
+    want, size, mag = reference(d, q, scale)
+    up = U["bf16"] if cache == "bf16" else U["f16"]
+    lost = 0.0 if cache == "bf16" else 2.0 ** -40 * np.abs(f64(d["v_cache"])).sum((0, 2))     # [1, D]: one head of keys
+    tol = U[act] * np.abs(want) + size * (up + 2 * D * 2.0 ** -23 * mag + (n / 16 + 32) * 2.0 ** -23) + lost + 2.0 ** -24
+    err = np.abs(f64(out) - want)
+    assert (err <= tol).all(), ((err / tol).max(), (err / size).max())
+
+
+@pytest.mark.parametrize("act,cache", [("f16", "f16"), ("bf16", "e4m3"), ("bf16", "bf16")])
+@pytest.mark.parametrize("high", [2.0 ** 12, 2.0 ** 19, 2.0 ** 22, 2.0 ** 25, -(2.0 ** 22), -(2.0 ** 25)])
+def test_attend_scores_past_a_step_of_fp32(high, act, cache):
+    """Scores of `high` up to 2^28, equal for two or all of the keys: the mean of those keys' values."""
+    torch = torch_()
+    g = gen_of(3)
+    n, D, Hq = 900, 64, 5
+    k, v = torch.zeros(n, 1, D, device="cuda"), torch.randn(n, 1, D, generator=g, device="cuda") * 4
+    k[..., 0] = 16 if high < 0 else -16
+    k[300, 0, 0] = k[777, 0, 0] = 16
+    d, handle = one_request(k, v, act, cache)
+    q = torch.zeros(1, Hq, D, device="cuda")
+    q[0, :, 0] = torch.tensor([1.0, 1.5, 1.25, 7.0, 3.0], device="cuda")
+    out = handle(Hq).attend(q.to(dt(act)), scale=high / 16, **d)
+    v = f64(d["v_cache"]).reshape(-1, D)[:n]
+    mine = v if high < 0 else v[[300, 777]]
+    want, size = mine.mean(0), np.abs(mine).mean(0)
+    up = U["bf16"] if cache == "bf16" else U["f16"]
+    assert (np.abs(f64(out)[0] - want) <= U[act] * np.abs(want) + size * (up + (n / 16 + 32) * 2.0 ** -23) + 2.0 ** -24).all()

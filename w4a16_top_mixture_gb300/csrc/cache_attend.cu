@@ -76,6 +76,9 @@ struct Shape {
   static constexpr int GPS = 16384 / (16 * RB) < KT ? 16384 / (16 * RB) : KT;   // 16-token groups of a stage
   static constexpr int GROUP_BYTES = 16 * RB, STAGE = GPS * GROUP_BYTES;
   static constexpr int MD = D / 16 / WARPS;                 // 16-row tiles of O per warp
+  // the highest weight is 2^LIFT: fp16 loses bits below 2^-14, and a long flat tail under one high score can be most of
+  // the output (131071 tokens 17.4 below one whose value is 0: 16 % off without). The factor is in O and the sums alike.
+  static constexpr float LIFT = MMA_BF16 ? 0.f : 15.f;
   static constexpr int EXTRA = 2;                           // units of an item, see the division of the work
   static constexpr int PP = TN + 8;                         // pitch of P: rows of 8 fall on different banks
   static constexpr int QP = D + 8;                          // pitch of queries and gates
@@ -122,6 +125,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// The base of a tile's weights 2^(score - base): LIFT below its maximum, where fp32 holds that step (so that no weight
+// passes 2^LIFT), else the maximum.
+template <class S>
+__device__ __forceinline__ float base_of(float top) {
+  const float b = top - S::LIFT;
+  return top - b == S::LIFT ? b : top;
 }
 // y * sigmoid(x): exp and quotient good to a few 2^-23
 __device__ __forceinline__ float gated(float y, float x) { return __fdividef(y, 1.f + __expf(-x)); }
@@ -835,7 +845,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           }
       }
 
-      // ---- the tile's maximum for each head
+      // ---- the tile's maximum for each head, as the base of its weights: so are all maxima from here on
       float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -851,7 +861,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       if (lane < 4)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          *reinterpret_cast<float2*>(&s_max[wt * NH + nt * 8 + 2 * t4]) = make_float2(top[nt][0], top[nt][1]);
+          *reinterpret_cast<float2*>(&s_max[wt * NH + nt * 8 + 2 * t4]) =
+              make_float2(base_of<S>(top[nt][0]), base_of<S>(top[nt][1]));
       team_barrier<S>(team);
       bool moved = false;
       float c[NT][2];
@@ -883,7 +894,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             }
           l[nt][i] = l[nt][i] * c[nt][i] + sum;
         }
-        // P^T for the second product: 16 bits a weight, an error of half a step of the cache's own type
+        // P^T for the second product: 16 bits a weight, an error of half a step of the products' type, which adds up
+        // like the values' own rounding; fp16 keeps all its bits for weights down to 2^-29 of the highest
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
