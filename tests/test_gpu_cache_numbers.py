@@ -92,3 +92,29 @@ def test_attend_scores_past_a_step_of_fp32(high, act, cache):
     want, size = mine.mean(0), np.abs(mine).mean(0)
     up = U["bf16"] if cache == "bf16" else U["f16"]
     assert (np.abs(f64(out)[0] - want) <= U[act] * np.abs(want) + size * (up + (n / 16 + 32) * 2.0 ** -23) + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 3), (128, 16), (256, 8), (256, 17)])
+@pytest.mark.parametrize("e", [-125, -110, -60, -3, 0, 40, 99, 100, 101, 110, 124])
+def test_attend_bf16_queries_of_any_size_over_e4m3(e, D, Hq):
+    """Queries around 2^e with scales that bring the scores back to a few units: the products run in fp16, for which the
+    queries are scaled by a power of two. Elements below 2^-14 of a head's largest lose bits there: half a step is 2^-25,
+    so a score is off by 2^-25 max|q| sum|k| scale more."""
+    torch = torch_()
+    g = gen_of(e + D)
+    n = 333
+    k, v = (torch.randn(n, 1, D, generator=g, device="cuda") * 8 for _ in range(2))
+    d, handle = one_request(k, v, "bf16", "e4m3")
+    half = e // 2
+    d["k_scale"].fill_(0.125 * 2.0 ** -half)
+    scale = D ** -0.5 * 2.0 ** (half - e)
+    q = (torch.randn(1, Hq, D, generator=g, device="cuda").clamp(-3.5, 3.5) * 1.1).to(torch.bfloat16).double() * 2.0 ** e
+    q = q.to(torch.bfloat16)
+    c = handle(Hq)
+    out = c.attend(q, scale=scale, **d)
+    want, size, mag = reference(d, q, scale)
+    keys = np.abs(f64(d["k_cache"])).sum(-1).max() * f64(d["k_scale"])[0]
+    delta = D * 2.0 ** -23 * mag + 2.0 ** -25 * np.abs(f64(q)).max(-1, keepdims=True) * keys * scale
+    tol = U["bf16"] * np.abs(want) + size * (U["f16"] + 2 * delta + (n / 16 + 32) * 2.0 ** -23) + 2.0 ** -24
+    err = np.abs(f64(out) - want)
+    assert (err <= tol).all(), ((err / tol).max(), (err / size).max())

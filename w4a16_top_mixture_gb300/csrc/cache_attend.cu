@@ -716,10 +716,10 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           }
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const int e = (__float_as_int(m) >> 23) - 127;
-        const bool fine = e > -100 && e < 100;
-        up = fine ? __int_as_float((127 + e) << 23) : 1.f;
-        const float down = fine ? __int_as_float((127 - e) << 23) : 1.f;
+        // (0, infinities and NaN stay what they are at any power; past 2^126 its inverse would lose bits)
+        const int e = min(max((__float_as_int(m) >> 23) - 127, -126), 126);
+        up = __int_as_float((127 + e) << 23);
+        const float down = __int_as_float((127 - e) << 23);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
