@@ -118,3 +118,28 @@ def test_attend_bf16_queries_of_any_size_over_e4m3(e, D, Hq):
     tol = U["bf16"] * np.abs(want) + size * (U["f16"] + 2 * delta + (n / 16 + 32) * 2.0 ** -23) + 2.0 ** -24
     err = np.abs(f64(out) - want)
     assert (err <= tol).all(), ((err / tol).max(), (err / size).max())
+
+
+@pytest.mark.parametrize("n", [1, 40000])
+@pytest.mark.parametrize("D,Hq,act,cache", [(64, 8, "bf16", "bf16"), (64, 2, "bf16", "e4m3"), (256, 24, "bf16", "bf16"), (128, 9, "f16", "f16")])
+def test_attend_gates_far_from_zero(n, D, Hq, act, cache):
+    """exp(-|gate|) in fp32 is off by 2 + 1.17 |gate| steps, 2^-16 at its smallest normal value, then by steps of 2^-149; all
+    tokens hold one value, so the output is that value times the sigmoid."""
+    torch = torch_()
+    g = gen_of(D + n)
+    v = torch.full((n, 1, D), 448.0 if cache == "e4m3" else 1e4, device="cuda")
+    d, handle = one_request(torch.randn(n, 1, D, generator=g, device="cuda"), v, act, cache)
+    if cache == "e4m3":
+        d["v_scale"].fill_(20.0)
+    gates = [-float("inf"), -110, -104, -100, -95, -90, -89, -88.5, -88, -87.5, -87, -80, -40, -11, -3, 0, 2, 17, 87, 88, 89, 104, float("inf")]
+    gate = torch.tensor(gates, device="cuda").repeat(-(-Hq * D // len(gates)))[:Hq * D].view(1, Hq, D).to(dt(act))
+    q = randn(g, (1, Hq, D), act)
+    out = handle(Hq).attend(q, gate=gate, **d)
+    y = float(f64(d["v_cache"])[0, 0, 0, 0]) * (20.0 if cache == "e4m3" else 1.0)
+    x = f64(gate)
+    want = y * np.exp(np.minimum(x, 0)) / (1 + np.exp(-np.abs(x)))
+    up = U["bf16"] if cache == "bf16" else U["f16"]
+    least = 2.0 ** -134 if act == "bf16" else 2.0 ** -25
+    tol = want * (U[act] + up + (n / 16 + 32) * 2.0 ** -23 + 2.0 ** -16) + 3 * y * 2.0 ** -149 + least
+    err = np.abs(f64(out) - want)
+    assert (err <= tol).all(), (x[err > tol], f64(out)[err > tol], want[err > tol])
