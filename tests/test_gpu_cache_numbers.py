@@ -143,3 +143,26 @@ def test_attend_gates_far_from_zero(n, D, Hq, act, cache):
     tol = want * (U[act] + up + (n / 16 + 32) * 2.0 ** -23 + 2.0 ** -16) + 3 * y * 2.0 ** -149 + least
     err = np.abs(f64(out) - want)
     assert (err <= tol).all(), (x[err > tol], f64(out)[err > tol], want[err > tol])
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_write_codes_are_those_of_an_fp32_division(D, act):
+    """Code for code, over scales from fp32's smallest to its largest; the same for keys that nothing norms or turns."""
+    torch = torch_()
+    scales = [1e-45, 1e-39, 2.0 ** -130, 1.3e-38, 1e-30, 3e-20, 6e-20, 0.0123, 0.7, 1.0, 0.0137, 1.7e19, 2e19, 1e30, 3e38]
+    T, H, page = 400, len(scales), 32
+    g = gen_of(D)
+    s = torch.tensor(scales, device="cuda")
+    near = (torch.randn(2, T, H, D, generator=g, device="cuda").double() * 100 * s.double()[:, None]).to(dt(act))
+    wild = (torch.randn(2, T, H, D, generator=g, device="cuda").double()
+            * 2.0 ** (torch.rand(2, T, H, D, generator=g, device="cuda") * 260 - 134).double()).to(dt(act))
+    x = torch.where(torch.rand(2, T, H, D, generator=g, device="cuda") < 0.5, near, wild)
+    x[:, :5, :, 7:] = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan")], device="cuda").to(dt(act))[None, :, None, None]
+    pool = torch.zeros(2, -(-T // page), H, page, D, device="cuda").to(dt("e4m3"))
+    c = lib.PagedCache(H, H, D, page, pool.shape[1], 1, 1, dtype=act, cache_dtype="e4m3")
+    slots = torch.randperm(T, generator=g, device="cuda").int()
+    c.write(None, x[0], x[1], slots, slots, pool[0], pool[1], k_scale=s, v_scale=s)
+    got = pool.float().transpose(2, 3).reshape(2, -1, H, D)[:, slots.long()].cpu()
+    want = (x.float().cpu() / s.cpu()[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).float()
+    assert ((got == want) | (got.isnan() & want.isnan())).all()

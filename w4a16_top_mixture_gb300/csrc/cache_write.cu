@@ -59,16 +59,31 @@ __device__ __forceinline__ void weights(const void* gamma, int e, float offset, 
   g[0] = make_pair2(offset + f0.x, offset + f0.y);
   g[1] = make_pair2(offset + f1.x, offset + f1.y);
 }
-// x / s with r = 1 / s: the product corrected by its remainder, as good as a division, in three operations. Where it is
-// past what e4m3 holds the correction could only lose an infinity.
-__device__ __forceinline__ float quotient(float x, float s, float r) {
-  const float q = x * r;
-  return fabsf(q) < 1e30f ? fmaf(fmaf(-q, s, x), r, q) : q;
-}
-__device__ __forceinline__ uint32_t quantize4(const pair x[2], float s, float r) {
+// A head's scale of e4m3 codes s, its reciprocal, and the power of two that it and what it divides are multiplied by
+// first: beyond 2^-64 .. 2^64 the reciprocal, or the remainder below, could leave fp32's normal range.
+struct CodeScale {
+  float s, r, by;
+  __device__ __forceinline__ explicit CodeScale(float scale) {
+    by = fabsf(scale) < 0x1p-64f ? 0x1p100f : fabsf(scale) > 0x1p64f ? 0x1p-100f : 1.f;
+    s = scale * by;
+    r = 1.f / s;
+  }
+  // x / s in three operations: Markstein's correction of a product with the reciprocal by its remainder. Where the
+  // product is past what e4m3 holds the correction could only lose an infinity.
+  __device__ __forceinline__ float quotient(float x) const {
+    const float q = x * r;
+    return fabsf(q) < 1e30f ? fmaf(fmaf(-q, s, x), r, q) : q;
+  }
+};
+__device__ __forceinline__ uint32_t quantize4(pair x[2], const CodeScale& c) {
+  if (c.by != 1.f) {
+    const pair by = make_pair2(c.by, c.by);
+    x[0] = mul2(x[0], by);
+    x[1] = mul2(x[1], by);
+  }
   const float2 f0 = split(x[0]), f1 = split(x[1]);
-  const float2 a = make_float2(quotient(f0.x, s, r), quotient(f0.y, s, r));
-  const float2 b = make_float2(quotient(f1.x, s, r), quotient(f1.y, s, r));
+  const float2 a = make_float2(c.quotient(f0.x), c.quotient(f0.y));
+  const float2 b = make_float2(c.quotient(f1.x), c.quotient(f1.y));
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
@@ -217,9 +232,9 @@ __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const
       }
       if (!in) continue;
       if (E4M3) {
-        const float sc = __ldcg((is_k ? w.k_scale : w.v_scale) + h), r = 1.f / sc;
-        *reinterpret_cast<uint32_t*>((uint8_t*)pool + at) = quantize4(x[0], sc, r);
-        *reinterpret_cast<uint32_t*>((uint8_t*)pool + at + (e1 - e0)) = quantize4(x[1], sc, r);
+        const CodeScale sc(__ldcg((is_k ? w.k_scale : w.v_scale) + h));
+        *reinterpret_cast<uint32_t*>((uint8_t*)pool + at) = quantize4(x[0], sc);
+        *reinterpret_cast<uint32_t*>((uint8_t*)pool + at + (e1 - e0)) = quantize4(x[1], sc);
       } else {
         *reinterpret_cast<uint2*>((uint16_t*)pool + at) = out[0];
         *reinterpret_cast<uint2*>((uint16_t*)pool + at + (e1 - e0)) = out[1];
