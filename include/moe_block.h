@@ -377,11 +377,12 @@ typedef struct {
 
 MOE_API int moe_cache_attend(moe_cache_t *cache, const moe_cache_attend_t *attend, void *stream);
 
-/* Waits for the stream of the handle's last call and returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side
- * wait of an attend call ran out: its outputs are wrong, and later attend calls leave theirs unwritten until this call
- * has reported it) or MOE_ERR_INVALID_ARG (a call met a value on the device
- * that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits: 1 a wait ran out,
- * 2 a length, 4 a page id or slot, 8 a free_state out of range. */
+/* Waits for the handle's device (for graphs that hold calls of the handle too, on whichever stream they run) and returns
+ * MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side wait of an attend call ran out: its outputs are wrong, and later
+ * attend calls leave theirs unwritten until this call has reported it) or MOE_ERR_INVALID_ARG (a call met a value on the
+ * device that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits: 1 a wait ran
+ * out, 2 a length, 4 a page id or slot, 8 a free_state out of range. Not while a stream is being captured: a wait for
+ * the device ends the capture with an error. */
 MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);
 
 /* Test control of the attention's bounded device waits: timeout_us = microseconds a wait for a copy may last before it

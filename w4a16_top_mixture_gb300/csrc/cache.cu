@@ -21,7 +21,6 @@ struct moe_cache {
   size_t workspace_bytes = 0;
   uint64_t timeout_ns = 500ull * 1000 * 1000;
   int skip_copy = 0;
-  cudaStream_t last_stream = nullptr;
 };
 
 namespace {
@@ -154,17 +153,33 @@ extern "C" int moe_cache_create(const moe_cache_config_t* cfg, moe_cache_t** out
   return MOE_OK;
 }
 
-extern "C" void moe_cache_destroy(moe_cache_t* c) {
-  if (!c) return;
-  cudaDeviceSynchronize();
-  cudaFree(c->mem);
-  delete c;
-}
-
 // a handle works on the device that was current when it was made
 static bool on_device(const moe_cache* c) {
   int dev = -1;
   return cudaGetDevice(&dev) == cudaSuccess && dev == c->dev;
+}
+// makes a device current for as long as it lives
+struct OnDevice {
+  int before = -1;
+  cudaError_t e;
+  explicit OnDevice(int dev) {
+    e = cudaGetDevice(&before);
+    if (e == cudaSuccess && before == dev) before = -1;
+    else if (e == cudaSuccess) e = cudaSetDevice(dev);
+  }
+  ~OnDevice() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
+extern "C" void moe_cache_destroy(moe_cache_t* c) {
+  if (!c) return;
+  {
+    const OnDevice on(c->dev);
+    cudaDeviceSynchronize();
+    cudaFree(c->mem);
+  }
+  delete c;
 }
 
 extern "C" int moe_debug_cache_check(const moe_cache_config_t* cfg, const moe_cache_plan_t* p,
@@ -183,7 +198,6 @@ extern "C" int moe_cache_plan(moe_cache_t* c, const moe_cache_plan_t* p, void* s
   const int r = check_plan(c->cfg, *p);
   if (r != MOE_OK) return r;
   if (!on_device(c)) return MOE_ERR_INVALID_ARG;
-  c->last_stream = (cudaStream_t)stream;
   const cudaError_t e = cache_plan_launch(c->S, *p, c->arrivals, c->status, c->num_sms, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_plan");
 }
@@ -193,7 +207,6 @@ extern "C" int moe_cache_write(moe_cache_t* c, const moe_cache_write_t* w, void*
   const int r = check_write(c->S, *w);
   if (r != MOE_OK || w->n_rows == 0) return r;
   if (!on_device(c)) return MOE_ERR_INVALID_ARG;
-  c->last_stream = (cudaStream_t)stream;
   const cudaError_t e = cache_write_launch(c->S, *w, c->turns, c->status, c->num_sms, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_write");
 }
@@ -203,7 +216,6 @@ extern "C" int moe_cache_attend(moe_cache_t* c, const moe_cache_attend_t* a, voi
   const int r = check_attend(c->cfg, c->S, *a);
   if (r != MOE_OK || a->n_requests == 0) return r;
   if (!on_device(c)) return MOE_ERR_INVALID_ARG;
-  c->last_stream = (cudaStream_t)stream;
   const CacheAttendState w{c->workspace, c->status, c->num_sms, c->timeout_ns, c->skip_copy};
   c->skip_copy = 0;
   const cudaError_t e = cache_attend_launch(c->S, *a, w, (cudaStream_t)stream);
@@ -219,12 +231,16 @@ extern "C" int moe_cache_debug_set_wait(moe_cache_t* c, uint32_t timeout_us, int
 
 extern "C" int moe_cache_get_status(moe_cache_t* c, uint32_t* flags) {
   if (!c) return MOE_ERR_INVALID_ARG;
-  cudaError_t e = cudaStreamSynchronize(c->last_stream);
+  const OnDevice on(c->dev);
+  // the whole device: a captured call runs on whatever stream its graph is launched on, which the handle never sees
+  cudaError_t e = on.e;
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   uint32_t st = 0;
   if (e == cudaSuccess) e = cudaMemcpy(&st, c->status, 4, cudaMemcpyDeviceToHost);
-  // the counts of parts too: a call that gave up may have left some behind
-  if (e == cudaSuccess && st) e = cudaMemset(c->mem, 0, CTL_WORDS * 4);
-  if (e == cudaSuccess && st) e = cudaMemset(c->workspace, 0, c->workspace_bytes);
+  if (e == cudaSuccess && st) e = cudaMemset(c->status, 0, 4);
+  // the counts of parts too where a call gave up, which may have left some behind
+  if (e == cudaSuccess && st & CACHE_BAD_WAIT) e = cudaMemset(c->mem, 0, CTL_WORDS * 4);
+  if (e == cudaSuccess && st & CACHE_BAD_WAIT) e = cudaMemset(c->workspace, 0, c->workspace_bytes);
   if (e == cudaSuccess && st) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return report_cuda(e, "moe_cache_get_status");
   if (flags) *flags = st;

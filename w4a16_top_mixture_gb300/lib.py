@@ -589,6 +589,9 @@ class PagedCache:
         _check(self.lib.moe_cache_debug_set_wait(self.h, int(timeout_us), int(bool(skip_copy))), "set_wait")
 
     def status(self):
+        """(status, flags) of the calls so far, on any stream and in graphs: waits for the device (moe_cache_get_status)."""
+        if self._torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("status() waits for the device: not while a stream is being captured")
         f = ctypes.c_uint32(0)
         s = self.lib.moe_cache_get_status(self.h, ctypes.byref(f))
         return s, f.value
