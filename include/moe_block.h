@@ -304,7 +304,8 @@ MOE_API void moe_cache_destroy(moe_cache_t *cache);
 /* One step's block tables and slot maps. Request b has lengths[b] tokens in the cache and brings new_tokens[b] more
  * (0: none this step; NULL: one for every request; negative: the request has ended). The rows of the step's token
  * batch are the requests' new tokens one after another: starts[b] .. starts[b + 1] - 1 are request b's.
- *   - An ended request's pages go to the tail of the ring and its length becomes 0.
+ *   - An ended request's pages go to the tail of the ring and its length becomes 0. Pages past the ring's room (a page
+ *     that several requests hold or that is free already) are left out.
  *   - A request whose tokens need further pages takes them from the head of the ring, in the order of the requests,
  *     into the next entries of its table row. Pages given back in a call are not taken in the same call. When the
  *     running need passes the pages that are free, that request and every later one that needs a page are refused:
@@ -313,7 +314,8 @@ MOE_API void moe_cache_destroy(moe_cache_t *cache);
  *     the last token get -1 and 0.
  * lengths_out may be lengths, free_state_out may be free_state (with them in place a captured graph steps the cache);
  * no other buffers may overlap. A page id outside the pool gives slot -1; it, a length outside
- * 0 .. max_pages * page_size and a free_state outside the ring are reported by moe_cache_get_status. */
+ * 0 .. max_pages * page_size, a free_state outside the ring and pages past its room are reported by
+ * moe_cache_get_status. */
 typedef struct {
   const int32_t *lengths;      /* [B] */
   const int32_t *new_tokens;   /* [B], or NULL */
@@ -381,8 +383,8 @@ MOE_API int moe_cache_attend(moe_cache_t *cache, const moe_cache_attend_t *atten
  * MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side wait of an attend call ran out: its outputs are wrong, and later
  * attend calls leave theirs unwritten until this call has reported it) or MOE_ERR_INVALID_ARG (a call met a value on the
  * device that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits: 1 a wait ran
- * out, 2 a length, 4 a page id or slot, 8 a free_state out of range. Not while a stream is being captured: a wait for
- * the device ends the capture with an error. */
+ * out, 2 a length, 4 a page id or slot, 8 a free_state out of range or more pages than the ring has room for. Not while
+ * a stream is being captured: a wait for the device ends the capture with an error. */
 MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);
 
 /* Test control of the attention's bounded device waits: timeout_us = microseconds a wait for a copy may last before it

@@ -73,12 +73,15 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
     head = count = 0;
     if (tid == 0) atomicOr(a.status, CACHE_BAD_STATE);
   }
+  // what the ring can take back: all that the requests hold, if no page is in two places
+  const int room = a.n_pages - count;
   // where each request's rows end
   unsigned long long sum = 0, total;
 #pragma unroll
   for (int i = 0; i < EACH; ++i) sum += nw[i] > 0 ? nw[i] : 0;
   unsigned long long end = block_scan(sum, ws[0], &total);
-  // the pages it needs (low half: those that fit take at most n_rows / 16 + B) and gives back (high half)
+  // the pages it needs (BACK bits: those that fit take at most n_rows / 16 + B) and gives back (at most 2^32 in all)
+  constexpr int BACK = 30;
   int held[EACH], need[EACH];
   bool fits[EACH];
   sum = 0;
@@ -91,7 +94,7 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
     held[i] = good ? (int)(((long long)len[i] + ps - 1) >> a.page_log2) : 0;
     fits[i] = in && good && nw[i] >= 0 && len[i] + n <= max_len && end <= (unsigned long long)a.rows;
     need[i] = fits[i] ? (int)((len[i] + n + ps - 1) >> a.page_log2) - held[i] : 0;
-    sum += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(in && nw[i] < 0 ? held[i] : 0) << 32;
+    sum += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(in && nw[i] < 0 ? held[i] : 0) << BACK;
     if (in) {
       s_end[b] = (int)(end < 0x7FFFFFFF ? end : 0x7FFFFFFF);
       s_len[b] = len[i];
@@ -99,19 +102,21 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
     }
   }
   unsigned long long at = block_scan(sum, ws[1], &total);
-  const uint32_t back_total = (uint32_t)(total >> 32);
+  const int back_total = (int)(total >> BACK < (unsigned)room ? total >> BACK : (unsigned)room);
+  if (tid == 0 && total >> BACK > (unsigned)room) atomicOr(a.status, CACHE_BAD_STATE);
   int refused = 0, taken = 0;
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
     const int b = tid * EACH + i;
     if (b < a.B) {
-      const uint32_t need_at = (uint32_t)at, back_at = (uint32_t)(at >> 32);
+      const uint32_t need_at = (uint32_t)at & ((1u << BACK) - 1);
+      const unsigned long long back_at = at >> BACK;
       const bool done = nw[i] < 0, ok = fits[i] && (need[i] == 0 || need_at + (uint32_t)need[i] <= (uint32_t)count);
       const int back_to = (int)(back_at < 0x3FFFFFFFu ? back_at : 0x3FFFFFFFu);
       s_at[b] = ok ? (need[i] ? (int)need_at : 0) : done ? -2 - back_to : -1;
       if (ok) taken += need[i];
       else if (!done) ++refused;
-      at += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(done ? held[i] : 0) << 32;
+      at += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(done ? held[i] : 0) << BACK;
     }
   }
   refused = __reduce_add_sync(0xFFFFFFFFu, refused);
@@ -136,9 +141,11 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
         for (int j = held + lane; j < want; j += 32)
           row[j] = __ldcg(p.free_pages + ((uint32_t)head + (uint32_t)at + (uint32_t)(j - held)) % (uint32_t)a.n_pages);
       } else if (at <= -2 && len > 0 && len <= max_len) {
-        const int held = (int)(((long long)len + ps - 1) >> a.page_log2);
-        const uint32_t to = (uint32_t)head + (uint32_t)count + (uint32_t)(-2 - at);
-        for (int j = lane; j < held; j += 32) p.free_pages[(to + (uint32_t)j) % (uint32_t)a.n_pages] = __ldcg(row + j);
+        const int back = -2 - at, held = (int)(((long long)len + ps - 1) >> a.page_log2);
+        // no further than the ring has room: beyond lie entries that this call's requests take
+        const int fit = held < room - back ? held : room - back;
+        const uint32_t to = (uint32_t)head + (uint32_t)count + (uint32_t)back;
+        for (int j = lane; j < fit; j += 32) p.free_pages[(to + (uint32_t)j) % (uint32_t)a.n_pages] = __ldcg(row + j);
       }
     }
   }
@@ -184,8 +191,7 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
   if (tid == 0) {
     p.starts[0] = 0;
     p.free_state_out[0] = (int)((uint32_t)(head + s_taken) % (uint32_t)a.n_pages);
-    const long long left = (long long)count - s_taken + back_total;
-    p.free_state_out[1] = (int)(left < a.n_pages ? left : a.n_pages);
+    p.free_state_out[1] = count - s_taken + back_total;
     p.free_state_out[2] = s_refused;
     if (a.in_place && gridDim.x > 1) *a.arrivals = 0;
   }
