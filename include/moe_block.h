@@ -291,7 +291,7 @@ typedef struct {
 } moe_cache_config_t;
 
 /* A [rows][heads][head_dim] tensor: strides in elements, the innermost 1. The pointer is 16-byte aligned and the
- * strides are multiples of 8, below 2^40 (rows) and 2^30 (heads). */
+ * strides are multiples of 8, below 2^40 (rows) and 2^30 (heads) either way, the rows times their stride 2^60 at most. */
 typedef struct {
   const void *p;
   int64_t row_stride, head_stride;
@@ -337,11 +337,11 @@ MOE_API int moe_cache_plan(moe_cache_t *cache, const moe_cache_plan_t *plan, voi
  *   (y_i, y_{i+R/2}) <- (y_i cos a - y_{i+R/2} sin a, y_{i+R/2} cos a + y_i sin a),  a = positions[t] * theta^(-2i/R),
  *   0 <= i < R/2.
  * q goes to q_out (which may be q itself), k and v to slots[t] of the pools; a negative slot writes neither. The
- * pools are 16-byte aligned, their page strides in elements, multiples of head_dim and of 128 bytes (n_kv_heads *
- * page_size * head_dim when the pool is dense). With an e4m3 cache k / k_scale[head] and v / v_scale[head] are
- * rounded to e4m3, values past its range to its largest. Computed in fp32 (an angle's whole turns exactly), rounded
- * once. q may be NULL together with q_out. Slots past the pool write nothing and are reported by
- * moe_cache_get_status. Rows with the same slot race. */
+ * pools are 16-byte aligned, their page strides in elements, multiples of head_dim and of 128 bytes, below 2^38 and
+ * 2^60 / n_pages at most (n_kv_heads * page_size * head_dim when the pool is dense). With an e4m3 cache
+ * k / k_scale[head] and v / v_scale[head] are rounded to e4m3, values past its range to its largest. Computed in fp32
+ * (an angle's whole turns exactly), rounded once. q may be NULL together with q_out. Slots past the pool write nothing
+ * and are reported by moe_cache_get_status. Rows with the same slot race. */
 typedef struct {
   moe_rows_t q, k, v;                          /* [T][n_heads | n_kv_heads][head_dim] */
   moe_rows_t q_out;                            /* written */

@@ -61,15 +61,17 @@ int check_config(const moe_cache_config_t& c, CacheShape* S) {
 }
 
 bool aligned(const void* p, int n) { return p && ((uintptr_t)p & (n - 1)) == 0; }
-// strides are bounded so that no row's byte offset can pass 63 bits
-bool rows_ok(const moe_rows_t& r) {
-  return aligned(r.p, 16) && r.row_stride % 8 == 0 && r.head_stride % 8 == 0 &&
-         llabs(r.row_stride) < (int64_t)1 << 40 && llabs(r.head_stride) < (int64_t)1 << 30;
+// strides and their products with the rows and pages are bounded, so that every offset in bytes fits 62 bits
+bool within(int64_t v, int bits) { return v > -((int64_t)1 << bits) && v < (int64_t)1 << bits; }
+constexpr int64_t FARTHEST = (int64_t)1 << 60;
+bool rows_ok(const moe_rows_t& r, int64_t n) {
+  return aligned(r.p, 16) && r.row_stride % 8 == 0 && r.head_stride % 8 == 0 && within(r.row_stride, 40) &&
+         within(r.head_stride, 30) && llabs(r.row_stride) <= FARTHEST / n;
 }
 // a pool: 16-byte aligned, pages that do not overlap, whole rows of D and whole lines of 128 bytes apart
 bool pool_ok(const CacheShape& S, const void* p, int64_t page_stride) {
   return aligned(p, 16) && page_stride >= ((int64_t)S.Hkv << S.page_log2) * S.D && page_stride < (int64_t)1 << 38 &&
-         page_stride % S.D == 0 &&
+         page_stride <= FARTHEST / S.n_pages && page_stride % S.D == 0 &&
          (S.e4m3 ? page_stride : 2 * page_stride) % 128 == 0;
 }
 bool scales_ok(const CacheShape& S, const float* k, const float* v) {
@@ -94,8 +96,9 @@ int check_plan(const moe_cache_config_t& cfg, const moe_cache_plan_t& p) {
 int check_write(const CacheShape& S, const moe_cache_write_t& w) {
   if (w.n_rows < 0 || w.n_rows > (int64_t)1 << 24) return MOE_ERR_INVALID_ARG;
   if (w.n_rows == 0) return MOE_OK;
-  if ((w.q.p != nullptr) != (w.q_out.p != nullptr) || (w.q.p && (!rows_ok(w.q) || !rows_ok(w.q_out))) ||
-      !rows_ok(w.k) || !rows_ok(w.v) || ((uintptr_t)w.q_gamma & 15) || ((uintptr_t)w.k_gamma & 15) ||
+  if ((w.q.p != nullptr) != (w.q_out.p != nullptr) ||
+      (w.q.p && (!rows_ok(w.q, w.n_rows) || !rows_ok(w.q_out, w.n_rows))) || !rows_ok(w.k, w.n_rows) ||
+      !rows_ok(w.v, w.n_rows) || ((uintptr_t)w.q_gamma & 15) || ((uintptr_t)w.k_gamma & 15) ||
       !aligned(w.positions, 4) || !aligned(w.slots, 4) || !pool_ok(S, w.k_cache, w.k_page_stride) ||
       !pool_ok(S, w.v_cache, w.v_page_stride) || !scales_ok(S, w.k_scale, w.v_scale))
     return MOE_ERR_INVALID_ARG;
@@ -104,9 +107,10 @@ int check_write(const CacheShape& S, const moe_cache_write_t& w) {
 int check_attend(const moe_cache_config_t& cfg, const CacheShape& S, const moe_cache_attend_t& a) {
   if (a.n_requests < 0 || a.n_requests > cfg.max_requests || !isfinite(a.scale)) return MOE_ERR_INVALID_ARG;
   if (a.n_requests == 0) return MOE_OK;
-  if (!rows_ok(a.q) || (a.gate.p && !rows_ok(a.gate)) || !rows_ok(a.out) || !aligned(a.tables, 4) ||
-      !table_ok(cfg, a.table_stride) || !aligned(a.lengths, 4) || !pool_ok(S, a.k_cache, a.k_page_stride) ||
-      !pool_ok(S, a.v_cache, a.v_page_stride) || !scales_ok(S, a.k_scale, a.v_scale))
+  if (!rows_ok(a.q, a.n_requests) || (a.gate.p && !rows_ok(a.gate, a.n_requests)) || !rows_ok(a.out, a.n_requests) ||
+      !aligned(a.tables, 4) || !table_ok(cfg, a.table_stride) || !aligned(a.lengths, 4) ||
+      !pool_ok(S, a.k_cache, a.k_page_stride) || !pool_ok(S, a.v_cache, a.v_page_stride) ||
+      !scales_ok(S, a.k_scale, a.v_scale))
     return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
