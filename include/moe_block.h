@@ -374,7 +374,7 @@ typedef struct {
   int64_t k_page_stride, v_page_stride;
   const float *k_scale, *v_scale;              /* [n_kv_heads]: both given with an e4m3 cache, NULL otherwise */
   int64_t n_requests;                          /* B: 0..max_requests */
-  double scale;                                /* finite; usually 1 / sqrt(head_dim) */
+  double scale;                                /* up to 2.35e38 either way; usually 1 / sqrt(head_dim) */
 } moe_cache_attend_t;
 
 MOE_API int moe_cache_attend(moe_cache_t *cache, const moe_cache_attend_t *attend, void *stream);

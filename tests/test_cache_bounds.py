@@ -31,3 +31,14 @@ def test_pages_whose_offsets_pass_63_bits(L):  # noqa: F811
         cfg = dict(n_pages=n_pages)
         for change in (dict(k_page=page), dict(v_page=page)):
             assert status(L, cfg=cfg, write=change) == want and status(L, cfg=cfg, attend=change) == want, (n_pages, page)
+
+
+@pytest.mark.parametrize("scale", [1e39, -1e39, 3.4e38, -2.5e38, 1e300])
+def test_attend_refuses_scales_that_fp32_does_not_hold(L, scale):  # noqa: F811
+    """The kernels multiply scores by scale * log2(e) in fp32: past 2.35e38 that is an infinity, and the outputs NaN."""
+    assert status(L, attend=dict(scale=scale)) == -1
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0625, 1e-300, 1e30, 2.3e38, -2.3e38])
+def test_attend_takes_every_other_scale(L, scale):  # noqa: F811
+    assert status(L, attend=dict(scale=scale)) == 0

@@ -26,6 +26,7 @@ struct moe_cache {
 namespace {
 
 constexpr int CTL_WORDS = 64;
+constexpr double MAX_SCALE = 2.35e38;    // of the attention, which multiplies it by log2(e) in fp32
 
 int check_config(const moe_cache_config_t& c, CacheShape* S) {
   if (c.n_kv_heads < 1 || c.n_kv_heads > 256 || c.n_heads < 1 || c.n_heads % c.n_kv_heads ||
@@ -105,7 +106,7 @@ int check_write(const CacheShape& S, const moe_cache_write_t& w) {
   return MOE_OK;
 }
 int check_attend(const moe_cache_config_t& cfg, const CacheShape& S, const moe_cache_attend_t& a) {
-  if (a.n_requests < 0 || a.n_requests > cfg.max_requests || !isfinite(a.scale)) return MOE_ERR_INVALID_ARG;
+  if (a.n_requests < 0 || a.n_requests > cfg.max_requests || !(fabs(a.scale) <= MAX_SCALE)) return MOE_ERR_INVALID_ARG;
   if (a.n_requests == 0) return MOE_OK;
   if (!rows_ok(a.q, a.n_requests) || (a.gate.p && !rows_ok(a.gate, a.n_requests)) || !rows_ok(a.out, a.n_requests) ||
       !aligned(a.tables, 4) || !table_ok(cfg, a.table_stride) || !aligned(a.lengths, 4) ||
