@@ -496,11 +496,12 @@ class PagedCache:
     def _pool(self, t):
         if t.dtype is self.cache_dtype and t.shape == self.pool_shape and t.get_device() == self._dev:
             page, head, row, one = t.stride()
-            _, heads, p, d = self.pool_shape
-            if one == 1 and row == d and (head == p * d or heads == 1):
-                return t.data_ptr(), max(page, heads * p * d)
-        raise ValueError(f"want a pool {self.cache_dtype} {self.pool_shape} on {self.device}, dense within a page; got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+            n, heads, p, d = self.pool_shape
+            dense = heads * p * d
+            if one == 1 and row == d and (head == p * d or heads == 1) and (page >= dense or n == 1):
+                return t.data_ptr(), page if n > 1 else dense
+        raise ValueError(f"want a pool {self.cache_dtype} {self.pool_shape} on {self.device}, dense within a page, pages "
+                         f"apart; got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
     def _scales(self, k, v):
         return (self._vector(k, self.n_kv_heads, self._f32) if k is not None else 0,
