@@ -56,3 +56,12 @@ def test_a_pool_of_one_page_may_have_any_page_stride(cache):
         one = x.kc[:1].as_strided((1, 2, 16, 64), (stride, 1024, 64, 1))
         cache.attend(x.q, x.tables, x.lengths, one, one)
         assert lib.CACHE_ATTEND.unpack(cache.calls.pop()[1])[14:16] == (2 * 16 * 64,) * 2
+
+
+def test_an_output_without_queries_is_refused(cache):
+    """It came back as the result of the call, unwritten."""
+    x = inputs()
+    with pytest.raises(ValueError):
+        cache.write(None, x.k, x.v, x.positions, x.slots, x.kc, x.vc, q_out=x.q)
+    assert not cache.calls
+    assert cache.write(None, x.k, x.v, x.positions, x.slots, x.kc, x.vc) is None and len(cache.calls) == 1

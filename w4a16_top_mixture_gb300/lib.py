@@ -553,6 +553,8 @@ class PagedCache:
             out_rows = q_out.data_ptr(), heads * self.head_dim, self.head_dim
         elif q is not None:
             out_rows = self._rows(q_out, heads, T)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
         kc, ks = self._pool(k_cache)
         vc, vs = self._pool(v_cache)
         args = CACHE_WRITE.pack(
