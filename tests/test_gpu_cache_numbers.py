@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 
 import oracle.cache_oracle as O
-from tests.test_gpu_cache import U, dt, f64, gen_of, ints, randn, torch_
+from tests.test_gpu_cache import U, attend_case, dt, f64, gen_of, ints, randn, torch_
 from w4a16_top_mixture_gb300 import build, lib
 
 pytestmark = pytest.mark.gpu
@@ -166,3 +166,38 @@ def test_write_codes_are_those_of_an_fp32_division(D, act):
     got = pool.float().transpose(2, 3).reshape(2, -1, H, D)[:, slots.long()].cpu()
     want = (x.float().cpu() / s.cpu()[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).float()
     assert ((got == want) | (got.isnan() & want.isnan())).all()
+
+
+@pytest.mark.parametrize("n,shortest,longest,empty,Hq,Hkv,D,page,act,cache,gate", [
+    (128, 512, 16000, 5, 16, 2, 256, 16, "f16", "f16", True), (61, 1, 9000, 1, 32, 8, 128, 64, "bf16", "bf16", False),
+    (256, 300, 5000, 11, 16, 2, 256, 32, "bf16", "e4m3", True)])
+def test_attend_full_batches_with_empty_slots(n, shortest, longest, empty, Hq, Hkv, D, page, act, cache, gate):
+    """A server's batches, every request compared, with a reference in 64 bits on the GPU. Nothing but the rows past a
+    request's end and the page that nobody holds is NaN."""
+    torch = torch_()
+    lengths = [int(round(shortest * (longest / shortest) ** (i / (n - 1)))) for i in range(n)]
+    lengths[:empty] = [0] * empty
+    lengths = [lengths[i] for i in np.random.default_rng(n).permutation(n)]
+    d, n_pages, width = attend_case(lengths, Hq, Hkv, D, page, act, cache, n, gate)
+    c = lib.PagedCache(Hq, Hkv, D, page, n_pages, n, width, dtype=act, cache_dtype=cache)
+    out = c.attend(**d)
+    assert c.status() == (0, 0)
+    one = torch.ones(Hkv, device="cuda")
+    ks, vs = (d.get(x, one).double()[:, None, None] for x in ("k_scale", "v_scale"))
+    up = U["bf16"] if cache == "bf16" else U["f16"]
+    for b, m in enumerate(lengths):
+        if not m:
+            assert (out[b] == 0).all()
+            continue
+        ids = d["tables"][b, :-(-m // page)].long()
+        k, v = (torch.stack([pool[i] for i in ids.tolist()]).transpose(0, 1).reshape(Hkv, -1, D)[:, :m].double() for pool in (d["k_cache"], d["v_cache"]))
+        k, v = k * ks, v * vs
+        q = d["q"][b].double().view(Hkv, -1, D)
+        p = torch.softmax(q @ k.transpose(1, 2) * D ** -0.5, -1)
+        mag = (q.abs() @ k.abs().transpose(1, 2)).amax(-1, keepdim=True) * D ** -0.5
+        want, size = p @ v, p @ v.abs()
+        if gate:
+            sg = torch.sigmoid(d["gate"][b].double()).view(Hkv, -1, D)
+            want, size = want * sg, size * sg
+        tol = U[act] * want.abs() + size * (up + 2 * D * 2.0 ** -23 * mag + (m / 16 + 32) * 2.0 ** -23) + 2.0 ** -24
+        assert ((out[b].double().view(Hkv, -1, D) - want).abs() <= tol).all(), (b, m)
