@@ -126,13 +126,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The base of a tile's weights 2^(score - base): LIFT below its maximum, where fp32 holds that step (so that no weight
-// passes 2^LIFT), else the maximum.
+// The base of a tile's weights 2^(score - base): LIFT below its maximum, rounded up so that none passes 2^LIFT.
 template <class S>
-__device__ __forceinline__ float base_of(float top) {
-  const float b = top - S::LIFT;
-  return top - b == S::LIFT ? b : top;
-}
+__device__ __forceinline__ float base_of(float top) { return __fsub_ru(top, S::LIFT); }
 // y * sigmoid(x) from e = exp(-|x|), which cannot overflow: __expf is off by 2 + 1.17 |x| steps at most, 2^-16 at the
 // smallest normal e, well under half a step of a 16-bit output; the quotient by 1 + e <= 2 by two.
 __device__ __forceinline__ float gated(float y, float x) {
