@@ -66,10 +66,11 @@ struct CodeScale {
   __device__ __forceinline__ explicit CodeScale(float scale) {
     by = fabsf(scale) < 0x1p-64f ? 0x1p100f : fabsf(scale) > 0x1p64f ? 0x1p-100f : 1.f;
     s = scale * by;
-    r = 1.f / s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
   }
-  // x / s in three operations: Markstein's correction of a product with the reciprocal by its remainder. Where the
-  // product is past what e4m3 holds the correction could only lose an infinity.
+  // x / s in three operations: Markstein's correction of a product with the reciprocal by its remainder. A reciprocal
+  // good to one step does: the product is off by two, and the corrected one by 2^-21 of a step before its rounding.
+  // Where the product is past what e4m3 holds the correction could only lose an infinity.
   __device__ __forceinline__ float quotient(float x) const {
     const float q = x * r;
     return fabsf(q) < 1e30f ? fmaf(fmaf(-q, s, x), r, q) : q;
