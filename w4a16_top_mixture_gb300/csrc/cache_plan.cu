@@ -80,8 +80,8 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
 #pragma unroll
   for (int i = 0; i < EACH; ++i) sum += nw[i] > 0 ? nw[i] : 0;
   unsigned long long end = block_scan(sum, ws[0], &total);
-  // the pages it needs (BACK bits: those that fit take at most n_rows / 16 + B) and gives back (at most 2^32 in all)
-  constexpr int BACK = 30;
+  // the pages it needs (low half: those that fit take at most n_rows / 16 + B) and gives back (high half: below 2^32 but
+  // where 2^12 requests hold 2^20 pages each, of a pool's 2^27; then none of them count)
   int held[EACH], need[EACH];
   bool fits[EACH];
   sum = 0;
@@ -94,7 +94,7 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
     held[i] = good ? (int)(((long long)len[i] + ps - 1) >> a.page_log2) : 0;
     fits[i] = in && good && nw[i] >= 0 && len[i] + n <= max_len && end <= (unsigned long long)a.rows;
     need[i] = fits[i] ? (int)((len[i] + n + ps - 1) >> a.page_log2) - held[i] : 0;
-    sum += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(in && nw[i] < 0 ? held[i] : 0) << BACK;
+    sum += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(in && nw[i] < 0 ? held[i] : 0) << 32;
     if (in) {
       s_end[b] = (int)(end < 0x7FFFFFFF ? end : 0x7FFFFFFF);
       s_len[b] = len[i];
@@ -102,21 +102,19 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
     }
   }
   unsigned long long at = block_scan(sum, ws[1], &total);
-  const int back_total = (int)(total >> BACK < (unsigned)room ? total >> BACK : (unsigned)room);
-  if (tid == 0 && total >> BACK > (unsigned)room) atomicOr(a.status, CACHE_BAD_STATE);
+  const uint32_t back_total = (uint32_t)(total >> 32);
   int refused = 0, taken = 0;
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
     const int b = tid * EACH + i;
     if (b < a.B) {
-      const uint32_t need_at = (uint32_t)at & ((1u << BACK) - 1);
-      const unsigned long long back_at = at >> BACK;
+      const uint32_t need_at = (uint32_t)at, back_at = (uint32_t)(at >> 32);
       const bool done = nw[i] < 0, ok = fits[i] && (need[i] == 0 || need_at + (uint32_t)need[i] <= (uint32_t)count);
       const int back_to = (int)(back_at < 0x3FFFFFFFu ? back_at : 0x3FFFFFFFu);
       s_at[b] = ok ? (need[i] ? (int)need_at : 0) : done ? -2 - back_to : -1;
       if (ok) taken += need[i];
       else if (!done) ++refused;
-      at += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(done ? held[i] : 0) << BACK;
+      at += (unsigned long long)need[i] | (unsigned long long)(uint32_t)(done ? held[i] : 0) << 32;
     }
   }
   refused = __reduce_add_sync(0xFFFFFFFFu, refused);
@@ -191,8 +189,9 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
   if (tid == 0) {
     p.starts[0] = 0;
     p.free_state_out[0] = (int)((uint32_t)(head + s_taken) % (uint32_t)a.n_pages);
-    p.free_state_out[1] = count - s_taken + back_total;
+    p.free_state_out[1] = count - s_taken + (back_total < (uint32_t)room ? (int)back_total : room);
     p.free_state_out[2] = s_refused;
+    if (back_total > (uint32_t)room) atomicOr(a.status, CACHE_BAD_STATE);
     if (a.in_place && gridDim.x > 1) *a.arrivals = 0;
   }
 }
