@@ -10,16 +10,18 @@
 //   Copies. For each of two teams of math warps a warp walks the block table ahead of it and brings 16 tokens x 128
 //   bytes at a time (more tokens where their rows are short) with TMA into the team's ring of 16 KB stages, keys and
 //   values in stages of their own, across the borders of items; queries and gates of the next item with it. One copying
-//   warp for both teams issued too slowly (188 us where two take 183, and 114 against 101 with an e4m3 cache).
+//   warp for both teams issued too slowly (a first form of the kernel: 188 us where two take 183, and 114 against 101
+//   with an e4m3 cache).
 //   Products. Heads are the narrow side of the tensor cores' m16n8k16: S^T[tokens x heads] = K Q^T and
 //   O^T[d x heads] = V^T P^T, so that eight query heads fill a tile (tcgen05's 128 rows would leave its results in
-//   tensor memory, a round trip away from the softmax between the products; mma.sync needs a tenth of the tensor cores'
-//   time here). The teams take the tiles in turn, so that one's softmax hides behind the other's products. The four
+//   tensor memory, a round trip away from the softmax between the products; with eight heads mma.sync keeps the tensor
+//   cores 10 % of the time over a 16-bit cache and 17 % over e4m3; 32 heads are four times the products for each byte).
+//   The teams take the tiles in turn, so that one's softmax hides behind the other's products. The four
 //   warps of a team share a tile: each takes 16 tokens (or 32, or 64) of S and then its share of the rows d of O. One
 //   maximum for the four, exchanged through shared memory, lets O be kept once.
-// Measured (16 query over 2 key-value heads of 256): 128 requests of 512 to 16000 tokens, 1.19 GB: 179 us, 6.6 TB/s (a
-// plain copy runs at 6.8); 256 requests over an e4m3 cache, 445 MB: 75 us, where a tile's conversions and products
-// leave less slack; one request of 130 tokens: 7.4 us, of which the chain lengths - table - keys takes 3, the launch 2.
+// Measured (16 query over 2 key-value heads of 256): 128 requests of 512 to 16000 tokens, 1.19 GB: 180 us, 6.6 TB/s (a
+// plain copy runs at 6.8); 256 requests over an e4m3 cache, 445 MB: 74 us, where a tile's conversions and products
+// leave less slack; one request of 130 tokens: 7.5 us, of which the chain lengths - table - keys takes 3, the launch 2.
 // What is left in between: 5 us until the first keys arrive, up to 8 us of joining, and SMs that do not all get the
 // same bandwidth (on equal shares 48 of them end 10 % later; smaller shares for whoever is done first cost more than
 // they won).
@@ -34,7 +36,10 @@ namespace moe {
 namespace {
 
 constexpr int SHORT = 5;                          // units of an item that is not split without need
-constexpr int GROUP = 10, FLAT = 20;              // CTAs whose parts are joined first; from FLAT + 1 parts on
+// CTAs whose parts are joined first, from FLAT + 1 parts on. One request of 131072 tokens, 16 over 2 heads of 256, 76
+// parts each: 51.4 us; groups of 5 53.2, of 20 52.3, none 57.7; 32 over 1 heads of 128, 147 parts: 34.6, 38.3, 35.6 and
+// 79. Three of 65536, 8 over 2 heads of 128, some 25 parts: 39.4, 39.3, 38.3 and 38.4.
+constexpr int GROUP = 10, FLAT = 20;
 constexpr int MAX_CTAS = 1024, COUNT_WORDS = 2048;                               // of the workspace
 static_assert(COUNT_WORDS >= MAX_CTAS + 2 * ((MAX_CTAS + GROUP - 1) / GROUP) && COUNT_WORDS % 4 == 0, "all counts");
 constexpr int PART_MAX = 32 * 256 + 2 * 32;       // floats of the largest part
