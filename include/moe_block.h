@@ -291,7 +291,8 @@ typedef struct {
 } moe_cache_config_t;
 
 /* A [rows][heads][head_dim] tensor: strides in elements, the innermost 1. The pointer is 16-byte aligned and the
- * strides are multiples of 8, below 2^40 (rows) and 2^30 (heads) either way, the rows times their stride 2^60 at most. */
+ * strides are multiples of 8, below 2^40 (rows) and 2^30 (heads) either way, the rows times their stride 2^60 at
+ * most. */
 typedef struct {
   const void *p;
   int64_t row_stride, head_stride;
@@ -340,7 +341,8 @@ MOE_API int moe_cache_plan(moe_cache_t *cache, const moe_cache_plan_t *plan, voi
  * pools are 16-byte aligned, their page strides in elements, multiples of head_dim and of 128 bytes, below 2^38 and
  * 2^60 / n_pages at most (n_kv_heads * page_size * head_dim when the pool is dense). With an e4m3 cache
  * k / k_scale[head] and v / v_scale[head] are rounded to e4m3, values past its range to its largest. Computed in fp32
- * (an angle's whole turns exactly), rounded once. q may be NULL together with q_out. Slots past the pool write nothing
+ * (an angle's whole turns exactly; squares too, so that heads with elements past 2^59, or with norm_eps 0 none above
+ * 2^-60, do not come out), rounded once. q may be NULL together with q_out. Slots past the pool write nothing
  * and are reported by moe_cache_get_status. Rows with the same slot race. */
 typedef struct {
   moe_rows_t q, k, v;                          /* [T][n_heads | n_kv_heads][head_dim] */
@@ -379,12 +381,12 @@ typedef struct {
 
 MOE_API int moe_cache_attend(moe_cache_t *cache, const moe_cache_attend_t *attend, void *stream);
 
-/* Waits for the handle's device (for graphs that hold calls of the handle too, on whichever stream they run) and returns
- * MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side wait of an attend call ran out: its outputs are wrong, and later
- * attend calls leave theirs unwritten until this call has reported it) or MOE_ERR_INVALID_ARG (a call met a value on the
- * device that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits: 1 a wait ran
- * out, 2 a length, 4 a page id or slot, 8 a free_state out of range or more pages than the ring has room for. Not while
- * a stream is being captured: a wait for the device ends the capture with an error. */
+/* Waits for the handle's device (for graphs that hold calls of the handle too, on whichever stream they run) and
+ * returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side wait of an attend call ran out: its outputs are wrong,
+ * and later attend calls leave theirs unwritten until this call has reported it) or MOE_ERR_INVALID_ARG (a call met a
+ * value on the device that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits:
+ * 1 a wait ran out, 2 a length, 4 a page id or slot, 8 a free_state out of range or more pages than the ring has room
+ * for. Not while a stream is being captured: a wait for the device ends the capture with an error. */
 MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);
 
 /* Test control of the attention's bounded device waits: timeout_us = microseconds a wait for a copy may last before it

@@ -81,8 +81,9 @@ struct Shape {
   static constexpr int GPS = 16384 / (16 * RB) < KT ? 16384 / (16 * RB) : KT;   // 16-token groups of a stage
   static constexpr int GROUP_BYTES = 16 * RB, STAGE = GPS * GROUP_BYTES;
   static constexpr int MD = D / 16 / WARPS;                 // 16-row tiles of O per warp
-  // the highest weight is 2^LIFT: fp16 loses bits below 2^-14, and a long flat tail under one high score can be most of
-  // the output (131071 tokens 17.4 below one whose value is 0: 16 % off without). The factor is in O and the sums alike.
+  // the highest weight is 2^LIFT: fp16 loses bits below 2^-14, and a long flat tail under one high score can be most
+  // of the output (131071 tokens 17.4 below one whose value is 0: 16 % off without). The factor is in O and the sums
+  // alike.
   static constexpr float LIFT = MMA_BF16 ? 0.f : 15.f;
   static constexpr int EXTRA = 2;                           // units of an item, see the division of the work
   static constexpr int PP = TN + 8;                         // pitch of P: rows of 8 fall on different banks

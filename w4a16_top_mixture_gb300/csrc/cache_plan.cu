@@ -80,8 +80,8 @@ __global__ void k_cache_plan(const __grid_constant__ PlanArgs a) {
 #pragma unroll
   for (int i = 0; i < EACH; ++i) sum += nw[i] > 0 ? nw[i] : 0;
   unsigned long long end = block_scan(sum, ws[0], &total);
-  // the pages it needs (low half: those that fit take at most n_rows / 16 + B) and gives back (high half: below 2^32 but
-  // where 2^12 requests hold 2^20 pages each, of a pool's 2^27; then none of them count)
+  // the pages it needs (low half: those that fit take at most n_rows / 16 + B) and gives back (high half: below 2^32
+  // but where 2^12 requests hold 2^20 pages each, of a pool's 2^27; then none of them count)
   int held[EACH], need[EACH];
   bool fits[EACH];
   sum = 0;

@@ -97,9 +97,9 @@ __device__ __forceinline__ uint32_t quantize4(pair x[2], const CodeScale& c) {
 // exactly, as integers (fp32 loses its fraction), and its upper 32 bits are the argument. What bounds the kernel is the
 // bytes, then the instructions and whole waves of warps: the loads of three steps are on their way while three others
 // are worked on, nothing synchronises, and a row is cut in two where that fills the last wave. 8192 rows of 32 + 2 x 8
-// heads of 128 (201 MB): 41 us, 4.9 TB/s; with four steps ahead and four CTAs to an SM 64 us, with whole rows 43 us; into
-// an e4m3 cache (185 MB) 52 us. 80 registers are a cap that every variant spills at (20 to 40 bytes); the heads of a
-// warp's step make the same sines, two or four times over.
+// heads of 128 (201 MB): 41 us, 4.9 TB/s; with four steps ahead and four CTAs to an SM 64 us, with whole rows 43 us;
+// into an e4m3 cache (185 MB) 52 us. 80 registers are a cap that every variant spills at (20 to 40 bytes); the heads of
+// a warp's step make the same sines, two or four times over.
 template <int D, bool BF16, bool E4M3>
 __global__ void __launch_bounds__(WRITE_THREADS, WRITE_CTAS) k_cache_write(const __grid_constant__ WriteArgs a) {
   constexpr int LANES = D / 8, PER_WARP = 32 / LANES;
