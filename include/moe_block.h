@@ -381,12 +381,145 @@ typedef struct {
 
 MOE_API int moe_cache_attend(moe_cache_t *cache, const moe_cache_attend_t *attend, void *stream);
 
+/* ---- steps that bring several tokens of a request: drafted trees and chains, chunks of a prompt ----
+ *
+ * moe_cache_plan and moe_cache_write take any number of new tokens of a request; the calls below attend to them, keep what
+ * was right of them, and let requests share pages. A step with drafted trees: moe_cache_plan (slots, starts, lengths),
+ * moe_cache_tree (masks, and the positions for moe_cache_write), moe_cache_write and moe_cache_attend_tree for each layer,
+ * moe_cache_keep once for all layers.
+ *
+ * The new tokens of request b are the last n = starts[b + 1] - starts[b] of its lengths[b] tokens in the cache, and the
+ * rows starts[b] .. starts[b + 1] - 1 of the step; P = lengths[b] - n are older. `slots`, where it is given, is the plan's:
+ * a request whose first row has a negative slot was refused, has lengths[b] tokens all of them older, and its rows have no
+ * token. starts that do not ascend or pass n_rows, more new tokens than the call takes and the like are reported by
+ * moe_cache_get_status (bit 16), a length below n as bit 2; such a request is left out (where starts descend, rows may be
+ * two requests', and get either one's output). */
+
+/* Allocates what these calls need besides, for up to max_new (1..256) new tokens of a request: once for a handle, before
+ * the first of them (MOE_ERR_NOT_LOADED otherwise). Waits for the device. MOE_ERR_INVALID_ARG: a NULL handle, one that has
+ * it already, another device than the handle's; MOE_ERR_UNSUPPORTED: max_new out of range. */
+MOE_API int moe_cache_reserve(moe_cache_t *cache, int max_new);
+
+/* Ancestor masks and positions of trees. parents[r] is the place among its request's new tokens of row r's parent, which
+ * comes before it; -1 for a child of the last older token. Bit j % 64 of masks[r][j / 64] is set where new token j is row
+ * r's ancestor or itself; positions[r] = P + its depth. Rows of refused requests, of those left out and past the last
+ * token get masks and positions of 0. A parent that does not come before its child counts as -1 and is reported. */
+typedef struct {
+  const int32_t *parents;      /* [n_rows] */
+  const int32_t *starts;       /* [B + 1] */
+  const int32_t *lengths;      /* [B] */
+  const int32_t *slots;        /* [n_rows], or NULL */
+  uint64_t *masks;             /* [n_rows][mask_words] */
+  int32_t *positions;          /* [n_rows] */
+  int64_t n_requests, n_rows;  /* B: 0..max_requests; n_rows: 0..2^24 */
+  int64_t mask_words;          /* 1..4: new tokens up to 64 * mask_words, and max_new */
+} moe_cache_tree_t;
+
+MOE_API int moe_cache_tree(moe_cache_t *cache, const moe_cache_tree_t *tree, void *stream);
+
+/* Attention of each request's new tokens over its pages (all of them in the cache, once moe_cache_write has put them
+ * there): row r, new token i of its request, sees the P older tokens and those new tokens j whose bit j is set in its
+ * mask; without masks those with j <= i, a chain. With g the key-value head of query head h,
+ *   out[r][h] = sum_j softmax_j(scale * q[r][h] . k_j[g]) v_j[g]  * sigmoid(gate[r][h])       over the tokens j it sees.
+ * A row that sees no token gives 0, rows of refused requests and of those left out too; rows past the last token are left
+ * as they are. What a row does not see has no effect on it, infinities and NaN among them; what lies past a request's
+ * end has none on any. Numbers as for moe_cache_attend; bf16 weights are rounded to bf16 unless the cache is e4m3. out
+ * may be q or gate itself. Page ids outside the pool read as zeros and are reported. */
+typedef struct {
+  moe_rows_t q, gate;                          /* [n_rows][n_heads][head_dim]; gate.p NULL: no gate */
+  moe_rows_t out;                              /* written */
+  const int32_t *starts;                       /* [B + 1] */
+  const int32_t *slots;                        /* [n_rows], or NULL */
+  const uint64_t *masks;                       /* [n_rows][mask_words], or NULL */
+  const int32_t *tables;                       /* [B][table_stride] */
+  int64_t table_stride;
+  const int32_t *lengths;                      /* [B] */
+  const void *k_cache, *v_cache;
+  int64_t k_page_stride, v_page_stride;
+  const float *k_scale, *v_scale;              /* [n_kv_heads]: both given with an e4m3 cache, NULL otherwise */
+  int64_t n_requests, n_rows;                  /* B: 0..max_requests; n_rows: 0..2^24 */
+  int64_t mask_words;                          /* 1..4: new tokens up to 64 * mask_words; unused without masks */
+  double scale;                                /* up to 2.35e38 either way; usually 1 / sqrt(head_dim) */
+} moe_cache_attend_tree_t;
+
+MOE_API int moe_cache_attend_tree(moe_cache_t *cache, const moe_cache_attend_tree_t *attend, void *stream);
+
+/* What of the new tokens stays. counts[b] = k of request b's stay, path[b][0 .. k-1] in ascending order (path NULL: the
+ * first k); they move up behind its P older tokens, keys and values, in every pool given, and the length becomes P + k. A
+ * negative count ends the request: its length becomes 0. starts NULL: all of a request's tokens are new (counts are
+ * lengths to go back to; no path then).
+ *   - Pages past the new length go to the tail of the ring, in the order of the requests and of each one's pages.
+ *   - refs (NULL: no page is shared) holds the number of further holders of each page, 0 for a page with one: a page
+ *     that is given back loses one of them, and goes to the ring when it had none left, in the place of the first
+ *     request of this call that gave it back.
+ *   - A shared page into which tokens move up, or which the next token will enter (the new length ends inside it), is
+ *     exchanged for one from the head of the ring, which gets the rows that stay. The request gives the shared one back.
+ *     Pages given back in a call are not taken in the same call. When the running need, in the order of the requests,
+ *     passes the pages that are free, that request and every later one that needs a page stay as they were.
+ * A page belongs once to a table at most, and two requests that share a page both count in refs. Requests of a step that
+ * ends them by moe_cache_plan give their pages back whatever refs holds: a request that shares pages ends here.
+ * A count above n, a path that does not ascend or leaves the n new tokens, or n above max_new with a path: reported, the
+ * request stays as it was. Page ids outside the pool are not given back, and their rows not moved; they are reported, as
+ * are pages past the ring's room. lengths_out may be lengths, free_state_out may be free_state. */
+typedef struct {
+  const int32_t *counts;       /* [B] */
+  const int32_t *lengths;      /* [B] */
+  const int32_t *starts;       /* [B + 1], or NULL */
+  const int32_t *slots;        /* [n_rows], or NULL */
+  const int32_t *path;         /* [B][path_stride], counts[b] of them in use, or NULL */
+  int64_t path_stride;         /* at least the largest count */
+  int32_t *tables;             /* [B][table_stride] */
+  int64_t table_stride;
+  int32_t *free_pages;         /* [n_pages] */
+  const int32_t *free_state;   /* [3] */
+  int32_t *free_state_out;     /* [3]: the new head and count, and the number of requests that stayed for want of pages */
+  int32_t *lengths_out;        /* [B] */
+  int32_t *refs;               /* [n_pages], or NULL */
+  void *const *pools;          /* [n_pools], host memory: k_cache and v_cache of every layer */
+  const int64_t *page_strides; /* [n_pools], host memory */
+  int64_t n_pools;             /* 0..1024 */
+  int64_t n_requests, n_rows;  /* B: 0..max_requests; n_rows: 0..2^24 */
+} moe_cache_keep_t;
+
+MOE_API int moe_cache_keep(moe_cache_t *cache, const moe_cache_keep_t *keep, void *stream);
+
+/* Further requests over the tokens of others: for each entry i, request dst[i], which has none, gets the lengths[src[i]]
+ * tokens of src[i]. It shares the full pages (their refs grow by 1); the last one, if tokens fill it in part, is copied
+ * in every pool to a page from the head of the ring, in the order of the entries. When the running need passes the pages
+ * that are free, that entry and every later one that needs a page are refused. A negative src: the entry is unused.
+ * Lengths are those at the call's start. A request out of range, a dst that has tokens or that an earlier entry has
+ * named: reported (bit 16), the entry is left out. lengths_out may be lengths, free_state_out may be free_state. */
+typedef struct {
+  const int32_t *src, *dst;    /* [n_entries] */
+  const int32_t *lengths;      /* [B] */
+  int32_t *lengths_out;        /* [B] */
+  int32_t *tables;             /* [B][table_stride] */
+  int64_t table_stride;
+  const int32_t *free_pages;   /* [n_pages] */
+  const int32_t *free_state;   /* [3] */
+  int32_t *free_state_out;     /* [3]: the new head and count, and the number of entries refused */
+  int32_t *refs;               /* [n_pages] */
+  void *const *pools;          /* [n_pools], host memory: k_cache and v_cache of every layer */
+  const int64_t *page_strides; /* [n_pools], host memory */
+  int64_t n_pools;             /* 0..1024 */
+  int64_t n_entries;           /* 0..max_requests */
+  int64_t n_requests;          /* B: 0..max_requests */
+} moe_cache_fork_t;
+
+MOE_API int moe_cache_fork(moe_cache_t *cache, const moe_cache_fork_t *fork, void *stream);
+
+/* Host-only check of a shape and of any of these calls' arguments (each may be NULL) after moe_cache_reserve(max_new), as
+ * moe_debug_cache_check. */
+MOE_API int moe_debug_cache_check_new(const moe_cache_config_t *cfg, int max_new, const moe_cache_tree_t *tree,
+                                      const moe_cache_attend_tree_t *attend, const moe_cache_keep_t *keep,
+                                      const moe_cache_fork_t *fork);
+
 /* Waits for the handle's device (for graphs that hold calls of the handle too, on whichever stream they run) and
- * returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side wait of an attend call ran out: its outputs are wrong,
- * and later attend calls leave theirs unwritten until this call has reported it) or MOE_ERR_INVALID_ARG (a call met a
+ * returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded device-side wait of an attend or attend_tree call ran out: its outputs
+ * are wrong, and later such calls leave theirs unwritten until this call has reported it) or MOE_ERR_INVALID_ARG (a call met a
  * value on the device that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits:
  * 1 a wait ran out, 2 a length, 4 a page id or slot, 8 a free_state out of range or more pages than the ring has room
- * for. Not while a stream is being captured: a wait for the device ends the capture with an error. */
+ * for, 16 starts, a parent, a count, a path or an entry that cannot be. Not while a stream is being captured: a wait for the device ends the capture with an error. */
 MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);
 
 /* Test control of the attention's bounded device waits: timeout_us = microseconds a wait for a copy may last before it

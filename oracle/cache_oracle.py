@@ -86,3 +86,151 @@ def attend(q, tables, lengths, k_pool, v_pool, scale, gate=None):
         sg = 1.0 / (1.0 + np.exp(-gate))
         out, size = out * sg, size * sg
     return out, size, mag
+
+
+def _ring(free_pages, free_state, n_pages):
+    head, count = int(free_state[0]), int(free_state[1])
+    return [int(free_pages[(head + i) % n_pages]) for i in range(count)], head, count
+
+
+def tree(parents, starts, lengths, refused, n_rows, words):
+    """Masks (uint64 [n_rows, words]) and positions of drafted trees: each token's ancestors by walking up. refused: the
+    requests whose tokens are not in the cache."""
+    masks, positions = np.zeros((n_rows, words), np.uint64), np.zeros(n_rows, np.int32)
+    for b, length in enumerate(map(int, lengths)):
+        lo, n = int(starts[b]), int(starts[b + 1]) - int(starts[b])
+        if refused[b]:
+            continue
+        for i in range(n):
+            depth, j = -1, i
+            while j >= 0:
+                masks[lo + i, j // 64] |= np.uint64(1 << (j % 64))
+                depth += 1
+                j = int(parents[lo + j])
+            positions[lo + i] = length - n + depth
+    return masks, positions
+
+
+def attend_tree(q, starts, refused, masks, tables, lengths, k_pool, v_pool, scale, gate=None):
+    """As attend, for rows starts[b] .. starts[b + 1] - 1 of request b, its last tokens: each sees the older tokens and the
+    new ones in its mask (None: those up to itself). Rows of refused requests are 0, rows past the last token NaN (not
+    given). Also returns each row's number of tokens seen."""
+    rows, Hq, D = q.shape
+    n_pages, Hkv, page, _ = k_pool.shape
+    out, size, mag, seen = np.zeros(q.shape), np.zeros(q.shape), np.zeros((rows, Hq, 1)), np.zeros((rows, 1, 1))
+    out[int(starts[-1]):] = np.nan
+    for b in range(len(lengths)):
+        lo, hi, length = int(starts[b]), int(starts[b + 1]), int(lengths[b])
+        m = hi - lo
+        if m == 0 or refused[b]:
+            continue
+        sees = np.ones((m, length), bool)
+        for i in range(m):
+            for j in range(m):
+                sees[i, length - m + j] = j <= i if masks is None else int(masks[lo + i, j // 64]) >> (j % 64) & 1
+        seen[lo:hi, 0, 0] = sees.sum(1)
+        ids = tables[b, :-(-length // page)]
+        for g in range(Hkv):
+            k = np.concatenate([k_pool[p, g] if 0 <= p < n_pages else np.zeros((page, D)) for p in ids])[:length]
+            v = np.concatenate([v_pool[p, g] if 0 <= p < n_pages else np.zeros((page, D)) for p in ids])[:length]
+            for h in range(g * (Hq // Hkv), (g + 1) * (Hq // Hkv)):
+                for i in range(m):
+                    kk, vv, x = k[sees[i]], v[sees[i]], q[lo + i, h]
+                    if len(kk) == 0:
+                        continue
+                    with np.errstate(invalid="ignore", over="ignore"):
+                        s = kk @ x * scale
+                        e = np.exp(s - s.max())
+                        p = e / e.sum()
+                        out[lo + i, h], size[lo + i, h] = p @ vv, p @ np.abs(vv)
+                        mag[lo + i, h] = (np.abs(kk) @ np.abs(x)).max() * abs(scale)
+    if gate is not None:
+        sg = 1.0 / (1.0 + np.exp(-gate))
+        out, size = out * sg, size * sg
+    return out, size, mag, seen
+
+
+def keep(counts, lengths, starts, refused, path, tables, free_pages, free_state, refs, pools, page, n_pages):
+    """What of the new tokens stays, over copies: (lengths, free_state, tables, ring, refs, pools). starts None: every token
+    is new. pools: arrays [n_pages, heads, page, ...]."""
+    tables, ring, pools = tables.copy(), free_pages.copy(), [p.copy() for p in pools]
+    before = [p.copy() for p in pools]
+    holders = None if refs is None else [int(r) + 1 for r in refs]
+    free, head, count = _ring(free_pages, free_state, n_pages)
+    out_len, back, moves, used, wanted, stayed = [], [], [], 0, 0, 0
+    for b, (k, length) in enumerate(zip(map(int, counts), map(int, lengths))):
+        n = length if starts is None else 0 if refused[b] else int(starts[b + 1]) - int(starts[b])
+        older = length - n
+        new = 0 if k < 0 else older + k
+        steps = [] if k < 0 else [i if path is None else int(path[b][i]) for i in range(k)]
+        held, stay = -(-length // page), -(-new // page)
+        changed = {(older + i) // page for i, j in enumerate(steps) if i != j}
+        if new % page:
+            changed.add(stay - 1)
+        swap = [i for i in sorted(changed) if refs is not None and refs[tables[b, i]] > 0]
+        wanted += len(swap)
+        if swap and wanted > count:
+            stayed += 1
+            out_len.append(length)
+            continue
+        old = tables[b].copy()
+        for i in swap:
+            tables[b, i] = free[used]
+            used += 1
+        back += [int(old[i]) for i in swap] + [int(old[i]) for i in range(stay, held)]
+        out_len.append(new)
+        for p in range(new):
+            s = p if p < older else older + steps[p - older]
+            if s != p or p // page in swap:
+                moves.append((old[s // page], s % page, tables[b, p // page], p % page))
+    for src, so, dst, do in moves:
+        for a, z in zip(before, pools):
+            z[dst, :, do] = a[src, :, so]
+    gone = []
+    if holders is None:
+        gone = back
+    else:
+        for p in back:
+            holders[p] -= 1
+        for p in back:
+            if holders[p] <= 0 and p not in gone:
+                gone.append(p)
+        refs = np.array([max(0, h - 1) for h in holders], np.int32)
+    for i, p in enumerate(gone[:n_pages - count]):
+        ring[(head + count + i) % n_pages] = p
+    state = [(head + used) % n_pages, count - used + min(len(gone), n_pages - count), stayed]
+    i32 = np.int32
+    return np.array(out_len, i32), np.array(state, i32), tables, ring, refs, pools
+
+
+def fork(src, dst, lengths, tables, free_pages, free_state, refs, pools, page, n_pages):
+    """Requests dst over the tokens of src, over copies: (lengths, free_state, tables, ring, refs, pools)."""
+    tables, refs, pools, out_len = tables.copy(), refs.copy(), [p.copy() for p in pools], lengths.copy()
+    free, head, count = _ring(free_pages, free_state, n_pages)
+    used, wanted, refused, named = 0, 0, 0, set()
+    for s, d in zip(map(int, src), map(int, dst)):
+        if s < 0:
+            continue
+        if not (s < len(lengths) and 0 <= d < len(lengths)):
+            continue
+        twice = d in named
+        named.add(d)
+        if twice or lengths[d] != 0:
+            continue
+        n = int(lengths[s])
+        full, part = n // page, n % page
+        wanted += part > 0
+        if part and wanted > count:
+            refused += 1
+            continue
+        tables[d, :full] = tables[s, :full]
+        for p in tables[s, :full]:
+            refs[p] += 1
+        if part:
+            tables[d, full] = free[used]
+            used += 1
+            for z in pools:
+                z[tables[d, full], :, :part] = z[tables[s, full], :, :part]
+        out_len[d] = n
+    i32 = np.int32
+    return out_len, np.array([(head + used) % n_pages, count - used, refused], i32), tables, free_pages.copy(), refs, pools

@@ -21,6 +21,9 @@ struct moe_cache {
   size_t workspace_bytes = 0;
   uint64_t timeout_ns = 500ull * 1000 * 1000;
   int skip_copy = 0;
+  // of moe_cache_reserve: the rows that calls move, the tree attention's workspace
+  int max_new = 0;
+  uint8_t* reserved = nullptr;
 };
 
 namespace {
@@ -116,6 +119,63 @@ int check_attend(const moe_cache_config_t& cfg, const CacheShape& S, const moe_c
   return MOE_OK;
 }
 
+constexpr int64_t MAX_ROWS = (int64_t)1 << 24;
+bool batch_ok(const moe_cache_config_t& cfg, int64_t n_requests, int64_t n_rows) {
+  return n_requests >= 0 && n_requests <= cfg.max_requests && n_rows >= 0 && n_rows <= MAX_ROWS;
+}
+bool ring_ok(const void* pages, const void* state, const void* state_out) {
+  return aligned(pages, 4) && aligned(state, 4) && aligned(state_out, 4);
+}
+bool pools_ok(const CacheShape& S, void* const* pools, const int64_t* strides, int64_t n) {
+  if (n < 0 || n > 1024 || (n > 0 && (!pools || !strides))) return false;
+  for (int64_t i = 0; i < n; ++i)
+    if (!pool_ok(S, pools[i], strides[i])) return false;
+  return true;
+}
+int check_tree(const moe_cache_config_t& cfg, const moe_cache_tree_t& t) {
+  if (!batch_ok(cfg, t.n_requests, t.n_rows) || t.mask_words < 1 || t.mask_words > CACHE_MAX_NEW / 64)
+    return MOE_ERR_INVALID_ARG;
+  if (t.n_rows == 0) return MOE_OK;
+  if (!aligned(t.masks, 8) || !aligned(t.positions, 4) || ((uintptr_t)t.slots & 3) ||
+      (t.n_requests > 0 && (!aligned(t.parents, 4) || !aligned(t.starts, 4) || !aligned(t.lengths, 4))))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+int check_attend_tree(const moe_cache_config_t& cfg, const CacheShape& S, const moe_cache_attend_tree_t& a) {
+  if (!batch_ok(cfg, a.n_requests, a.n_rows) || !(fabs(a.scale) <= MAX_SCALE) ||
+      (a.masks && (a.mask_words < 1 || a.mask_words > CACHE_MAX_NEW / 64)))
+    return MOE_ERR_INVALID_ARG;
+  if (a.n_requests == 0 || a.n_rows == 0) return MOE_OK;
+  if (!rows_ok(a.q, a.n_rows) || (a.gate.p && !rows_ok(a.gate, a.n_rows)) || !rows_ok(a.out, a.n_rows) ||
+      !aligned(a.starts, 4) || ((uintptr_t)a.slots & 3) || ((uintptr_t)a.masks & 7) || !aligned(a.tables, 4) ||
+      !table_ok(cfg, a.table_stride) || !aligned(a.lengths, 4) || !pool_ok(S, a.k_cache, a.k_page_stride) ||
+      !pool_ok(S, a.v_cache, a.v_page_stride) || !scales_ok(S, a.k_scale, a.v_scale))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+int check_keep(const moe_cache_config_t& cfg, const CacheShape& S, const moe_cache_keep_t& k) {
+  if (!batch_ok(cfg, k.n_requests, k.n_rows) || !ring_ok(k.free_pages, k.free_state, k.free_state_out) ||
+      ((uintptr_t)k.starts & 3) || ((uintptr_t)k.slots & 3) || ((uintptr_t)k.path & 3) || ((uintptr_t)k.refs & 3) ||
+      (!k.starts && (k.path || k.slots)) || !pools_ok(S, k.pools, k.page_strides, k.n_pools))
+    return MOE_ERR_INVALID_ARG;
+  if (k.n_requests == 0) return MOE_OK;
+  if (!aligned(k.counts, 4) || !aligned(k.lengths, 4) || !aligned(k.lengths_out, 4) || !aligned(k.tables, 4) ||
+      !table_ok(cfg, k.table_stride) || (k.path && (k.path_stride < 1 || k.path_stride >= (int64_t)1 << 40)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+int check_fork(const moe_cache_config_t& cfg, const CacheShape& S, const moe_cache_fork_t& f) {
+  if (!batch_ok(cfg, f.n_requests, 0) || f.n_entries < 0 || f.n_entries > cfg.max_requests ||
+      !ring_ok(f.free_pages, f.free_state, f.free_state_out) || !aligned(f.refs, 4) ||
+      !pools_ok(S, f.pools, f.page_strides, f.n_pools))
+    return MOE_ERR_INVALID_ARG;
+  if (f.n_entries > 0 && (!aligned(f.src, 4) || !aligned(f.dst, 4))) return MOE_ERR_INVALID_ARG;
+  if (f.n_requests > 0 && (!aligned(f.lengths, 4) || !aligned(f.lengths_out, 4) || !aligned(f.tables, 4) ||
+                           !table_ok(cfg, f.table_stride)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" int moe_cache_create(const moe_cache_config_t* cfg, moe_cache_t** out) {
@@ -183,6 +243,7 @@ extern "C" void moe_cache_destroy(moe_cache_t* c) {
     const OnDevice on(c->dev);
     cudaDeviceSynchronize();
     cudaFree(c->mem);
+    cudaFree(c->reserved);
   }
   delete c;
 }
@@ -225,6 +286,86 @@ extern "C" int moe_cache_attend(moe_cache_t* c, const moe_cache_attend_t* a, voi
   c->skip_copy = 0;
   const cudaError_t e = cache_attend_launch(c->S, *a, w, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_attend");
+}
+
+// ---- several new tokens of a request ----
+namespace {
+size_t moves_bytes(const moe_cache* c) { return ((size_t)c->cfg.max_requests * sizeof(CacheMoves) + 255) & ~(size_t)255; }
+// what the calls below check beside their arguments
+int ready(const moe_cache* c) {
+  if (!c->max_new) return MOE_ERR_NOT_LOADED;
+  return on_device(c) ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+}  // namespace
+
+extern "C" int moe_cache_reserve(moe_cache_t* c, int max_new) {
+  if (!c || c->max_new || !on_device(c)) return MOE_ERR_INVALID_ARG;
+  if (max_new < 1 || max_new > CACHE_MAX_NEW) return MOE_ERR_UNSUPPORTED;
+  const size_t bytes = moves_bytes(c) + cache_attend_tree_workspace(c->num_sms, c->S.D);
+  cudaError_t e = cache_pages_init();
+  if (e == cudaSuccess) e = cudaMalloc(&c->reserved, bytes);
+  if (e == cudaSuccess) e = cudaMemset(c->reserved, 0, bytes);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) {
+    cudaFree(c->reserved);
+    c->reserved = nullptr;
+    return report_cuda(e, "moe_cache_reserve");
+  }
+  c->max_new = max_new;
+  return MOE_OK;
+}
+
+extern "C" int moe_cache_tree(moe_cache_t* c, const moe_cache_tree_t* t, void* stream) {
+  if (!c || !t) return MOE_ERR_INVALID_ARG;
+  int r = check_tree(c->cfg, *t);
+  if (r == MOE_OK) r = ready(c);
+  if (r != MOE_OK || t->n_rows == 0) return r;
+  const cudaError_t e = cache_tree_launch(c->S, *t, c->max_new, c->status, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_tree");
+}
+
+extern "C" int moe_cache_attend_tree(moe_cache_t* c, const moe_cache_attend_tree_t* a, void* stream) {
+  if (!c || !a) return MOE_ERR_INVALID_ARG;
+  int r = check_attend_tree(c->cfg, c->S, *a);
+  if (r == MOE_OK) r = ready(c);
+  if (r != MOE_OK || a->n_requests == 0 || a->n_rows == 0) return r;
+  const CacheTreeState w{c->reserved + moves_bytes(c), c->status, c->num_sms, c->max_new, c->timeout_ns};
+  const cudaError_t e = cache_attend_tree_launch(c->S, *a, w, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_attend_tree");
+}
+
+extern "C" int moe_cache_keep(moe_cache_t* c, const moe_cache_keep_t* k, void* stream) {
+  if (!c || !k) return MOE_ERR_INVALID_ARG;
+  int r = check_keep(c->cfg, c->S, *k);
+  if (r == MOE_OK) r = ready(c);
+  if (r != MOE_OK) return r;
+  const cudaError_t e = cache_keep_launch(c->S, *k, c->max_new, (CacheMoves*)c->reserved, c->status, c->num_sms,
+                                          (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_keep");
+}
+
+extern "C" int moe_cache_fork(moe_cache_t* c, const moe_cache_fork_t* f, void* stream) {
+  if (!c || !f) return MOE_ERR_INVALID_ARG;
+  int r = check_fork(c->cfg, c->S, *f);
+  if (r == MOE_OK) r = ready(c);
+  if (r != MOE_OK) return r;
+  const cudaError_t e = cache_fork_launch(c->S, *f, (CacheMoves*)c->reserved, c->status, c->num_sms,
+                                          (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_fork");
+}
+
+extern "C" int moe_debug_cache_check_new(const moe_cache_config_t* cfg, int max_new, const moe_cache_tree_t* t,
+                                         const moe_cache_attend_tree_t* a, const moe_cache_keep_t* k,
+                                         const moe_cache_fork_t* f) {
+  if (!cfg) return MOE_ERR_INVALID_ARG;
+  CacheShape S;
+  int st = check_config(*cfg, &S);
+  if (st == MOE_OK && (max_new < 1 || max_new > CACHE_MAX_NEW)) st = MOE_ERR_UNSUPPORTED;
+  if (st == MOE_OK && t) st = check_tree(*cfg, *t);
+  if (st == MOE_OK && a) st = check_attend_tree(*cfg, S, *a);
+  if (st == MOE_OK && k) st = check_keep(*cfg, S, *k);
+  if (st == MOE_OK && f) st = check_fork(*cfg, S, *f);
+  return st;
 }
 
 extern "C" int moe_cache_debug_set_wait(moe_cache_t* c, uint32_t timeout_us, int skip_copy) {

@@ -29,7 +29,8 @@ EXPORTS = ["moe_block_create", "moe_block_load_weights", "moe_block_forward", "m
            "moe_stack_forward", "moe_stack_get_status", "moe_stack_layer", "moe_stack_destroy",
            "moe_affine_convert", "moe_affine_free", "moe_block_load_affine",
            "moe_cache_create", "moe_cache_destroy", "moe_cache_plan", "moe_cache_write", "moe_cache_attend",
-           "moe_cache_get_status", "moe_debug_cache_check", "moe_cache_debug_set_wait"]
+           "moe_cache_get_status", "moe_debug_cache_check", "moe_cache_debug_set_wait", "moe_cache_reserve",
+           "moe_cache_tree", "moe_cache_attend_tree", "moe_cache_keep", "moe_cache_fork", "moe_debug_cache_check_new"]
 
 
 class MoeError(RuntimeError):
@@ -76,10 +77,15 @@ class CacheConfig(ctypes.Structure):
 
 
 # The argument structures of the cache's calls hold pointers, int64_t and double alone (moe_cache_plan_t,
-# moe_cache_write_t, moe_cache_attend_t), so each is packed in one go.
+# moe_cache_write_t, moe_cache_attend_t; moe_cache_tree_t, moe_cache_attend_tree_t, moe_cache_keep_t, moe_cache_fork_t), so
+# each is packed in one go.
 CACHE_PLAN = struct.Struct("@3Pq7P2q")
 CACHE_WRITE = struct.Struct("@" + 4 * "P2q" + "6P2q2Pq")
 CACHE_ATTEND = struct.Struct("@" + 3 * "P2q" + "Pq3P2q2Pqd")
+CACHE_TREE = struct.Struct("@6P3q")
+CACHE_ATTEND_TREE = struct.Struct("@" + 3 * "P2q" + "4Pq3P2q2P3qd")
+CACHE_KEEP = struct.Struct("@5PqPq7P3q")
+CACHE_FORK = struct.Struct("@5Pq6P3q")
 
 
 def _affine_struct(aff: dict):
@@ -176,6 +182,10 @@ def load_library(path: str = LIB_PATH):
     for f in (lib.moe_cache_plan, lib.moe_cache_write, lib.moe_cache_attend):
         f.argtypes = [vp, vp, vp]
     lib.moe_debug_cache_check.argtypes = [ctypes.POINTER(CacheConfig), vp, vp, vp]
+    for f in (lib.moe_cache_tree, lib.moe_cache_attend_tree, lib.moe_cache_keep, lib.moe_cache_fork):
+        f.argtypes = [vp, vp, vp]
+    lib.moe_cache_reserve.argtypes = [vp, i]
+    lib.moe_debug_cache_check_new.argtypes = [ctypes.POINTER(CacheConfig), i, vp, vp, vp, vp]
     lib.moe_cache_debug_set_wait.argtypes = [vp, u32, i]
     lib.moe_cache_get_status.argtypes = [vp, ctypes.POINTER(u32)]
     lib.moe_cache_destroy.argtypes = [vp]
@@ -428,16 +438,30 @@ class MoeStack:
 
 
 CachePlan = collections.namedtuple("CachePlan", "slots positions starts lengths free_state")
+CacheTree = collections.namedtuple("CacheTree", "masks positions")
+CacheState = collections.namedtuple("CacheState", "lengths free_state")
+
+
+class CachePools:
+    """The pools of a model's layers, keys and values, as PagedCache.keep and .fork take them (made by PagedCache.pools).
+    It holds the tensors, so that their addresses stay theirs."""
+
+    def __init__(self, cache, tensors):
+        self.cache, self.tensors, n = cache, tuple(tensors), len(tensors)
+        at = [cache._pool(t) for t in self.tensors]
+        self._pools, self._strides = (ctypes.c_void_p * n)(*(p for p, _ in at)), (ctypes.c_int64 * n)(*(s for _, s in at))
+        self.args = (ctypes.addressof(self._pools), ctypes.addressof(self._strides), n)
 
 
 class PagedCache:
     """A paged key-value cache of one shape: the page plan of a step, the write of its rows, the attention that
     reads them (the paged key-value cache's section of include/moe_block.h has the formulas). One handle serves every
     layer; the pools [n_pages, n_kv_heads, page_size, head_dim], the tables and the ring of free pages are the
-    caller's. Outputs are new tensors unless given, allocated on `stream`."""
+    caller's. Outputs are new tensors unless given, allocated on `stream`. max_new: most new tokens of a request in a step
+    (1 to 256), for tree, attend_tree, keep and fork; 0: the handle has none of them."""
 
     def __init__(self, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests, max_pages, dtype="f16",
-                 cache_dtype=None, rope_dim=0, rope_theta=10000.0, gamma_offset=0.0, eps=1e-6):
+                 cache_dtype=None, rope_dim=0, rope_theta=10000.0, gamma_offset=0.0, eps=1e-6, max_new=0):
         import torch
         self.lib = load_library()
         cache_dtype = cache_dtype or dtype
@@ -455,6 +479,9 @@ class PagedCache:
         # a call costs the host about as much as the smallest one costs the GPU: what it looks up is kept at hand
         self._torch, self._dev, self._i32, self._f32 = torch, self.device.index, torch.int32, torch.float32
         self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._i64, self.max_new = torch.int64, max_new
+        if max_new:
+            _check(self.lib.moe_cache_reserve(self.h, int(max_new)), "moe_cache_reserve")
 
     def close(self):
         if getattr(self, "h", None):
@@ -586,6 +613,107 @@ class PagedCache:
             *(self._scales(k_scale, v_scale) if k_scale is not None or v_scale is not None else (0, 0)), B,
             scale if scale is not None else self.head_dim ** -0.5)
         self._call(self.lib.moe_cache_attend, args, stream, "moe_cache_attend")
+        return out
+
+    def pools(self, tensors):
+        """The pools of all layers, keys and values, for keep and fork: made once, when the pools are."""
+        return CachePools(self, tensors)
+
+    def _masks(self, t, rows):
+        if (t.dtype is self._i64 and t.dim() == 2 and t.shape[0] == rows and 1 <= t.shape[1] <= 4
+                and t.get_device() == self._dev and t.is_contiguous()):
+            return t.data_ptr(), t.shape[1]
+        raise ValueError(f"want contiguous masks int64 [{rows}, 1..4] on {self.device}; got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+
+    def tree(self, parents, starts, lengths, slots=None, words=None, out=None, stream=None):
+        """Ancestor masks and positions of drafted trees (moe_cache_tree): parents int32 [n_rows], each a place among its
+        request's new tokens or -1, starts int32 [B + 1], lengths int32 [B], slots int32 [n_rows] (the plan's). Returns
+        CacheTree(masks int64 [n_rows, words], positions int32 [n_rows]); words: enough for max_new unless given."""
+        rows, B, i32, vec = parents.shape[0], lengths.shape[0], self._i32, self._vector
+        if out is None:
+            words = words or max(1, -(-self.max_new // 64))
+            out = CacheTree(self._empty((rows, words), self._i64, stream), self._empty((rows,), i32, stream))
+        masks, words = self._masks(out.masks, rows)
+        args = CACHE_TREE.pack(vec(parents, rows, i32), vec(starts, B + 1, i32), vec(lengths, B, i32),
+                               vec(slots, rows, i32) if slots is not None else 0, masks, vec(out.positions, rows, i32),
+                               B, rows, words)
+        self._call(self.lib.moe_cache_tree, args, stream, "moe_cache_tree")
+        return out
+
+    def attend_tree(self, q, starts, tables, lengths, k_cache, v_cache, masks=None, slots=None, gate=None, scale=None,
+                    k_scale=None, v_scale=None, out=None, stream=None):
+        """Attention of each request's new tokens over its pages (moe_cache_attend_tree): q [n_rows, n_heads, head_dim],
+        starts int32 [B + 1], tables int32 [B, max_pages], lengths int32 [B], masks int64 [n_rows, words] (None: chains),
+        slots int32 [n_rows] (the plan's), gate None or like q. Rows past the last token stay as they are in out."""
+        rows, B, heads, vec = q.shape[0], lengths.shape[0], self.n_heads, self._vector
+        if out is None:
+            out = self._empty((rows, heads, self.head_dim), self.dtype, stream)
+            out_rows = out.data_ptr(), heads * self.head_dim, self.head_dim
+        else:
+            out_rows = self._rows(out, heads, rows)
+        kc, ks = self._pool(k_cache)
+        vc, vs = self._pool(v_cache)
+        mask, words = self._masks(masks, rows) if masks is not None else (0, 0)
+        args = CACHE_ATTEND_TREE.pack(
+            *self._rows(q, heads, rows), *(self._rows(gate, heads, rows) if gate is not None else (0, 0, 0)), *out_rows,
+            vec(starts, B + 1, self._i32), vec(slots, rows, self._i32) if slots is not None else 0, mask,
+            *self._table(tables, B), vec(lengths, B, self._i32), kc, vc, ks, vs,
+            *(self._scales(k_scale, v_scale) if k_scale is not None or v_scale is not None else (0, 0)), B, rows, words,
+            scale if scale is not None else self.head_dim ** -0.5)
+        self._call(self.lib.moe_cache_attend_tree, args, stream, "moe_cache_attend_tree")
+        return out
+
+    def _state(self, out, B, stream):
+        """(CacheState, pointers of its lengths and free_state)."""
+        if out is None:
+            buf = self._empty((B + 3,), self._i32, stream)
+            return CacheState(buf[:B], buf[B:]), buf.data_ptr(), buf.data_ptr() + 4 * B
+        return out, self._vector(out.lengths, B, self._i32), self._vector(out.free_state, 3, self._i32)
+
+    def _pool_args(self, pools):
+        if not isinstance(pools, CachePools) or pools.cache is not self:
+            raise ValueError("want pools made by this cache's pools()")
+        return pools.args
+
+    def keep(self, counts, lengths, tables, free_pages, free_state, pools, starts=None, slots=None, path=None, refs=None,
+             out=None, stream=None):
+        """What of the new tokens stays (moe_cache_keep): counts int32 [B] of them, those that path int32 [B, n] names (None:
+        the first ones), move up in all pools; the pages behind them go back to the ring. counts below 0 end a request;
+        without starts all of its tokens count as new. tables, free_pages and refs (int32 [n_pages], further holders of each
+        page) are updated in place. out: a CacheState to write into, which may be the inputs."""
+        B, i32, vec = lengths.shape[0], self._i32, self._vector
+        rows = slots.shape[0] if slots is not None else (1 << 24 if starts is not None else 0)
+        out, lengths_out, state_out = self._state(out, B, stream)
+        path_at = path_stride = 0
+        if path is not None:
+            if (path.dtype is not i32 or path.dim() != 2 or path.shape[0] != B or path.get_device() != self._dev
+                    or not path.is_contiguous() or path.shape[1] < 1):
+                raise ValueError(f"want a contiguous path int32 [{B}, n] on {self.device}; got {path.dtype} "
+                                 f"{tuple(path.shape)} on {path.device}")
+            path_at, path_stride = path.data_ptr(), path.shape[1]
+        table, table_stride = self._table(tables, B)
+        pool_args = self._pool_args(pools)
+        args = CACHE_KEEP.pack(
+            vec(counts, B, i32), vec(lengths, B, i32), vec(starts, B + 1, i32) if starts is not None else 0,
+            vec(slots, rows, i32) if slots is not None else 0, path_at, path_stride, table, table_stride,
+            vec(free_pages, self.n_pages, i32), vec(free_state, 3, i32), state_out, lengths_out,
+            vec(refs, self.n_pages, i32) if refs is not None else 0, *pool_args, B, rows)
+        self._call(self.lib.moe_cache_keep, args, stream, "moe_cache_keep")
+        return out
+
+    def fork(self, src, dst, lengths, tables, free_pages, free_state, refs, pools, out=None, stream=None):
+        """Further requests over the tokens of others (moe_cache_fork): request dst[i] gets src[i]'s tokens, its full pages
+        shared (refs int32 [n_pages] grow), the last one copied in all pools. src, dst int32 [n]; a negative src is left
+        out. tables and refs are updated in place. out: a CacheState to write into, which may be the inputs."""
+        B, n, i32, vec = lengths.shape[0], src.shape[0], self._i32, self._vector
+        out, lengths_out, state_out = self._state(out, B, stream)
+        table, table_stride = self._table(tables, B)
+        args = CACHE_FORK.pack(
+            vec(src, n, i32), vec(dst, n, i32), vec(lengths, B, i32), lengths_out, table, table_stride,
+            vec(free_pages, self.n_pages, i32), vec(free_state, 3, i32), state_out, vec(refs, self.n_pages, i32),
+            *self._pool_args(pools), n, B)
+        self._call(self.lib.moe_cache_fork, args, stream, "moe_cache_fork")
         return out
 
     def set_wait(self, timeout_us=0, skip_copy=False):
