@@ -329,7 +329,9 @@ extern "C" int moe_cache_attend_tree(moe_cache_t* c, const moe_cache_attend_tree
   int r = check_attend_tree(c->cfg, c->S, *a);
   if (r == MOE_OK) r = ready(c);
   if (r != MOE_OK || a->n_requests == 0 || a->n_rows == 0) return r;
-  const CacheTreeState w{c->reserved + moves_bytes(c), c->status, c->num_sms, c->max_new, c->timeout_ns};
+  const CacheTreeState w{c->reserved + moves_bytes(c), c->status, c->num_sms, c->max_new, c->timeout_ns,
+                         c->skip_copy};
+  c->skip_copy = 0;
   const cudaError_t e = cache_attend_tree_launch(c->S, *a, w, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : report_cuda(e, "moe_cache_attend_tree");
 }

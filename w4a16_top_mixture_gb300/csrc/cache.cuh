@@ -56,6 +56,7 @@ struct CacheTreeState {
   uint32_t* status;
   int num_sms, max_new;
   uint64_t timeout_ns;                   // of the device's waits
+  int skip_copy;
 };
 size_t cache_attend_tree_workspace(int num_sms, int head_dim);
 cudaError_t cache_attend_tree_launch(const CacheShape& S, const moe_cache_attend_tree_t& a, const CacheTreeState& w,

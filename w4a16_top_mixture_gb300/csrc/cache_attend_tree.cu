@@ -1,134 +1,1062 @@
 // Attention of several new tokens of each request over the paged cache (moe_cache_attend_tree).
 //
-// The simple form: a CTA to a row and query head, four warps that take the tokens in turn, each lane D / 32 elements of
-// the head; running maxima and sums, joined in shared memory.
+// The new tokens of a request times the query heads of a group are rows that meet the same keys and values: 128 of them
+// are a tile of the tensor cores, so that S[rows x tokens] = Q K^T and O[rows x d] += P V are tcgen05 products with the
+// rows' statistics a thread's each. Up to 128 rows the bytes of the cache bound the kernel, above it the products.
+//   Work. An item is a request, a key-value head and 128 rows. The tiles of TN tokens of all items, one after another, are
+// divided evenly over the CTAs, one to an SM; an item that crosses a CTA's border is split, and its parts (O, the rows'
+// bases and sums) are joined by a second kernel: O of 128 rows is too much for one CTA to join where there are many parts.
+//   Roles. One warp finds the CTA's items, one copies (TMA, a ring of stages, keys one tile ahead of values), one issues
+// the products, four do the softmax, a row to a thread, and four prepare: the queries go to tensor memory, where they are
+// the first operand; 8-bit tiles are converted; and values of tiles with new tokens are looked through (below).
+//   Tensor memory. O, Q and two S: the products of one tile run during the softmax of the other. P lies where S was.
+//   Layout. A stage holds [8 tokens][64 elements] blocks of 1 KB in the 128-byte swizzle, the blocks of 8 tokens side by
+// side, whatever the pages: as K it is read along d, as V along the tokens, by the descriptors' strides alone.
+//   Bases. P = 2^(score - base): the base is a row's first maximum and follows when one passes it by more than TAU, since
+// that rescales O. fp16 weights are lifted by 2^LIFT, so that a long tail below the highest keeps its bits.
+//   Values that are not finite. A weight of 0 does not keep NaN out of a product. What lies past a request's end is zeroed
+// in shared memory; a new token's value that some rows do not see is looked at, and where it is not finite, zeroed too and
+// added by the epilogue to the rows that see it.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "cache.cuh"
+#include "ptx.cuh"
+#include "umma.cuh"
 
 namespace moe {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr int THREADS = 384, MAX_CTAS = 1024, EXTRA = 2, SHORT = 5, ITEMS = 4, M = 128;
+constexpr int SMEM = 227 * 1024, MISC = 2048;
+constexpr int W_PRODUCE = 0, W_MMA = 1, W_FIND = 2, W_SOFT = 4, W_PREP = 8;
 
-struct TreeAttendArgs {
-  moe_cache_attend_tree_t a;
-  int B, rows, Hq, Hkv, group, page_log2, n_pages, most;
-  long long max_len;
-  float scale;
-  uint32_t* status;
+struct Part {                // of an item that starts in a CTA and ends in another
+  int lo, g, m0, rows;       // its first row in the batch, key-value head, first row and rows of the item's 128
+  int last;                  // the CTA of its last part; 0: there is no such item
+  int pad[3];
 };
 
-template <int D, bool BF16, bool E4M3>
-__device__ __forceinline__ void load_row(const void* pool, int64_t at, int lane, float (&x)[D / 32]) {
+struct TreeArgs {
+  moe_cache_attend_tree_t a;
+  int B, rows, Hkv, group, page_log2, n_pages, most;
+  long long max_len;
+  float scale;               // with log2(e)
+  float* parts;              // [CTA][2][M * D + 2 * M]: the item a CTA begins in the middle of, the one it leaves so
+  Part* joins;               // [CTA]
+  uint32_t* status;
+  uint64_t timeout_ns;
+  int skip_copy;
+};
+
+template <int D_, bool BF16_, bool E4M3_>
+struct Shape {
+  static constexpr int D = D_;
+  static constexpr bool BF16 = BF16_, E4M3 = E4M3_, PBF16 = BF16_ && !E4M3_;   // e4m3 values are exact in fp16
+  static constexpr int TN = D == 256 ? 64 : 128;
+  static constexpr int BLOCKS = D / 64, GROUP = BLOCKS * 1024;                 // of 8 tokens
+  static constexpr int TILE = TN / 8 * GROUP, RAW = E4M3 ? TN * D : TILE;
+  static constexpr int NC = E4M3 ? 4 : 0;                                      // converted tiles
+  static constexpr int NR0 = (SMEM - 1024 - MISC - NC * TILE) / RAW, NR = NR0 > 12 ? 12 : NR0;
+  static constexpr int DYN = 1024 + NC * TILE + NR * RAW + MISC;
+  static constexpr uint32_t O = 0, Q = D, S0 = D + D / 2;                      // columns of tensor memory
+  static constexpr float TAU = PBF16 ? 8.f : 2.f, LIFT = PBF16 ? 0.f : 13.f;
+  static constexpr int PART = M * D + 2 * M;
+  static_assert(S0 + 2 * TN <= 512 && DYN <= SMEM && NR >= 4, "fits");
+};
+
+struct Item {
+  int b, lo, n, older, len;  // b < 0: no more items. n: rows of the batch
+  int g, m0, rows;           // key-value head; first row of the 128 and how many there are
+  int t0, t1, part, pad;     // tiles; -1: the whole item, else which of the CTA's two parts
+};
+
+struct Control {
+  uint64_t full[12], empty[12], c_full[4], c_empty[4], new_full[8], fixed[8], s_full[2], p_ready[2], pv_done, q_ready, q_free, o_free, drained;
+  uint64_t item_full[ITEMS], item_empty[ITEMS];
+  long long sums[THREADS / 32];
+  int longest[THREADS / 32];
+  Item items[ITEMS];
+  int odd[ITEMS];            // values that are not finite were taken out
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Control) <= MISC, "control words");
+
+// ---- instructions ----
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float gated(float y, float x) {       // y * sigmoid(x), see cache_attend.cu
+  const float e = __expf(-fabsf(x));
+  return __fdividef(x < 0.f ? y * e : y, 1.f + e);
+}
+__device__ __forceinline__ void tma5(void* dst, const CUtensorMap* m, int group, int page, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(0), "r"(group), "r"(page), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma3(void* dst, const CUtensorMap* m, int row, int page, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(0), "r"(row), "r"(page), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// see tmem_wait_ld: the registers are valid from here on
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+// a shared-memory descriptor of blocks in the 128-byte swizzle: bytes between blocks along the other dimension of the
+// layout (lead, read where the operand runs across its rows) and between groups of 8 rows (stride)
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// 128 rows x n: 16-bit operands, fp32 sums, B across its rows where `across`
+__device__ __forceinline__ uint32_t idesc(bool bf16, bool across, int n) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (across ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+         (uint32_t)(M >> 4) << 24;
+}
+
+__device__ __forceinline__ uint16_t* rows_at(const moe_rows_t& r, int64_t row, int h) {
+  return (uint16_t*)r.p + row * r.row_stride + h * r.head_stride;
+}
+
+// ---- the division of the work ----
+// A request's items are of n_tiles tiles and EXTRA units for what an item's beginning and end cost.
+struct Request {
+  int lo, n, older, len, tiles, m_tiles;
+};
+template <class S>
+__device__ __forceinline__ Request request(const TreeArgs& A, int b, uint32_t* bad) {
+  Request r = {};
+  if (b >= A.B) return r;
+  const NewTokens t = new_tokens_of(A.a.starts, A.a.slots, A.a.lengths, b, A.rows, A.max_len, A.most, bad);
+  r.lo = t.lo;
+  r.n = t.rows;
+  const bool live = !t.left_out && t.n > 0;
+  r.len = live ? t.len : 0;
+  r.older = live ? t.len - t.n : 0;
+  r.tiles = (int)(((unsigned)r.len + S::TN - 1) / S::TN);
+  r.m_tiles = (int)(((long long)r.n * A.group + M - 1) / M);
+  return r;
+}
+__device__ __forceinline__ long long units_of(const TreeArgs& A, const Request& r) {
+  return (long long)A.Hkv * r.m_tiles * (r.tiles + EXTRA);
+}
+
+// Where tile k of an item of n tiles lies among its stages: keys one tile ahead of values, K0 K1 V0 K2 V1 .. V(n-1)
+__device__ __forceinline__ int key_at(int k) { return k ? 2 * k - 1 : 0; }
+__device__ __forceinline__ int value_at(int k, int n) { return k + 1 < n ? 2 * k + 2 : 2 * n - 1; }
+
+// a row's mask over its request's new tokens, as 32-bit words
+struct Mask {
+  uint32_t w[CACHE_MAX_NEW / 32];
+  __device__ __forceinline__ uint32_t word(int k) const {
+    uint32_t r = k < 0 ? 0xFFFFFFFFu : 0u;          // older tokens are seen, what lies past the end is not
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const int64_t e = at + i * 64 + lane * 2;
-    if (E4M3) {
-      const uint16_t c = __ldcg((const unsigned short*)((const uint8_t*)pool + e));
-      uint32_t lo, hi;
-      e4m3x4_to_f16x4(c, lo, hi);
-      const float2 f = unpack2<false>(lo);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    } else {
-      const float2 f = unpack2<BF16>(__ldcg((const uint32_t*)((const uint16_t*)pool + e)));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+    for (int i = 0; i < CACHE_MAX_NEW / 32; ++i) r = k == i ? w[i] : r;
+    return r;
+  }
+  // the 32 tokens from place `from` among the new ones on (below 0: older ones)
+  __device__ __forceinline__ uint32_t window(int from) const {
+    const int k = from >> 5;
+    return __funnelshift_r(word(k), word(k + 1), from & 31);
+  }
+  __device__ __forceinline__ void load(const TreeArgs& A, int row, int i, int n, bool some) {
+#pragma unroll
+    for (int k = 0; k < CACHE_MAX_NEW / 64; ++k) {
+      uint64_t v = 0;
+      if (some && A.a.masks) {
+        if (k < A.a.mask_words) v = __ldcg((const unsigned long long*)A.a.masks + (size_t)row * A.a.mask_words + k);
+      } else if (some) {
+        const int upto = i - 64 * k;
+        v = upto < 0 ? 0ull : upto >= 63 ? ~0ull : (2ull << upto) - 1;
+      }
+      const int left = n - 64 * k;
+      v = left <= 0 ? 0ull : left >= 64 ? v : v & ((1ull << left) - 1);
+      w[2 * k] = (uint32_t)v;
+      w[2 * k + 1] = (uint32_t)(v >> 32);
+    }
+  }
+};
+
+// two elements in 16 bits with those that are not finite made 0
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+  const uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+  if ((v & e) == e) v &= 0xFFFF0000u;
+  if ((v >> 16 & e) == e) v &= 0xFFFFu;
+  return v;
+}
+template <bool BF16>
+__device__ __forceinline__ float odd(float x) { return fabsf(x) <= 3.4028234663852886e38f ? 0.f : x; }
+
+// e4m3 codes to 16-bit pairs, four at a time
+template <bool BF16>
+__device__ __forceinline__ void codes4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  e4m3x4_to_f16x4(v, lo, hi);
+  if (BF16) {
+    const float2 a = unpack2<false>(lo), b = unpack2<false>(hi);
+    lo = pack2<true>(a.x, a.y);
+    hi = pack2<true>(b.x, b.y);
+  }
+}
+
+// 32 elements of a row, fp32
+template <bool BF16>
+__device__ __forceinline__ void gate32(float (&y)[32], const uint16_t* at) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(at) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2<BF16>(w[j]);
+      y[8 * i + 2 * j] = gated(y[8 * i + 2 * j], f.x);
+      y[8 * i + 2 * j + 1] = gated(y[8 * i + 2 * j + 1], f.y);
     }
   }
 }
 
-template <int D, bool BF16, bool E4M3>
-__global__ void __launch_bounds__(128) k_tree_simple(const __grid_constant__ TreeAttendArgs A) {
-  __shared__ float s_o[4][D], s_m[4], s_l[4];
+template <class S>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_attend_tree(const __grid_constant__ TreeArgs A, const __grid_constant__ CUtensorMap km,
+                  const __grid_constant__ CUtensorMap vm) {
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+  uint8_t* conv = sm;                               // converted tiles
+  uint8_t* ring = sm + S::NC * S::TILE;
+  Control& C = *reinterpret_cast<Control*>(ring + S::NR * S::RAW);
   const moe_cache_attend_tree_t& a = A.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
+  const unsigned ALL = 0xFFFFFFFFu;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 12; ++i) {
+      mbar_init(&C.full[i], 1);
+      mbar_init(&C.empty[i], S::E4M3 ? 4 : 1);      // the converting warps, or the products that read it
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&C.c_full[i], 4);
+      mbar_init(&C.c_empty[i], 1);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&C.new_full[i], 1);
+      mbar_init(&C.fixed[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&C.s_full[i], 1);
+      mbar_init(&C.p_ready[i], 4);
+    }
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(&C.item_full[i], 1);
+      mbar_init(&C.item_empty[i], 10);
+    }
+    mbar_init(&C.pv_done, 1);
+    mbar_init(&C.drained, 1);
+    mbar_init(&C.q_ready, 4);
+    mbar_init(&C.q_free, 1);
+    mbar_init(&C.o_free, 4);
+    C.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(&C.tmem, 512);
+    tmem_relinquish();
+  }
   follow_predecessor();
-  int lo = 0, hi = A.B;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldcg(a.starts + mid + 1) > r) hi = mid; else lo = mid + 1;
-  }
-  if (lo >= A.B) return;
+  // an earlier call gave up and has not been reported: nothing is computed
+  const bool dead = __ldcg(A.status) & CACHE_BAD_WAIT;
+  // the units of all requests, a block of them to a warp
+  const int per = (A.B + THREADS / 32 - 1) / (THREADS / 32);
   uint32_t bad = 0;
-  const NewTokens t = new_tokens_of(a.starts, a.slots, a.lengths, lo, A.rows, A.max_len, A.most, &bad);
-  if (bad && threadIdx.x == 0) atomicOr(A.status, bad);
-  const int i = r - t.lo, older = t.len - t.n, g = h / A.group;
-  const int len = t.left_out || t.n == 0 ? 0 : t.len;
-  float q[D / 32], o[D / 32] = {}, m = -INFINITY, l = 0.f;
-  load_row<D, BF16, false>(a.q.p, r * a.q.row_stride + h * a.q.head_stride, lane, q);
-  const float scale = A.scale * (E4M3 ? __ldcg(a.k_scale + g) : 1.f);
-  for (int p = warp; p < len; p += 4) {
-    if (p >= older) {
-      const int j = p - older;
-      if (!(a.masks ? __ldcg(a.masks + (size_t)r * a.mask_words + (j >> 6)) >> (j & 63) & 1 : j <= i)) continue;
-    }
-    const int page = __ldcg(a.tables + (size_t)lo * a.table_stride + (p >> A.page_log2));
-    const bool in = page >= 0 && page < A.n_pages;
-    if (!in && lane == 0) atomicOr(A.status, CACHE_BAD_PAGE);
-    const int64_t off = ((int64_t)g << A.page_log2) * D + (int64_t)(p & ((1 << A.page_log2) - 1)) * D;
-    float k[D / 32] = {}, v[D / 32] = {}, s = 0.f;
-    if (in) {
-      load_row<D, BF16, E4M3>(a.k_cache, page * a.k_page_stride + off, lane, k);
-      load_row<D, BF16, E4M3>(a.v_cache, page * a.v_page_stride + off, lane, v);
+  {
+    long long sum = 0;
+    int longest = 0;
+    for (int i = lane; i < per && !dead; i += 32) {
+      const Request r = request<S>(A, warp * per + i < A.B ? warp * per + i : A.B, &bad);
+      sum += units_of(A, r);
+      if (r.n > 0) longest = max(longest, r.tiles + EXTRA);
     }
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) s += q[d] * k[d];
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    s *= scale;
-    const float top = fmaxf(m, s), w = exp2f(s - top), keep = m == -INFINITY ? 0.f : exp2f(m - top);
-    l = l * keep + w;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) o[d] = o[d] * keep + w * v[d];
-    m = top;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
+    longest = __reduce_max_sync(ALL, longest);
+    bad = __reduce_or_sync(ALL, bad);
+    if (lane == 0) {
+      C.sums[warp] = sum;
+      C.longest[warp] = longest;
+      if (bad && cta == 0) atomicOr(A.status, bad);
+    }
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = C.tmem;
+  const uint64_t limit = A.timeout_ns;
+  // By whole warps. A wait that runs out ends the CTA's work: everyone gives up at the next wait.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(ALL, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(ALL, mbar_wait_slow(bar, parity, limit))) return true;
+    if (!*(volatile int*)&C.abort) {
+      *(volatile int*)&C.abort = 1;
+      atomicOr(A.status, CACHE_BAD_WAIT);
+    }
+    return false;
+  };
+  // the next item, from the ring of items; k counts them
+  auto next_item = [&](int k, Item& it) {
+    if (!wait(&C.item_full[k % ITEMS], (k / ITEMS) & 1)) return false;
+    it = C.items[k % ITEMS];
+    return it.b >= 0;
+  };
+  auto done_item = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&C.item_empty[k % ITEMS]);
+  };
+
+  if (warp == W_FIND) {
+    long long total = 0;
+    int longest = 0;
+    for (int i = 0; i < THREADS / 32; ++i) {
+      total += C.sums[i];
+      longest = max(longest, C.longest[i]);
+    }
+    const long long even = total > 0 ? (total + ctas - 1) / ctas : 1;
+    const long long share = longest <= SHORT && even < longest ? longest : even;
+    long long u = share * cta;
+    const long long end = min(total, u + share);
+    int k = 0;
+    Part pt = {};
+    if (u < end) {
+      int base = 0;                                 // first request of the window of 32, and its first unit
+      long long at = 0;
+      for (int i = 0; i < THREADS / 32 && at + C.sums[i] <= u; ++i) {
+        at += C.sums[i];
+        base += per;
+      }
+      uint32_t none = 0;
+      Request r = request<S>(A, min(base + lane, A.B), &none);
+      long long upto = units_of(A, r);
+      auto scan = [&] {
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) s_o[warp][d / 2 * 64 + lane * 2 + d % 2] = o[d];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(ALL, upto, o);
+          if (lane >= o) upto += y;
+        }
+      };
+      scan();
+      while (u < end) {
+        const unsigned past = __ballot_sync(ALL, at + upto > u);
+        if (!past) {                                // the next 32 requests
+          at += __shfl_sync(ALL, upto, 31);
+          base += 32;
+          if (base >= A.B) break;
+          r = request<S>(A, min(base + lane, A.B), &none);
+          upto = units_of(A, r);
+          scan();
+          continue;
+        }
+        const int l = __ffs(past) - 1;
+        Request q;
+        q.lo = __shfl_sync(ALL, r.lo, l);
+        q.n = __shfl_sync(ALL, r.n, l);
+        q.older = __shfl_sync(ALL, r.older, l);
+        q.len = __shfl_sync(ALL, r.len, l);
+        q.tiles = __shfl_sync(ALL, r.tiles, l);
+        q.m_tiles = __shfl_sync(ALL, r.m_tiles, l);
+        const long long start = l ? at + __shfl_sync(ALL, upto, l - 1) : (__shfl_sync(ALL, upto, 0), at);
+        const int size = q.tiles + EXTRA;
+        const long long off = u - start, index = off / size;
+        const int j0 = (int)(off - index * size);
+        const long long first = u - j0;             // the item's first unit
+        const int j1 = (int)min((long long)size, end - first);
+        const int t0 = min(j0, q.tiles), t1 = min(j1, q.tiles);
+        if (q.tiles ? t0 < t1 : j0 == 0) {
+          if (!wait(&C.item_empty[k % ITEMS], ((k / ITEMS) & 1) ^ 1)) break;
+          if (lane == 0) {
+            Item it;
+            it.b = base + l;
+            it.lo = q.lo;
+            it.n = q.n;
+            it.older = q.older;
+            it.len = q.len;
+            it.g = (int)(index / q.m_tiles);
+            it.m0 = (int)(index % q.m_tiles) * M;
+            it.rows = (int)min((long long)M, (long long)q.n * A.group - it.m0);
+            it.t0 = t0;
+            it.t1 = t1;
+            it.part = t0 > 0 ? 0 : t1 < q.tiles ? 1 : -1;
+            it.pad = 0;
+            C.items[k % ITEMS] = it;
+            C.odd[k % ITEMS] = 0;
+            if (it.part == 1) {
+              pt.lo = it.lo;
+              pt.g = it.g;
+              pt.m0 = it.m0;
+              pt.rows = it.rows;
+              pt.last = (int)((first + q.tiles - 1) / share);
+            }
+            mbar_arrive(&C.item_full[k % ITEMS]);
+          }
+          ++k;
+          __syncwarp();
+        }
+        u = first + size;
+      }
+    }
+    if (!dead && lane == 0) A.joins[cta] = pt;
+    if (wait(&C.item_empty[k % ITEMS], ((k / ITEMS) & 1) ^ 1) && lane == 0) {
+      C.items[k % ITEMS].b = -1;
+      mbar_arrive(&C.item_full[k % ITEMS]);
+    }
+  } else if (warp == W_PRODUCE) {
+    const uint64_t policy = policy_evict_first();
+    const int ps = 1 << A.page_log2;
+    const int box = ps < S::TN ? ps : S::TN;        // tokens of a copy
+    const uint32_t bytes = (uint32_t)box * S::D * (S::E4M3 ? 1 : 2);
+    int at = 0, news = 0;                           // stages filled; those with values of new tokens, 16-bit
+    bool ok = true, skip = A.skip_copy && cta == 0;
+    Item it;
+    for (int k = 0; ok && next_item(k, it); ++k) {
+      done_item(k);
+      const int n = it.t1 - it.t0, held = (int)(((long long)it.len + ps - 1) >> A.page_log2);
+      const int32_t* row = a.tables + (size_t)it.b * a.table_stride;
+      auto entries = [&](int chunk) {               // 32 of the request's pages
+        const int p = chunk * 32 + lane;
+        if (p >= held) return -1;
+        const int id = __ldcg(row + p);
+        if (id >= 0 && id < A.n_pages) return id;
+        atomicOr(A.status, CACHE_BAD_PAGE);
+        return A.n_pages;                           // past the pool: copied as zeros
+      };
+      int chunk = ((int64_t)it.t0 * S::TN >> A.page_log2) >> 5;
+      int ids = n ? entries(chunk) : 0, next = n ? entries(chunk + 1) : 0;
+      auto ids_of = [&](int t) {
+        const int p = (int)((int64_t)t * S::TN >> A.page_log2);
+        if (p >> 5 != chunk) {
+          chunk = p >> 5;
+          ids = next;
+          next = entries(chunk + 1);
+        }
+        return __shfl_sync(ALL, ids, (p & 31) + lane & 31);
+      };
+      auto copy = [&](const CUtensorMap* map, int t, int id, bool values) {
+        const int st = at % S::NR;
+        // what is looked through first has barriers of its own: whoever looks waits for these alone, and would pass a
+        // stage's barrier, by its parity, on an earlier use of the stage
+        const bool fresh = !S::E4M3 && values && (int64_t)(t + 1) * S::TN > it.older;
+        uint64_t* bar = fresh ? &C.new_full[news % 8] : &C.full[st];
+        ok = ok && wait(&C.empty[st], ((at / S::NR) & 1) ^ 1);
+        if (!ok) return;
+        const int64_t tok = (int64_t)t * S::TN;
+        const int pages = min(S::TN / box, held - (int)(tok >> A.page_log2));
+        if (lane == 0) {
+          mbar_expect_tx(bar, bytes * pages);
+          if (fresh) mbar_arrive(&C.full[st]);
+        }
+        __syncwarp();
+        if (lane < pages && !skip) {
+          const int off = it.g * ps + (int)(tok & (ps - 1));
+          uint8_t* to = ring + st * S::RAW + lane * bytes;
+          if (S::E4M3) tma3(to, map, off, id, bar, policy);
+          else tma5(to, map, off >> 3, id, bar, policy);
+        }
+        skip = false;
+        ++at;
+        news += fresh;
+      };
+      int kid = n ? ids_of(it.t0) : 0;
+      if (n) copy(&km, it.t0, kid, false);
+      for (int t = it.t0; t < it.t1 && ok; ++t) {
+        const int vid = kid;
+        if (t + 1 < it.t1) {
+          kid = ids_of(t + 1);
+          copy(&km, t + 1, kid, false);
+        }
+        copy(&vm, t, vid, true);
+      }
+    }
+    // copies in flight land before the CTA ends
+    if (!ok || *(volatile int*)&C.abort) {
+      for (int i = max(0, at - S::NR); i < at; ++i) mbar_wait(&C.full[i % S::NR], (i / S::NR) & 1, 1000000);
+      for (int i = max(0, news - 8); i < news; ++i) mbar_wait(&C.new_full[i % 8], (i / 8) & 1, 1000000);
+    }
+  } else if (warp == W_MMA) {
+    int at = 0, tiles = 0, fixes = 0, items = 0;    // stages, tiles, looked-through tiles, items with tiles so far
+    bool ok = true;
+    Item it;
+    for (int k = 0; ok && next_item(k, it); ++k) {
+      done_item(k);
+      const int n = it.t1 - it.t0;
+      if (n == 0) continue;
+      ok = wait(&C.q_ready, items & 1);
+      tc_fence_after();
+      auto stage = [&](int i, uint32_t* addr, uint64_t** release) {   // waits for it
+        const int x = at + i;
+        if (S::E4M3) {
+          ok = ok && wait(&C.c_full[x % 4], (x / 4) & 1);
+          *addr = smem_u32(conv + x % 4 * S::TILE);
+          *release = &C.c_empty[x % 4];
+        } else {
+          ok = ok && wait(&C.full[x % S::NR], (x / S::NR) & 1);
+          *addr = smem_u32(ring + x % S::NR * S::RAW);
+          *release = &C.empty[x % S::NR];
+        }
+      };
+      auto scores = [&](int j) {                    // S = Q K^T of the item's tile j
+        uint32_t addr;
+        uint64_t* release;
+        stage(key_at(j), &addr, &release);
+        if (!ok) return;
+        const int left = it.len - (it.t0 + j) * S::TN;
+        const int cols = left < S::TN ? (left + 15) & ~15 : S::TN;
+        const uint32_t id = idesc(S::BF16, false, cols), s = tmem + S::S0 + (uint32_t)((tiles + j) & 1) * S::TN;
+        const uint64_t d = desc_sw128(addr, 0, S::GROUP);
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < S::D / 16; ++x)
+            umma_f16_ts(s, tmem + S::Q + x * 8, d + (x / 4) * 64 + (x % 4) * 2, id, x > 0);
+          umma_commit(release);
+          umma_commit(&C.s_full[(tiles + j) & 1]);
+          if (j == n - 1) umma_commit(&C.q_free);
+        }
+        __syncwarp();
+      };
+      if (ok) scores(0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) scores(j + 1);
+        const int g = tiles + j, left = it.len - (it.t0 + j) * S::TN;
+        ok = ok && wait(&C.p_ready[g & 1], (g >> 1) & 1);
+        if (j == 0) ok = ok && wait(&C.o_free, (items & 1) ^ 1);
+        if (!S::E4M3 && (int64_t)(it.t0 + j + 1) * S::TN > it.older) {
+          ok = ok && wait(&C.fixed[fixes % 8], (fixes / 8) & 1);
+          ++fixes;
+        }
+        uint32_t addr;
+        uint64_t* release;
+        stage(value_at(j, n), &addr, &release);
+        if (!ok) break;
+        tc_fence_after();
+        const int steps = left < S::TN ? (left + 15) >> 4 : S::TN / 16;
+        const uint32_t id = idesc(S::PBF16, true, S::D), p = tmem + S::S0 + (uint32_t)(g & 1) * S::TN;
+        const uint64_t d = desc_sw128(addr, 1024, S::GROUP);
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < S::TN / 16; ++x)
+            if (x < steps) umma_f16_ts(tmem + S::O, p + x * 8, d + (uint64_t)(x * 2 * S::GROUP >> 4), id, j > 0 || x > 0);
+          umma_commit(release);
+          umma_commit(&C.pv_done);
+        }
+        __syncwarp();
+      }
+      at += 2 * n;
+      tiles += n;
+      ++items;
+    }
+    // what was issued ends before tensor memory is given back
+    if (elect_one()) umma_commit(&C.drained);
+    __syncwarp();
+    mbar_wait(&C.drained, 0, 100000000);
+  } else if (warp >= W_PREP) {
+    const int t = threadIdx.x - W_PREP * 32, wq = warp - W_PREP;   // a row's thread
+    int at = 0, items = 0, news = 0;
+    bool ok = true;
+    Item it;
+    for (int k = 0; ok && next_item(k, it); ++k) {
+      const int n = it.t1 - it.t0;
+      if (n) {
+        // the queries, turned where the scale is negative: the largest score is then the largest product
+        const bool turn = A.scale * (S::E4M3 ? __ldcg(a.k_scale + it.g) : 1.f) < 0.f;
+        const int m = it.m0 + t, i = m / A.group;
+        const uint4* q = reinterpret_cast<const uint4*>(rows_at(a.q, it.lo + i, it.g * A.group + m - i * A.group));
+        uint32_t r[S::D / 2];
+#pragma unroll
+        for (int x = 0; x < S::D / 8; ++x) {
+          const uint4 v = t < it.rows ? __ldcg(q + x) : make_uint4(0, 0, 0, 0);
+          r[4 * x] = v.x;
+          r[4 * x + 1] = v.y;
+          r[4 * x + 2] = v.z;
+          r[4 * x + 3] = v.w;
+        }
+        if (turn)
+#pragma unroll
+          for (int x = 0; x < S::D / 2; ++x) r[x] ^= 0x80008000u;
+        ok = wait(&C.q_free, (items & 1) ^ 1);
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < S::D / 32; ++x) {
+          uint32_t c[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) c[y] = r[16 * x + y];
+          tmem_st16(tmem + ((uint32_t)(wq * 32) << 16) + S::Q + 16 * x, c);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C.q_ready);
+        ++items;
+      }
+      bool some = false;                            // values that are not finite
+      if (S::E4M3) {
+        // every tile, in the order of the stages
+        for (int x = 0; x < 2 * n && ok; ++x) {
+          const bool key = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
+          const int j = x == 0 ? 0 : x == 2 * n - 1 ? n - 1 : key ? (x + 1) / 2 : x / 2 - 1;
+          const int st = (at + x) % S::NR, cv = (at + x) % 4;
+          ok = ok && wait(&C.full[st], ((at + x) / S::NR) & 1) && wait(&C.c_empty[cv], (((at + x) / 4) & 1) ^ 1);
+          if (!ok) break;
+          const uint8_t* from = ring + st * S::RAW;
+          uint8_t* to = conv + cv * S::TILE;
+          const int tok0 = (it.t0 + j) * S::TN, left = it.len - tok0, fresh = it.older - tok0;
+          const int rows = left < S::TN ? (left + 15) & ~15 : S::TN;
+          constexpr int VR = S::D / 16;             // vectors of a row
+#pragma unroll 4
+          for (int e = t; e < rows * VR; e += 128) {
+            const int tok = e / VR, c = e % VR;
+            uint4 v = *reinterpret_cast<const uint4*>(from + e * 16);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w}, o[8];
+            if (!key && tok >= fresh) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t nan = __vcmpeq4(w[y] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                some = some || (nan && tok < left);
+                w[y] = tok < left ? w[y] & ~nan : 0u;
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if (key) codes4<S::BF16>(w[y], o[2 * y], o[2 * y + 1]);
+              else codes4<false>(w[y], o[2 * y], o[2 * y + 1]);
+            }
+            uint8_t* base = to + (tok >> 3) * S::GROUP + (c >> 2) * 1024 + (tok & 7) * 128;
+            const int turn = c >> 2 & 1;            // lanes of two blocks take their halves in other orders: other banks
+            const int c0 = (2 * (c & 3)) ^ (tok & 7), c1 = c0 ^ 1;
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(base + (turn ? c1 : c0) * 16) = turn ? hi : lo;
+            *reinterpret_cast<uint4*>(base + (turn ? c0 : c1) * 16) = turn ? lo : hi;
+          }
+          fence_proxy_async_smem();
+          if (__any_sync(ALL, some) && lane == 0) *(volatile int*)&C.odd[k % ITEMS] = 1;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&C.empty[st]);
+            mbar_arrive(&C.c_full[cv]);
+          }
+        }
+      } else {
+        // values of tiles with new tokens
+        int j = it.older / S::TN - it.t0;
+        for (j = j < 0 ? 0 : j; j < n && ok; ++j) {
+          const int x = at + value_at(j, n), st = x % S::NR;
+          ok = wait(&C.new_full[news % 8], (news / 8) & 1);
+          if (!ok) break;
+          uint8_t* v = ring + st * S::RAW;
+          const int tok0 = (it.t0 + j) * S::TN, left = it.len - tok0, fresh = max(0, it.older - tok0);
+          const int rows = left < S::TN ? (left + 15) & ~15 : S::TN;
+          constexpr int VR = S::D / 8;
+          for (int e = fresh * VR + t; e < rows * VR; e += 128) {
+            const int tok = e / VR, c = e % VR;
+            uint4* p = reinterpret_cast<uint4*>(v + (tok >> 3) * S::GROUP + (c >> 3) * 1024 + (tok & 7) * 128 +
+                                                (((c & 7) ^ (tok & 7)) << 4));
+            if (tok >= left) {
+              *p = make_uint4(0, 0, 0, 0);
+            } else {
+              const uint4 w = *p;
+              const uint4 f = make_uint4(finite2<S::BF16>(w.x), finite2<S::BF16>(w.y), finite2<S::BF16>(w.z),
+                                         finite2<S::BF16>(w.w));
+              if (f.x != w.x || f.y != w.y || f.z != w.z || f.w != w.w) {
+                *p = f;
+                some = true;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          if (__any_sync(ALL, some) && lane == 0) *(volatile int*)&C.odd[k % ITEMS] = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&C.fixed[news % 8]);
+          ++news;
+        }
+      }
+      at += 2 * n;
+      done_item(k);
+    }
+  } else if (warp >= W_SOFT) {
+    const int wq = warp - W_SOFT, t = threadIdx.x - W_SOFT * 32;
+    const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+    int tiles = 0;
+    bool ok = true;
+    Item it;
+    for (int k = 0; ok && next_item(k, it); ++k) {
+      const int n = it.t1 - it.t0, m = it.m0 + t, i = m / A.group, h = it.g * A.group + m - i * A.group;
+      const bool row = t < it.rows;
+      Mask mask;
+      mask.load(A, it.lo + i, i, it.len - it.older, row && n);
+      float c = fabsf(A.scale * (S::E4M3 ? __ldcg(a.k_scale + it.g) : 1.f));
+      c = c < 0x1p-149f ? 0x1p-149f : c;            // a score of -inf stays one when the scale is 0
+      float ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++tiles) {
+        ok = wait(&C.s_full[tiles & 1], (tiles >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t s = lanes + S::S0 + (uint32_t)(tiles & 1) * S::TN;
+        const int rel = (it.t0 + j) * S::TN - it.older;
+        const bool edge = rel + S::TN > 0;
+        float top = -INFINITY;
+        uint32_t r[32];
+#pragma unroll
+        for (int x = 0; x < S::TN; x += 32) {
+          tmem_ld32(s + x, r);
+          tmem_wait_ld32(r);
+          if (edge) {
+            const uint32_t w = mask.window(rel + x);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (w >> y & 1) top = fmaxf(top, __uint_as_float(r[y]));
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) top = fmaxf(top, __uint_as_float(r[y]));
+          }
+        }
+        top *= c;
+        // the base follows
+        const bool up = top > ref + S::TAU || (ref == -INFINITY && top > ref);
+        if (__any_sync(ALL, up)) {
+          const float f = up ? exp2_fast(ref - top) : 1.f;
+          if (up) ref = top;
+          l *= f;
+          if (j > 0) {
+            ok = wait(&C.pv_done, (tiles - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < S::D; x += 32) {
+              __syncwarp();
+              tmem_ld32(lanes + S::O + x, r);
+              tmem_wait_ld32(r);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * f);
+              tmem_st32(lanes + S::O + x, r);
+            }
+          }
+        }
+        const float base = ref == -INFINITY ? 0.f : ref - S::LIFT;
+        float sum0 = 0.f, sum1 = 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < S::TN; x += 32) {
+          tmem_ld32(s + x, r);
+          tmem_wait_ld32(r);
+          const uint32_t w = edge ? mask.window(rel + x) : ALL;
+          uint32_t p[16];
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            float e0 = exp2_fast(fmaf(__uint_as_float(r[y]), c, -base));
+            float e1 = exp2_fast(fmaf(__uint_as_float(r[y + 1]), c, -base));
+            if (edge) {
+              e0 = w >> y & 1 ? e0 : 0.f;
+              e1 = w >> (y + 1) & 1 ? e1 : 0.f;
+            }
+            sum0 += e0;
+            sum1 += e1;
+            p[y / 2] = pack2<S::PBF16>(e0, e1);
+          }
+          tmem_st16(s + x / 2, p);
+        }
+        l += sum0 + sum1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C.p_ready[tiles & 1]);
+      }
+      if (!ok) break;
+      // what the item's rows get
+      if (n) {                                      // the last but one first: parities tell neighbours apart alone
+        ok = (tiles < 2 || wait(&C.pv_done, tiles & 1)) && wait(&C.pv_done, (tiles - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool patch = n && *(volatile int*)&C.odd[k % ITEMS];
+      const float vs = S::E4M3 ? __ldcg(a.v_scale + it.g) : 1.f;
+      const float by = l == 0.f ? 0.f : vs / l;
+      float* part = A.parts + (size_t)(cta * 2 + (it.part > 0)) * S::PART;
+      const int ps = 1 << A.page_log2;
+#pragma unroll 1
+      for (int x = 0; x < S::D; x += 32) {
+        float y[32];
+        if (n) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(lanes + S::O + x, r);
+          tmem_wait_ld32(r);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(r[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = 0.f;
+        }
+        if (patch) {
+          const int from = max(it.older, it.t0 * S::TN), upto = (int)min((int64_t)it.len, (int64_t)it.t1 * S::TN);
+          for (int p = from; p < upto; ++p) {
+            const int j = p - it.older;
+            if (!(mask.word(j >> 5) >> (j & 31) & 1)) continue;
+            const int page = __ldcg(a.tables + (size_t)it.b * a.table_stride + (p >> A.page_log2));
+            if (page < 0 || page >= A.n_pages) continue;
+            const int64_t at = page * a.v_page_stride + ((int64_t)it.g * ps + (p & (ps - 1))) * S::D + x;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float v;
+              if (S::E4M3) {
+                uint32_t lo, hi;
+                e4m3x4_to_f16x4(__ldcg((const uint8_t*)a.v_cache + at + e), lo, hi);
+                v = unpack2<false>(lo).x;
+              } else {
+                v = unpack2<S::BF16>(__ldcg((const unsigned short*)a.v_cache + at + e)).x;
+              }
+              y[e] += odd<S::BF16>(v);
+            }
+          }
+        }
+        if (it.part >= 0) {                         // [D / 4][rows] of four elements
+          if (row)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              __stcg(reinterpret_cast<float4*>(part) + (x + e) / 4 * M + t, make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]));
+          continue;
+        }
+        if (!row) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = l == 0.f ? 0.f : y[e] * by;
+        if (a.gate.p) gate32<S::BF16>(y, rows_at(a.gate, it.lo + i, h) + x);
+        uint4* out = reinterpret_cast<uint4*>(rows_at(a.out, it.lo + i, h) + x);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+          out[e / 8] = make_uint4(pack2<S::BF16>(y[e], y[e + 1]), pack2<S::BF16>(y[e + 2], y[e + 3]),
+                                  pack2<S::BF16>(y[e + 4], y[e + 5]), pack2<S::BF16>(y[e + 6], y[e + 7]));
+      }
+      if (it.part >= 0 && row) {
+        __stcg(part + M * S::D + t, ref);
+        __stcg(part + M * S::D + M + t, l);
+      }
+      if (n) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C.o_free);
+      }
+      done_item(k);
+    }
   }
   __syncthreads();
-  const float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float total = 0.f, w[4];
-  for (int k = 0; k < 4; ++k) {
-    w[k] = s_m[k] == -INFINITY && s_l[k] == 0.f ? 0.f : exp2f(s_m[k] - top);
-    total += w[k] * s_l[k];
-  }
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float y = 0.f;
-    for (int k = 0; k < 4; ++k) y += w[k] == 0.f ? 0.f : w[k] * s_o[k][d];
-    y = total == 0.f ? 0.f : y / total * (E4M3 ? __ldcg(a.v_scale + g) : 1.f);
-    if (a.gate.p) {
-      const uint16_t c = __ldcg((const unsigned short*)a.gate.p + r * a.gate.row_stride + h * a.gate.head_stride + d);
-      y /= 1.f + __expf(-unpack2<BF16>(c).x);
+  if (warp == W_MMA) tmem_dealloc(tmem, 512);
+}
+
+// ---- the parts of split items ----
+// A block to 32 rows and 16 elements of an item: its warps take the parts in turn.
+constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
+
+template <class S>
+__global__ void __launch_bounds__(JOIN_THREADS) k_join_tree(const __grid_constant__ TreeArgs A, int ctas) {
+  __shared__ float4 s_o[JOIN_WARPS][4][32];
+  __shared__ float s_m[JOIN_WARPS][32], s_l[JOIN_WARPS][32];
+  __shared__ int s_end[MAX_CTAS];
+  const moe_cache_attend_tree_t& a = A.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  follow_predecessor();
+  if (__ldcg(A.status) & CACHE_BAD_WAIT) return;
+  // blocks of work of each item, summed up
+  if (warp == 0) {
+    int sum = 0;
+    for (int c0 = 0; c0 < ctas; c0 += 32) {
+      const int c = c0 + lane;
+      int v = 0;
+      if (c < ctas && __ldcg(&A.joins[c].last)) v = (__ldcg(&A.joins[c].rows) + 31) / 32 * (S::D / 16);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (c < ctas) s_end[c] = sum + v;
+      sum += __shfl_sync(0xFFFFFFFFu, v, 31);
     }
-    ((uint16_t*)a.out.p)[r * a.out.row_stride + h * a.out.head_stride + d] = (uint16_t)pack2<BF16>(y, 0.f);
+  }
+  __syncthreads();
+  const int total = s_end[ctas - 1];
+  for (int w = blockIdx.x; w < total; w += gridDim.x) {
+    int lo = 0, hi = ctas - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_end[mid] > w) hi = mid; else lo = mid + 1;
+    }
+    Part pt;
+    *reinterpret_cast<int4*>(&pt) = __ldcg(reinterpret_cast<const int4*>(A.joins + lo));
+    pt.last = __ldcg(&A.joins[lo].last);
+    const int k = w - (lo ? s_end[lo - 1] : 0), x = k % (S::D / 16) * 16, r = k / (S::D / 16) * 32 + lane;
+    const int parts = pt.last - lo + 1;
+    const bool row = r < pt.rows;
+    // each warp's parts on their own base
+    float m = -INFINITY, l = 0.f;
+    float4 o[4] = {};
+    auto part_at = [&](int p) { return A.parts + (size_t)((lo + p) * 2 + (p == 0)) * S::PART; };
+    if (row)
+      for (int p = warp; p < parts; p += JOIN_WARPS) {
+        const float* part = part_at(p);
+        const float pm = __ldcg(part + M * S::D + r), pl = __ldcg(part + M * S::D + M + r);
+        float4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(part) + (x / 4 + e) * M + r);
+        const float top = fmaxf(m, pm);
+        const float keep = m == -INFINITY ? 0.f : exp2_fast(m - top), add = pm == -INFINITY ? (pl == pl ? 0.f : pl) : exp2_fast(pm - top);
+        l = l * keep + pl * add;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[e].x = o[e].x * keep + v[e].x * add;
+          o[e].y = o[e].y * keep + v[e].y * add;
+          o[e].z = o[e].z * keep + v[e].z * add;
+          o[e].w = o[e].w * keep + v[e].w * add;
+        }
+        m = top;
+      }
+    s_m[warp][lane] = m;
+    s_l[warp][lane] = l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s_o[warp][e][lane] = o[e];
+    __syncthreads();
+    // eight threads to a row, two elements each
+    const int rr = threadIdx.x >> 3, e = threadIdx.x & 7, rt = k / (S::D / 16) * 32 + rr;
+    if (rt < pt.rows) {
+      float top = -INFINITY, sum = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < JOIN_WARPS; ++i) top = fmaxf(top, s_m[i][rr]);
+#pragma unroll
+      for (int i = 0; i < JOIN_WARPS; ++i) {
+        if (i >= parts) break;
+        const float f = s_m[i][rr] == -INFINITY ? (s_l[i][rr] == s_l[i][rr] ? 0.f : s_l[i][rr]) : exp2_fast(s_m[i][rr] - top);
+        const float2 v = reinterpret_cast<const float2*>(&s_o[i][e >> 1][rr])[e & 1];
+        sum += s_l[i][rr] * f;
+        y0 += v.x * f;
+        y1 += v.y * f;
+      }
+      const float by = (S::E4M3 ? __ldcg(a.v_scale + pt.g) : 1.f) / sum;
+      y0 = sum == 0.f ? 0.f : y0 * by;
+      y1 = sum == 0.f ? 0.f : y1 * by;
+      const int mm = pt.m0 + rt, i = mm / A.group, h = pt.g * A.group + mm - i * A.group;
+      if (a.gate.p) {
+        const float2 g = unpack2<S::BF16>(__ldcg(reinterpret_cast<const uint32_t*>(rows_at(a.gate, pt.lo + i, h) + x + 2 * e)));
+        y0 = gated(y0, g.x);
+        y1 = gated(y1, g.y);
+      }
+      *reinterpret_cast<uint32_t*>(rows_at(a.out, pt.lo + i, h) + x + 2 * e) = pack2<S::BF16>(y0, y1);
+    }
+    __syncthreads();
   }
 }
 
-template <int D>
-cudaError_t run(const CacheShape& S, const TreeAttendArgs& A, cudaStream_t st) {
-  auto* k = S.bf16 ? (S.e4m3 ? k_tree_simple<D, true, true> : k_tree_simple<D, true, false>)
-                   : (S.e4m3 ? k_tree_simple<D, false, true> : k_tree_simple<D, false, false>);
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(A.rows, A.Hq);
-  c.blockDim = dim3(128);
-  c.stream = st;
-  return cudaLaunchKernelEx(&c, k, A);
+// ---- launches ----
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+std::atomic<EncodeFn> g_encode{nullptr};
+
+cudaError_t encode_fn(EncodeFn* out) {
+  EncodeFn f = g_encode.load(std::memory_order_relaxed);
+  if (!f) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+    g_encode.store(f = reinterpret_cast<EncodeFn>(p), std::memory_order_relaxed);
+  }
+  *out = f;
+  return cudaSuccess;
 }
+
+// a pool: 16-bit as blocks of 8 tokens x 64 elements, 8-bit as rows of a head's elements
+template <class S>
+cudaError_t pool_map(const CacheShape& c, const void* pool, int64_t page_stride, CUtensorMap* m) {
+  EncodeFn fn;
+  const cudaError_t e = encode_fn(&fn);
+  if (e != cudaSuccess) return e;
+  const int ps = 1 << c.page_log2, box_tokens = ps < S::TN ? ps : S::TN;
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  CUresult r;
+  if (S::E4M3) {
+    const cuuint64_t dims[3] = {(cuuint64_t)S::D, (cuuint64_t)c.Hkv * ps, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)S::D, (cuuint64_t)page_stride};
+    const cuuint32_t box[3] = {(cuuint32_t)S::D, (cuuint32_t)box_tokens, 1};
+    r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, (void*)pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else {
+    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)S::BLOCKS, (cuuint64_t)c.Hkv * ps / 8, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)S::D * 2, 128, (cuuint64_t)S::D * 16, (cuuint64_t)page_stride * 2};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)S::BLOCKS, (cuuint32_t)box_tokens / 8, 1};
+    r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, (void*)pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <class S>
+cudaError_t run(const CacheShape& c, const TreeArgs& A, int ctas, cudaStream_t st) {
+  CUtensorMap km, vm;
+  cudaError_t e = pool_map<S>(c, A.a.k_cache, A.a.k_page_stride, &km);
+  if (e == cudaSuccess) e = pool_map<S>(c, A.a.v_cache, A.a.v_page_stride, &vm);
+  // the kernel's shared-memory limit, once per device
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (e == cudaSuccess && !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k_attend_tree<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::DYN);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  if (e == cudaSuccess) e = launch_following(k_attend_tree<S>, ctas, THREADS, S::DYN, st, A, km, vm);
+  if (e == cudaSuccess) e = launch_following(k_join_tree<S>, ctas * 4, JOIN_THREADS, 0, st, A, ctas);
+  return e;
+}
+template <int D>
+cudaError_t run_types(const CacheShape& c, const TreeArgs& A, int ctas, cudaStream_t st) {
+  if (c.bf16) return c.e4m3 ? run<Shape<D, true, true>>(c, A, ctas, st) : run<Shape<D, true, false>>(c, A, ctas, st);
+  return c.e4m3 ? run<Shape<D, false, true>>(c, A, ctas, st) : run<Shape<D, false, false>>(c, A, ctas, st);
+}
+int ctas_of(int num_sms) { return num_sms < MAX_CTAS ? num_sms : MAX_CTAS; }
 
 }  // namespace
 
-size_t cache_attend_tree_workspace(int num_sms, int head_dim) { return 256; }
+size_t cache_attend_tree_workspace(int num_sms, int head_dim) {
+  return (size_t)ctas_of(num_sms) * (sizeof(Part) + 2 * (size_t)(M * head_dim + 2 * M) * 4);
+}
 
 cudaError_t cache_attend_tree_launch(const CacheShape& S, const moe_cache_attend_tree_t& a, const CacheTreeState& w,
                                      cudaStream_t st) {
-  TreeAttendArgs A;
+  TreeArgs A;
   A.a = a;
   A.B = (int)a.n_requests;
   A.rows = (int)a.n_rows;
-  A.Hq = S.Hq;
   A.Hkv = S.Hkv;
   A.group = S.Hq / S.Hkv;
   A.page_log2 = S.page_log2;
@@ -136,8 +1064,13 @@ cudaError_t cache_attend_tree_launch(const CacheShape& S, const moe_cache_attend
   A.most = a.masks && 64 * (int)a.mask_words < w.max_new ? 64 * (int)a.mask_words : w.max_new;
   A.max_len = (long long)S.max_pages << S.page_log2;
   A.scale = (float)a.scale * LOG2E;
+  const int ctas = ctas_of(w.num_sms);
+  A.joins = (Part*)w.workspace;
+  A.parts = (float*)(A.joins + ctas);
   A.status = w.status;
-  return S.D == 64 ? run<64>(S, A, st) : S.D == 128 ? run<128>(S, A, st) : run<256>(S, A, st);
+  A.timeout_ns = w.timeout_ns;
+  A.skip_copy = w.skip_copy;
+  return S.D == 64 ? run_types<64>(S, A, ctas, st) : S.D == 128 ? run_types<128>(S, A, ctas, st) : run_types<256>(S, A, ctas, st);
 }
 
 }  // namespace moe
