@@ -74,7 +74,7 @@ struct Item {
 };
 
 struct Control {
-  uint64_t full[12], empty[12], c_full[4], c_empty[4], new_full[8], fixed[8], s_full[2], p_ready[2], pv_done, q_ready, q_free, o_free, drained;
+  uint64_t full[12], empty[12], c_full[4], c_empty[4], new_full[8], fixed[8], s_full[2], p_ready[2], pv_done, q_ready, q_free, o_free, o_full, drained;
   uint64_t item_full[ITEMS], item_empty[ITEMS];
   long long sums[THREADS / 32];
   int longest[THREADS / 32];
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&C.item_empty[i], 10);
     }
     mbar_init(&C.pv_done, 1);
+    mbar_init(&C.o_full, 1);
     mbar_init(&C.drained, 1);
     mbar_init(&C.q_ready, 4);
     mbar_init(&C.q_free, 1);
@@ -571,6 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (x < steps) umma_f16_ts(tmem + S::O, p + x * 8, d + (uint64_t)(x * 2 * S::GROUP >> 4), id, j > 0 || x > 0);
           umma_commit(release);
           umma_commit(&C.pv_done);
+          if (j == n - 1) umma_commit(&C.o_full);
         }
         __syncwarp();
       }
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp >= W_SOFT) {
     const int wq = warp - W_SOFT, t = threadIdx.x - W_SOFT * 32;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-    int tiles = 0;
+    int tiles = 0, items = 0;
     bool ok = true;
     Item it;
     for (int k = 0; ok && next_item(k, it); ++k) {
@@ -749,7 +751,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float f = up ? exp2_fast(ref - top) : 1.f;
           if (up) ref = top;
           l *= f;
-          if (j > 0) {
+          if (j > 0) {                              // the product of the tile before; the one before that is done
             ok = wait(&C.pv_done, (tiles - 1) & 1);
             if (!ok) break;
             tc_fence_after();
@@ -795,8 +797,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!ok) break;
       // what the item's rows get
-      if (n) {                                      // the last but one first: parities tell neighbours apart alone
-        ok = (tiles < 2 || wait(&C.pv_done, tiles & 1)) && wait(&C.pv_done, (tiles - 1) & 1);
+      if (n) {
+        ok = wait(&C.o_full, items++ & 1);
         if (!ok) break;
         tc_fence_after();
       }
