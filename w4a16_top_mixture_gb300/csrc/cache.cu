@@ -389,6 +389,8 @@ extern "C" int moe_cache_get_status(moe_cache_t* c, uint32_t* flags) {
   // the counts of parts too where a call gave up, which may have left some behind
   if (e == cudaSuccess && st & CACHE_BAD_WAIT) e = cudaMemset(c->mem, 0, CTL_WORDS * 4);
   if (e == cudaSuccess && st & CACHE_BAD_WAIT) e = cudaMemset(c->workspace, 0, c->workspace_bytes);
+  if (e == cudaSuccess && st & CACHE_BAD_WAIT && c->reserved)
+    e = cudaMemset(c->reserved + moves_bytes(c), 0, CACHE_TREE_COUNTS);
   if (e == cudaSuccess && st) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return report_cuda(e, "moe_cache_get_status");
   if (flags) *flags = st;

@@ -51,6 +51,7 @@ cudaError_t cache_attend_launch(const CacheShape& S, const moe_cache_attend_t& a
 cudaError_t cache_tree_launch(const CacheShape& S, const moe_cache_tree_t& t, int max_new, uint32_t* status,
                               cudaStream_t st);
 
+constexpr int CACHE_TREE_COUNTS = 12288;  // bytes of counts at the workspace's start, zeroed once and after a lost wait
 struct CacheTreeState {
   void* workspace;                       // cache_attend_tree_workspace bytes
   uint32_t* status;

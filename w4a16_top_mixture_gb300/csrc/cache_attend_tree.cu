@@ -29,15 +29,10 @@ namespace moe {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int THREADS = 384, MAX_CTAS = 1024, EXTRA = 2, SHORT = 5, ITEMS = 4, M = 128;
-constexpr int SMEM = 227 * 1024, MISC = 2048;
-constexpr int W_PRODUCE = 0, W_MMA = 1, W_FIND = 2, W_SOFT = 4, W_PREP = 8;
-
-struct Part {                // of an item that starts in a CTA and ends in another
-  int lo, g, m0, rows;       // its first row in the batch, key-value head, first row and rows of the item's 128
-  int last;                  // the CTA of its last part; 0: there is no such item
-  int pad[3];
-};
+constexpr int THREADS = 512, MAX_CTAS = 1024, EXTRA = 2, SHORT = 5, ITEMS = 4, M = 128;
+constexpr int GROUP_OF = 8, FLAT = 12;    // parts that are joined at once; from FLAT + 1 on in groups first
+constexpr int SMEM = 227 * 1024, MISC = 3072;
+constexpr int W_PRODUCE = 0, W_MMA = 1, W_FIND = 2, W_SOFT = 4, W_PREP = 12, SOFT = 8;   // SOFT: warps of the softmax
 
 struct TreeArgs {
   moe_cache_attend_tree_t a;
@@ -45,7 +40,7 @@ struct TreeArgs {
   long long max_len;
   float scale;               // with log2(e)
   float* parts;              // [CTA][2][M * D + 2 * M]: the item a CTA begins in the middle of, the one it leaves so
-  Part* joins;               // [CTA]
+  uint32_t* counts;          // [CTA][3]: parts that have arrived, of an item, of its group of parts that starts in the CTA
   uint32_t* status;
   uint64_t timeout_ns;
   int skip_copy;
@@ -59,10 +54,10 @@ struct Shape {
   static constexpr int BLOCKS = D / 64, GROUP = BLOCKS * 1024;                 // of 8 tokens
   static constexpr int TILE = TN / 8 * GROUP, RAW = E4M3 ? TN * D : TILE;
   static constexpr int NC = E4M3 ? 4 : 0;                                      // converted tiles
-  static constexpr int NR0 = (SMEM - 1024 - MISC - NC * TILE) / RAW, NR = NR0 > 12 ? 12 : NR0;
-  static constexpr int DYN = 1024 + NC * TILE + NR * RAW + MISC;
+  static constexpr int NR0 = (SMEM - MISC - NC * TILE) / RAW, NR = NR0 > 12 ? 12 : NR0;
+  static constexpr int DYN = NC * TILE + NR * RAW + MISC;
   static constexpr uint32_t O = 0, Q = D, S0 = D + D / 2;                      // columns of tensor memory
-  static constexpr float TAU = PBF16 ? 8.f : 2.f, LIFT = PBF16 ? 0.f : 13.f;
+  static constexpr float TAU = 8.f, LIFT = PBF16 ? 0.f : 7.f;                  // fp16: 2^15 at most
   static constexpr int PART = M * D + 2 * M;
   static_assert(S0 + 2 * TN <= 512 && DYN <= SMEM && NR >= 4, "fits");
 };
@@ -70,16 +65,20 @@ struct Shape {
 struct Item {
   int b, lo, n, older, len;  // b < 0: no more items. n: rows of the batch
   int g, m0, rows;           // key-value head; first row of the 128 and how many there are
-  int t0, t1, part, pad;     // tiles; -1: the whole item, else which of the CTA's two parts
+  int t0, t1;                // tiles
+  int c0, c1;                // the CTAs of its first and last tile
 };
 
 struct Control {
-  uint64_t full[12], empty[12], c_full[4], c_empty[4], new_full[8], fixed[8], s_full[2], p_ready[2], pv_done, q_ready, q_free, o_free, o_full, drained;
+  // new_full, fixed: of the tiles that are looked through, or (c_full, c_empty) of the converted ones
+  uint64_t full[12], empty[12], new_full[8], fixed[8], s_full[2], p_ready[2], pv_done, q_ready, q_free, o_free, o_full, drained, pair[4][2], soft;
   uint64_t item_full[ITEMS], item_empty[ITEMS];
   long long sums[THREADS / 32];
   int longest[THREADS / 32];
   Item items[ITEMS];
   int odd[ITEMS];            // values that are not finite were taken out
+  int last;                  // this CTA's part is the last to arrive
+  float top[2][2][M];        // maxima of the halves of a row's tokens in a tile; their sums at an item's end
   uint32_t tmem;
   int abort;
 };
@@ -213,8 +212,6 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
   if ((v >> 16 & e) == e) v &= 0xFFFFu;
   return v;
 }
-template <bool BF16>
-__device__ __forceinline__ float odd(float x) { return fabsf(x) <= 3.4028234663852886e38f ? 0.f : x; }
 
 // e4m3 codes to 16-bit pairs, four at a time
 template <bool BF16>
@@ -227,18 +224,29 @@ __device__ __forceinline__ void codes4(uint32_t v, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-// 32 elements of a row, fp32
-template <bool BF16>
-__device__ __forceinline__ void gate32(float (&y)[32], const uint16_t* at) {
+// what was taken out of the values of new tokens, for the rows that see them: 32 elements from x on
+template <class S>
+__device__ __noinline__ void add_odd(const TreeArgs& A, const Item it, const Mask& mask, int x, uint32_t (&r)[32]) {
+  const moe_cache_attend_tree_t& a = A.a;
+  const int ps = 1 << A.page_log2;
+  const int from = max(it.older, it.t0 * S::TN), upto = (int)min((int64_t)it.len, (int64_t)it.t1 * S::TN);
+  for (int p = from; p < upto; ++p) {
+    const int j = p - it.older;
+    if (!(mask.word(j >> 5) >> (j & 31) & 1)) continue;
+    const int page = __ldcg(a.tables + (size_t)it.b * a.table_stride + (p >> A.page_log2));
+    if (page < 0 || page >= A.n_pages) continue;
+    const int64_t at = page * a.v_page_stride + ((int64_t)it.g * ps + (p & (ps - 1))) * S::D + x;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(at) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2<BF16>(w[j]);
-      y[8 * i + 2 * j] = gated(y[8 * i + 2 * j], f.x);
-      y[8 * i + 2 * j + 1] = gated(y[8 * i + 2 * j + 1], f.y);
+    for (int e = 0; e < 32; ++e) {
+      float v;
+      if (S::E4M3) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16x4(__ldcg((const uint8_t*)a.v_cache + at + e), lo, hi);
+        v = unpack2<false>(lo).x;
+      } else {
+        v = unpack2<S::BF16>(__ldcg((const unsigned short*)a.v_cache + at + e)).x;
+      }
+      if (!(fabsf(v) <= 3.4028234663852886e38f)) r[e] = __float_as_uint(__uint_as_float(r[e]) + v);
     }
   }
 }
@@ -247,42 +255,47 @@ template <class S>
 __global__ void __launch_bounds__(THREADS, 1)
     k_attend_tree(const __grid_constant__ TreeArgs A, const __grid_constant__ CUtensorMap km,
                   const __grid_constant__ CUtensorMap vm) {
-  extern __shared__ uint8_t sm_raw[];
-  uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (smem_u32(sm) & 1023) {                        // the swizzle needs it, and the attribute gives it
+    if (threadIdx.x == 0) atomicOr(A.status, CACHE_BAD_WAIT);
+    return;
+  }
   uint8_t* conv = sm;                               // converted tiles
   uint8_t* ring = sm + S::NC * S::TILE;
   Control& C = *reinterpret_cast<Control*>(ring + S::NR * S::RAW);
   const moe_cache_attend_tree_t& a = A.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
   const unsigned ALL = 0xFFFFFFFFu;
+  uint64_t *c_full = C.new_full, *c_empty = C.fixed;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 12; ++i) {
       mbar_init(&C.full[i], 1);
       mbar_init(&C.empty[i], S::E4M3 ? 4 : 1);      // the converting warps, or the products that read it
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&C.c_full[i], 4);
-      mbar_init(&C.c_empty[i], 1);
-    }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&C.new_full[i], 1);
-      mbar_init(&C.fixed[i], 4);
+      mbar_init(&C.new_full[i], S::E4M3 ? 4 : 1);
+      mbar_init(&C.fixed[i], S::E4M3 ? 1 : 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&C.s_full[i], 1);
-      mbar_init(&C.p_ready[i], 4);
+      mbar_init(&C.p_ready[i], SOFT);
     }
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(&C.item_full[i], 1);
-      mbar_init(&C.item_empty[i], 10);
+      mbar_init(&C.item_empty[i], 2 + SOFT + 4);
     }
     mbar_init(&C.pv_done, 1);
     mbar_init(&C.o_full, 1);
     mbar_init(&C.drained, 1);
     mbar_init(&C.q_ready, 4);
     mbar_init(&C.q_free, 1);
-    mbar_init(&C.o_free, 4);
+    mbar_init(&C.o_free, SOFT);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&C.pair[i][0], 2);
+      mbar_init(&C.pair[i][1], 2);
+    }
+    mbar_init(&C.soft, SOFT);
     C.abort = 0;
     fence_mbar_init();
   }
@@ -294,13 +307,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   // an earlier call gave up and has not been reported: nothing is computed
   const bool dead = __ldcg(A.status) & CACHE_BAD_WAIT;
   // the units of all requests, a block of them to a warp
-  const int per = (A.B + THREADS / 32 - 1) / (THREADS / 32);
+  const bool few = A.B <= 32;                       // the finding warp sees them all
+  const int per = few ? 32 : (A.B + THREADS / 32 - 1) / (THREADS / 32);
   uint32_t bad = 0;
-  {
+  if (!few) {
     long long sum = 0;
     int longest = 0;
     for (int i = lane; i < per && !dead; i += 32) {
-      const Request r = request<S>(A, warp * per + i < A.B ? warp * per + i : A.B, &bad);
+      const Request r = request<S>(A, min(warp * per + i, A.B), &bad);
       sum += units_of(A, r);
       if (r.n > 0) longest = max(longest, r.tiles + EXTRA);
     }
@@ -341,45 +355,56 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp == W_FIND) {
-    long long total = 0;
+    uint32_t bad = 0;
+    Request r = {};
+    long long total = 0, upto = 0;
     int longest = 0;
-    for (int i = 0; i < THREADS / 32; ++i) {
-      total += C.sums[i];
-      longest = max(longest, C.longest[i]);
+    auto window = [&](int base) {                   // 32 requests and where their units end
+      r = request<S>(A, dead ? A.B : min(base + lane, A.B), &bad);
+      upto = units_of(A, r);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(ALL, upto, o);
+        if (lane >= o) upto += y;
+      }
+    };
+    if (few) {
+      window(0);
+      total = __shfl_sync(ALL, upto, 31);
+      longest = __reduce_max_sync(ALL, r.n > 0 ? r.tiles + EXTRA : 0);
+      bad = __reduce_or_sync(ALL, bad);
+      if (bad && cta == 0 && lane == 0) atomicOr(A.status, bad);
+    } else {
+      for (int i = 0; i < THREADS / 32; ++i) {
+        total += C.sums[i];
+        longest = max(longest, C.longest[i]);
+      }
     }
-    const long long even = total > 0 ? (total + ctas - 1) / ctas : 1;
+    auto quotient = [](long long x, long long y) {  // of numbers that mostly fit 32 bits
+      return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+    };
+    const long long even = total > 0 ? quotient(total + ctas - 1, ctas) : 1;
     const long long share = longest <= SHORT && even < longest ? longest : even;
     long long u = share * cta;
     const long long end = min(total, u + share);
     int k = 0;
-    Part pt = {};
     if (u < end) {
-      int base = 0;                                 // first request of the window of 32, and its first unit
+      int base = 0;                                 // first request of the window, and its first unit
       long long at = 0;
-      for (int i = 0; i < THREADS / 32 && at + C.sums[i] <= u; ++i) {
-        at += C.sums[i];
-        base += per;
-      }
-      uint32_t none = 0;
-      Request r = request<S>(A, min(base + lane, A.B), &none);
-      long long upto = units_of(A, r);
-      auto scan = [&] {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(ALL, upto, o);
-          if (lane >= o) upto += y;
+      if (!few) {
+        for (int i = 0; i < THREADS / 32 && at + C.sums[i] <= u; ++i) {
+          at += C.sums[i];
+          base += per;
         }
-      };
-      scan();
+        window(base);
+      }
       while (u < end) {
         const unsigned past = __ballot_sync(ALL, at + upto > u);
         if (!past) {                                // the next 32 requests
           at += __shfl_sync(ALL, upto, 31);
           base += 32;
           if (base >= A.B) break;
-          r = request<S>(A, min(base + lane, A.B), &none);
-          upto = units_of(A, r);
-          scan();
+          window(base);
           continue;
         }
         const int l = __ffs(past) - 1;
@@ -390,14 +415,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         q.len = __shfl_sync(ALL, r.len, l);
         q.tiles = __shfl_sync(ALL, r.tiles, l);
         q.m_tiles = __shfl_sync(ALL, r.m_tiles, l);
-        const long long start = l ? at + __shfl_sync(ALL, upto, l - 1) : (__shfl_sync(ALL, upto, 0), at);
+        const long long before = __shfl_sync(ALL, upto, max(l - 1, 0)), start = at + (l ? before : 0);
         const int size = q.tiles + EXTRA;
-        const long long off = u - start, index = off / size;
-        const int j0 = (int)(off - index * size);
-        const long long first = u - j0;             // the item's first unit
-        const int j1 = (int)min((long long)size, end - first);
-        const int t0 = min(j0, q.tiles), t1 = min(j1, q.tiles);
-        if (q.tiles ? t0 < t1 : j0 == 0) {
+        const long long index = quotient(u - start, size), first = start + index * size;   // the item, its first unit
+        const int t0 = min((int)(u - first), q.tiles), t1 = (int)min((long long)q.tiles, end - first);
+        if (q.tiles ? t0 < t1 : u == first) {
           if (!wait(&C.item_empty[k % ITEMS], ((k / ITEMS) & 1) ^ 1)) break;
           if (lane == 0) {
             Item it;
@@ -406,22 +428,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             it.n = q.n;
             it.older = q.older;
             it.len = q.len;
-            it.g = (int)(index / q.m_tiles);
-            it.m0 = (int)(index % q.m_tiles) * M;
+            it.g = (int)quotient(index, q.m_tiles);
+            it.m0 = (int)(index - (long long)it.g * q.m_tiles) * M;
             it.rows = (int)min((long long)M, (long long)q.n * A.group - it.m0);
             it.t0 = t0;
             it.t1 = t1;
-            it.part = t0 > 0 ? 0 : t1 < q.tiles ? 1 : -1;
-            it.pad = 0;
+            it.c0 = t0 == 0 ? cta : (int)quotient(first, share);
+            it.c1 = t1 == q.tiles ? cta : (int)quotient(first + q.tiles - 1, share);
             C.items[k % ITEMS] = it;
             C.odd[k % ITEMS] = 0;
-            if (it.part == 1) {
-              pt.lo = it.lo;
-              pt.g = it.g;
-              pt.m0 = it.m0;
-              pt.rows = it.rows;
-              pt.last = (int)((first + q.tiles - 1) / share);
-            }
             mbar_arrive(&C.item_full[k % ITEMS]);
           }
           ++k;
@@ -430,7 +445,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         u = first + size;
       }
     }
-    if (!dead && lane == 0) A.joins[cta] = pt;
     if (wait(&C.item_empty[k % ITEMS], ((k / ITEMS) & 1) ^ 1) && lane == 0) {
       C.items[k % ITEMS].b = -1;
       mbar_arrive(&C.item_full[k % ITEMS]);
@@ -517,55 +531,49 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (n == 0) continue;
       ok = wait(&C.q_ready, items & 1);
       tc_fence_after();
-      auto stage = [&](int i, uint32_t* addr, uint64_t** release) {   // waits for it
+      auto landed = [&](int i) {                    // the item's stage i
         const int x = at + i;
-        if (S::E4M3) {
-          ok = ok && wait(&C.c_full[x % 4], (x / 4) & 1);
-          *addr = smem_u32(conv + x % 4 * S::TILE);
-          *release = &C.c_empty[x % 4];
-        } else {
-          ok = ok && wait(&C.full[x % S::NR], (x / S::NR) & 1);
-          *addr = smem_u32(ring + x % S::NR * S::RAW);
-          *release = &C.empty[x % S::NR];
-        }
+        return S::E4M3 ? wait(&c_full[x % 4], (x / 4) & 1) : wait(&C.full[x % S::NR], (x / S::NR) & 1);
+      };
+      auto place = [&](int i, uint64_t** release) {
+        const int x = at + i;
+        *release = S::E4M3 ? &c_empty[x % 4] : &C.empty[x % S::NR];
+        return smem_u32(S::E4M3 ? conv + x % 4 * S::TILE : ring + x % S::NR * S::RAW);
       };
       auto scores = [&](int j) {                    // S = Q K^T of the item's tile j
-        uint32_t addr;
         uint64_t* release;
-        stage(key_at(j), &addr, &release);
-        if (!ok) return;
+        const uint64_t d = desc_sw128(place(key_at(j), &release), 0, S::GROUP);
         const int left = it.len - (it.t0 + j) * S::TN;
         const int cols = left < S::TN ? (left + 15) & ~15 : S::TN;
         const uint32_t id = idesc(S::BF16, false, cols), s = tmem + S::S0 + (uint32_t)((tiles + j) & 1) * S::TN;
-        const uint64_t d = desc_sw128(addr, 0, S::GROUP);
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < S::D / 16; ++x)
             umma_f16_ts(s, tmem + S::Q + x * 8, d + (x / 4) * 64 + (x % 4) * 2, id, x > 0);
-          umma_commit(release);
           umma_commit(&C.s_full[(tiles + j) & 1]);
+          umma_commit(release);
           if (j == n - 1) umma_commit(&C.q_free);
         }
         __syncwarp();
       };
-      if (ok) scores(0);
+      for (int j = 0; j < 2 && j < n && ok; ++j) {
+        ok = landed(key_at(j));
+        if (ok) scores(j);
+      }
       for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) scores(j + 1);
         const int g = tiles + j, left = it.len - (it.t0 + j) * S::TN;
-        ok = ok && wait(&C.p_ready[g & 1], (g >> 1) & 1);
-        if (j == 0) ok = ok && wait(&C.o_free, (items & 1) ^ 1);
         if (!S::E4M3 && (int64_t)(it.t0 + j + 1) * S::TN > it.older) {
-          ok = ok && wait(&C.fixed[fixes % 8], (fixes / 8) & 1);
+          ok = wait(&C.fixed[fixes % 8], (fixes / 8) & 1);
           ++fixes;
         }
-        uint32_t addr;
-        uint64_t* release;
-        stage(value_at(j, n), &addr, &release);
+        ok = ok && landed(value_at(j, n)) && (j + 2 >= n || landed(key_at(j + 2))) &&
+             (j > 0 || wait(&C.o_free, (items & 1) ^ 1)) && wait(&C.p_ready[g & 1], (g >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
+        uint64_t* release;
+        const uint64_t d = desc_sw128(place(value_at(j, n), &release), 1024, S::GROUP);
         const int steps = left < S::TN ? (left + 15) >> 4 : S::TN / 16;
         const uint32_t id = idesc(S::PBF16, true, S::D), p = tmem + S::S0 + (uint32_t)(g & 1) * S::TN;
-        const uint64_t d = desc_sw128(addr, 1024, S::GROUP);
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < S::TN / 16; ++x)
@@ -575,6 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (j == n - 1) umma_commit(&C.o_full);
         }
         __syncwarp();
+        if (j + 2 < n) scores(j + 2);
       }
       at += 2 * n;
       tiles += n;
@@ -596,26 +605,32 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool turn = A.scale * (S::E4M3 ? __ldcg(a.k_scale + it.g) : 1.f) < 0.f;
         const int m = it.m0 + t, i = m / A.group;
         const uint4* q = reinterpret_cast<const uint4*>(rows_at(a.q, it.lo + i, it.g * A.group + m - i * A.group));
-        uint32_t r[S::D / 2];
+        constexpr int C0 = S::D / 2 < 64 ? S::D / 2 : 64;              // columns at a time
 #pragma unroll
-        for (int x = 0; x < S::D / 8; ++x) {
-          const uint4 v = t < it.rows ? __ldcg(q + x) : make_uint4(0, 0, 0, 0);
-          r[4 * x] = v.x;
-          r[4 * x + 1] = v.y;
-          r[4 * x + 2] = v.z;
-          r[4 * x + 3] = v.w;
-        }
-        if (turn)
+        for (int c = 0; c < S::D / 2; c += C0) {
+          uint32_t r[C0];
 #pragma unroll
-          for (int x = 0; x < S::D / 2; ++x) r[x] ^= 0x80008000u;
-        ok = wait(&C.q_free, (items & 1) ^ 1);
-        tc_fence_after();
+          for (int x = 0; x < C0 / 4; ++x) {
+            const uint4 v = t < it.rows ? __ldcg(q + c / 4 + x) : make_uint4(0, 0, 0, 0);
+            r[4 * x] = v.x;
+            r[4 * x + 1] = v.y;
+            r[4 * x + 2] = v.z;
+            r[4 * x + 3] = v.w;
+          }
+          if (turn)
 #pragma unroll
-        for (int x = 0; x < S::D / 32; ++x) {
-          uint32_t c[16];
+            for (int x = 0; x < C0; ++x) r[x] ^= 0x80008000u;
+          if (c == 0) {
+            ok = wait(&C.q_free, (items & 1) ^ 1);
+            tc_fence_after();
+          }
 #pragma unroll
-          for (int y = 0; y < 16; ++y) c[y] = r[16 * x + y];
-          tmem_st16(tmem + ((uint32_t)(wq * 32) << 16) + S::Q + 16 * x, c);
+          for (int x = 0; x < C0; x += 16) {
+            uint32_t v[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) v[y] = r[x + y];
+            tmem_st16(tmem + ((uint32_t)(wq * 32) << 16) + S::Q + c + x, v);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -630,7 +645,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const bool key = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
           const int j = x == 0 ? 0 : x == 2 * n - 1 ? n - 1 : key ? (x + 1) / 2 : x / 2 - 1;
           const int st = (at + x) % S::NR, cv = (at + x) % 4;
-          ok = ok && wait(&C.full[st], ((at + x) / S::NR) & 1) && wait(&C.c_empty[cv], (((at + x) / 4) & 1) ^ 1);
+          ok = ok && wait(&C.full[st], ((at + x) / S::NR) & 1) && wait(&c_empty[cv], (((at + x) / 4) & 1) ^ 1);
           if (!ok) break;
           const uint8_t* from = ring + st * S::RAW;
           uint8_t* to = conv + cv * S::TILE;
@@ -667,7 +682,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&C.empty[st]);
-            mbar_arrive(&C.c_full[cv]);
+            mbar_arrive(&c_full[cv]);
           }
         }
       } else {
@@ -708,14 +723,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       done_item(k);
     }
   } else if (warp >= W_SOFT) {
-    const int wq = warp - W_SOFT, t = threadIdx.x - W_SOFT * 32;
+    // two threads to a row: the first four warps take the first half of a tile's tokens and of the output's elements
+    constexpr int H = S::TN / 2, HD = S::D / 2;
+    const int wq = warp & 3, half = (warp - W_SOFT) >> 2, t = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-    int tiles = 0, items = 0;
+    int tiles = 0, items = 0, syncs = 0;
     bool ok = true;
     Item it;
+    auto all_arrive = [&] {                         // a barrier of the softmax's warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C.soft);
+      return wait(&C.soft, syncs++ & 1);
+    };
     for (int k = 0; ok && next_item(k, it); ++k) {
       const int n = it.t1 - it.t0, m = it.m0 + t, i = m / A.group, h = it.g * A.group + m - i * A.group;
       const bool row = t < it.rows;
+      const uint16_t* gate = a.gate.p && row ? rows_at(a.gate, it.lo + i, h) + half * HD : nullptr;
+      if (gate)
+#pragma unroll
+        for (int x = 0; x < HD; x += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(gate + x));
       Mask mask;
       mask.load(A, it.lo + i, i, it.len - it.older, row && n);
       float c = fabsf(A.scale * (S::E4M3 ? __ldcg(a.k_scale + it.g) : 1.f));
@@ -728,41 +754,54 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t s = lanes + S::S0 + (uint32_t)(tiles & 1) * S::TN;
         const int rel = (it.t0 + j) * S::TN - it.older;
         const bool edge = rel + S::TN > 0;
-        float top = -INFINITY;
-        uint32_t r[32];
+        uint32_t r[H / 32][32];
 #pragma unroll
-        for (int x = 0; x < S::TN; x += 32) {
-          tmem_ld32(s + x, r);
-          tmem_wait_ld32(r);
-          if (edge) {
-            const uint32_t w = mask.window(rel + x);
+        for (int x = 0; x < H / 32; ++x) tmem_ld32(s + half * H + 32 * x, r[x]);
+#pragma unroll
+        for (int x = 0; x < H / 32; ++x) tmem_wait_ld32(r[x]);
+        if (edge)
+#pragma unroll
+          for (int x = 0; x < H / 32; ++x) {
+            const uint32_t w = mask.window(rel + half * H + 32 * x);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-              if (w >> y & 1) top = fmaxf(top, __uint_as_float(r[y]));
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; ++y) top = fmaxf(top, __uint_as_float(r[y]));
+              if (!(w >> y & 1)) r[x][y] = 0xFF800000u;
           }
-        }
-        top *= c;
+        float top[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) top[y] = __uint_as_float(r[0][y]);
+#pragma unroll
+        for (int x = 0; x < H / 32; ++x)
+#pragma unroll
+          for (int y = 0; y < 32; ++y) top[y & 3] = fmaxf(top[y & 3], __uint_as_float(r[x][y]));
+        top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // the row's other half
+        float* tops = C.top[tiles & 1][0];
+        tops[half * M + t] = top[0];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&C.pair[wq][tiles & 1]);
+        ok = wait(&C.pair[wq][tiles & 1], (tiles >> 1) & 1);
+        if (!ok) break;
+        const float high = fmaxf(top[0], tops[(half ^ 1) * M + t]) * c;
         // the base follows
-        const bool up = top > ref + S::TAU || (ref == -INFINITY && top > ref);
+        const bool up = high > ref + S::TAU;
         if (__any_sync(ALL, up)) {
-          const float f = up ? exp2_fast(ref - top) : 1.f;
-          if (up) ref = top;
+          const float f = up ? exp2_fast(ref - high) : 1.f;
+          if (up) ref = high;
           l *= f;
           if (j > 0) {                              // the product of the tile before; the one before that is done
             ok = wait(&C.pv_done, (tiles - 1) & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < S::D; x += 32) {
+            for (int x = half * HD; x < half * HD + HD; x += 32) {
+              uint32_t o[32];
               __syncwarp();
-              tmem_ld32(lanes + S::O + x, r);
-              tmem_wait_ld32(r);
+              tmem_ld32(lanes + S::O + x, o);
+              tmem_wait_ld32(o);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * f);
-              tmem_st32(lanes + S::O + x, r);
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st32(lanes + S::O + x, o);
             }
           }
         }
@@ -770,24 +809,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         float sum0 = 0.f, sum1 = 0.f;
         __syncwarp();
 #pragma unroll
-        for (int x = 0; x < S::TN; x += 32) {
-          tmem_ld32(s + x, r);
-          tmem_wait_ld32(r);
-          const uint32_t w = edge ? mask.window(rel + x) : ALL;
+        for (int x = 0; x < H / 32; ++x) {
           uint32_t p[16];
 #pragma unroll
           for (int y = 0; y < 32; y += 2) {
-            float e0 = exp2_fast(fmaf(__uint_as_float(r[y]), c, -base));
-            float e1 = exp2_fast(fmaf(__uint_as_float(r[y + 1]), c, -base));
-            if (edge) {
-              e0 = w >> y & 1 ? e0 : 0.f;
-              e1 = w >> (y + 1) & 1 ? e1 : 0.f;
-            }
+            const float e0 = exp2_fast(fmaf(__uint_as_float(r[x][y]), c, -base));
+            const float e1 = exp2_fast(fmaf(__uint_as_float(r[x][y + 1]), c, -base));
             sum0 += e0;
             sum1 += e1;
             p[y / 2] = pack2<S::PBF16>(e0, e1);
           }
-          tmem_st16(s + x / 2, p);
+          tmem_st16(s + half * (H / 2) + 16 * x, p);
         }
         l += sum0 + sum1;
         tmem_wait_st();
@@ -796,185 +828,172 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&C.p_ready[tiles & 1]);
       }
       if (!ok) break;
-      // what the item's rows get
+      // the row's sum, and what the item's rows get
+      float* sums = C.top[tiles & 1][0];            // read last two tiles ago
+      sums[half * M + t] = l;
+      ok = all_arrive();
+      if (!ok) break;
+      l = sums[t] + sums[M + t];
+      ok = all_arrive();
+      if (!ok) break;
       if (n) {
         ok = wait(&C.o_full, items++ & 1);
         if (!ok) break;
         tc_fence_after();
       }
-      const bool patch = n && *(volatile int*)&C.odd[k % ITEMS];
+      const bool patch = n && *(volatile int*)&C.odd[k % ITEMS], whole = it.c0 == it.c1;
       const float vs = S::E4M3 ? __ldcg(a.v_scale + it.g) : 1.f;
-      const float by = l == 0.f ? 0.f : vs / l;
-      float* part = A.parts + (size_t)(cta * 2 + (it.part > 0)) * S::PART;
-      const int ps = 1 << A.page_log2;
-#pragma unroll 1
-      for (int x = 0; x < S::D; x += 32) {
-        float y[32];
-        if (n) {
-          uint32_t r[32];
-          __syncwarp();
-          tmem_ld32(lanes + S::O + x, r);
-          tmem_wait_ld32(r);
+      float* part = A.parts + (size_t)(cta * 2 + (cta == it.c0)) * S::PART;
+      uint16_t* out = rows_at(a.out, it.lo + i, h) + half * HD;
+      auto finish = [&](float (&y)[8], int x, float l) {               // 8 elements of the output from x on
+        const float by = vs / l;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(r[e]);
-        } else {
+        for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : y[e] * by;
+        if (gate) {
+          const uint4 v = __ldcg(reinterpret_cast<const uint4*>(gate + x));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = 0.f;
-        }
-        if (patch) {
-          const int from = max(it.older, it.t0 * S::TN), upto = (int)min((int64_t)it.len, (int64_t)it.t1 * S::TN);
-          for (int p = from; p < upto; ++p) {
-            const int j = p - it.older;
-            if (!(mask.word(j >> 5) >> (j & 31) & 1)) continue;
-            const int page = __ldcg(a.tables + (size_t)it.b * a.table_stride + (p >> A.page_log2));
-            if (page < 0 || page >= A.n_pages) continue;
-            const int64_t at = page * a.v_page_stride + ((int64_t)it.g * ps + (p & (ps - 1))) * S::D + x;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float v;
-              if (S::E4M3) {
-                uint32_t lo, hi;
-                e4m3x4_to_f16x4(__ldcg((const uint8_t*)a.v_cache + at + e), lo, hi);
-                v = unpack2<false>(lo).x;
-              } else {
-                v = unpack2<S::BF16>(__ldcg((const unsigned short*)a.v_cache + at + e)).x;
-              }
-              y[e] += odd<S::BF16>(v);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float2 g = unpack2<S::BF16>(w[e]);
+            y[2 * e] = gated(y[2 * e], g.x);
+            y[2 * e + 1] = gated(y[2 * e + 1], g.y);
           }
         }
-        if (it.part >= 0) {                         // [D / 4][rows] of four elements
-          if (row)
+        *reinterpret_cast<uint4*>(out + x) = make_uint4(pack2<S::BF16>(y[0], y[1]), pack2<S::BF16>(y[2], y[3]),
+                                                        pack2<S::BF16>(y[4], y[5]), pack2<S::BF16>(y[6], y[7]));
+      };
+#pragma unroll 1
+      for (int x = 0; x < HD; x += 32) {
+        uint32_t r[32];
+        __syncwarp();
+        if (n) {
+          tmem_ld32(lanes + S::O + half * HD + x, r);
+          tmem_wait_ld32(r);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              __stcg(reinterpret_cast<float4*>(part) + (x + e) / 4 * M + t, make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]));
-          continue;
+          for (int e = 0; e < 32; ++e) r[e] = 0;
         }
-        if (!row) continue;
+        if (patch) {                                // on copies: what is passed by address leaves the registers
+          const Mask seen = mask;
+          uint32_t o[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = l == 0.f ? 0.f : y[e] * by;
-        if (a.gate.p) gate32<S::BF16>(y, rows_at(a.gate, it.lo + i, h) + x);
-        uint4* out = reinterpret_cast<uint4*>(rows_at(a.out, it.lo + i, h) + x);
+          for (int e = 0; e < 32; ++e) o[e] = r[e];
+          add_odd<S>(A, it, seen, half * HD + x, o);
 #pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          out[e / 8] = make_uint4(pack2<S::BF16>(y[e], y[e + 1]), pack2<S::BF16>(y[e + 2], y[e + 3]),
-                                  pack2<S::BF16>(y[e + 4], y[e + 5]), pack2<S::BF16>(y[e + 6], y[e + 7]));
-      }
-      if (it.part >= 0 && row) {
-        __stcg(part + M * S::D + t, ref);
-        __stcg(part + M * S::D + M + t, l);
+          for (int e = 0; e < 32; ++e) r[e] = o[e];
+        }
+        if (row)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float y[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(r[e + z]);
+            if (whole) {
+              finish(y, x + e, l);
+            } else {                                // [D / 4][rows] of four elements
+              float4* to = reinterpret_cast<float4*>(part) + (half * HD + x + e) / 4 * M + t;
+              __stcg(to, make_float4(y[0], y[1], y[2], y[3]));
+              __stcg(to + M, make_float4(y[4], y[5], y[6], y[7]));
+            }
+          }
       }
       if (n) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&C.o_free);
       }
+      if (!whole) {
+        // Whoever counts itself last joins: the parts of its group, and then the groups.
+        if (row && half == 0) {
+          __stcg(part + M * S::D + t, ref);
+          __stcg(part + M * S::D + M + t, l);
+        }
+        const int parts = it.c1 - it.c0 + 1, step = parts > FLAT ? GROUP_OF : 1;
+        auto part_at = [&](int p) { return A.parts + (size_t)((it.c0 + p) * 2 + (p == 0)) * S::PART; };
+        auto last_of = [&](uint32_t* count, int of, bool* last) {
+          __threadfence();
+          if (!all_arrive()) return false;
+          if (warp == W_SOFT && lane == 0) {
+            const bool is = atomicAdd(count, 1u) == (uint32_t)of - 1;
+            if (is) *count = 0;
+            __threadfence();
+            C.last = is;
+          }
+          if (!all_arrive()) return false;
+          *last = C.last;
+          __threadfence();
+          return true;
+        };
+        // parts p0, p0 + by .. below p1 of this thread's row, 8 elements at a time: f(elements, x, base, sum)
+        auto join = [&](int p0, int p1, int by, auto f) {
+          float top = -INFINITY, sum = 0.f;
+          for (int p = p0; p < p1; p += by) top = fmaxf(top, __ldcg(part_at(p) + M * S::D + t));
+          auto factor = [&](int p) {                // no base and a sum of NaN: all scores were NaN
+            const float* q = part_at(p) + M * S::D + t;
+            const float pm = __ldcg(q), pl = __ldcg(q + M);
+            return pm == -INFINITY ? (pl == pl ? 0.f : pl) : exp2_fast(pm - top);
+          };
+          for (int p = p0; p < p1; p += by) sum += factor(p) * __ldcg(part_at(p) + M * S::D + M + t);
+#pragma unroll 1
+          for (int x = 0; x < HD; x += 16) {
+            float4 y[4] = {};
+#pragma unroll 4
+            for (int p = p0; p < p1; p += by) {
+              const float4* q = reinterpret_cast<const float4*>(part_at(p)) + (half * HD + x) / 4 * M + t;
+              const float w = factor(p);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 v = __ldcg(q + e * M);
+                y[e] = make_float4(y[e].x + v.x * w, y[e].y + v.y * w, y[e].z + v.z * w, y[e].w + v.w * w);
+              }
+            }
+            f(y, x, top, sum);
+          }
+        };
+        const int mine = cta - it.c0;
+        bool last = false;
+        int p0 = mine / GROUP_OF * GROUP_OF;
+        if (step > 1) {
+          const int p1 = min(parts, p0 + GROUP_OF);
+          ok = last_of(A.counts + 3 * (it.c0 + p0) + 1 + (p0 == 0), p1 - p0, &last);
+          if (!ok) break;
+          if (last) {
+            float top = 0.f, sum = 0.f;
+            if (row)
+              join(p0, p1, 1, [&](float4 (&y)[4], int x, float m, float l) {
+                float4* to = reinterpret_cast<float4*>(part_at(p0)) + (half * HD + x) / 4 * M + t;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) __stcg(to + e * M, y[e]);
+                top = m;
+                sum = l;
+              });
+            ok = all_arrive();                      // both halves have read the row's bases
+            if (!ok) break;
+            if (row && half == 0) {
+              __stcg(part_at(p0) + M * S::D + t, top);
+              __stcg(part_at(p0) + M * S::D + M + t, sum);
+            }
+          }
+        }
+        if (step == 1 || last) {
+          ok = last_of(A.counts + 3 * it.c0, (parts + step - 1) / step, &last);
+          if (!ok) break;
+          if (last && row)
+            join(0, parts, step, [&](float4 (&y)[4], int x, float m, float l) {
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                float v[8] = {y[e].x, y[e].y, y[e].z, y[e].w, y[e + 1].x, y[e + 1].y, y[e + 1].z, y[e + 1].w};
+                finish(v, x + 4 * e, l);
+              }
+            });
+        }
+        __syncwarp();
+      }
       done_item(k);
     }
   }
   __syncthreads();
   if (warp == W_MMA) tmem_dealloc(tmem, 512);
-}
-
-// ---- the parts of split items ----
-// A block to 32 rows and 16 elements of an item: its warps take the parts in turn.
-constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
-
-template <class S>
-__global__ void __launch_bounds__(JOIN_THREADS) k_join_tree(const __grid_constant__ TreeArgs A, int ctas) {
-  __shared__ float4 s_o[JOIN_WARPS][4][32];
-  __shared__ float s_m[JOIN_WARPS][32], s_l[JOIN_WARPS][32];
-  __shared__ int s_end[MAX_CTAS];
-  const moe_cache_attend_tree_t& a = A.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  follow_predecessor();
-  if (__ldcg(A.status) & CACHE_BAD_WAIT) return;
-  // blocks of work of each item, summed up
-  if (warp == 0) {
-    int sum = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const int c = c0 + lane;
-      int v = 0;
-      if (c < ctas && __ldcg(&A.joins[c].last)) v = (__ldcg(&A.joins[c].rows) + 31) / 32 * (S::D / 16);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (lane >= o) v += y;
-      }
-      if (c < ctas) s_end[c] = sum + v;
-      sum += __shfl_sync(0xFFFFFFFFu, v, 31);
-    }
-  }
-  __syncthreads();
-  const int total = s_end[ctas - 1];
-  for (int w = blockIdx.x; w < total; w += gridDim.x) {
-    int lo = 0, hi = ctas - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_end[mid] > w) hi = mid; else lo = mid + 1;
-    }
-    Part pt;
-    *reinterpret_cast<int4*>(&pt) = __ldcg(reinterpret_cast<const int4*>(A.joins + lo));
-    pt.last = __ldcg(&A.joins[lo].last);
-    const int k = w - (lo ? s_end[lo - 1] : 0), x = k % (S::D / 16) * 16, r = k / (S::D / 16) * 32 + lane;
-    const int parts = pt.last - lo + 1;
-    const bool row = r < pt.rows;
-    // each warp's parts on their own base
-    float m = -INFINITY, l = 0.f;
-    float4 o[4] = {};
-    auto part_at = [&](int p) { return A.parts + (size_t)((lo + p) * 2 + (p == 0)) * S::PART; };
-    if (row)
-      for (int p = warp; p < parts; p += JOIN_WARPS) {
-        const float* part = part_at(p);
-        const float pm = __ldcg(part + M * S::D + r), pl = __ldcg(part + M * S::D + M + r);
-        float4 v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(part) + (x / 4 + e) * M + r);
-        const float top = fmaxf(m, pm);
-        const float keep = m == -INFINITY ? 0.f : exp2_fast(m - top), add = pm == -INFINITY ? (pl == pl ? 0.f : pl) : exp2_fast(pm - top);
-        l = l * keep + pl * add;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[e].x = o[e].x * keep + v[e].x * add;
-          o[e].y = o[e].y * keep + v[e].y * add;
-          o[e].z = o[e].z * keep + v[e].z * add;
-          o[e].w = o[e].w * keep + v[e].w * add;
-        }
-        m = top;
-      }
-    s_m[warp][lane] = m;
-    s_l[warp][lane] = l;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s_o[warp][e][lane] = o[e];
-    __syncthreads();
-    // eight threads to a row, two elements each
-    const int rr = threadIdx.x >> 3, e = threadIdx.x & 7, rt = k / (S::D / 16) * 32 + rr;
-    if (rt < pt.rows) {
-      float top = -INFINITY, sum = 0.f, y0 = 0.f, y1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < JOIN_WARPS; ++i) top = fmaxf(top, s_m[i][rr]);
-#pragma unroll
-      for (int i = 0; i < JOIN_WARPS; ++i) {
-        if (i >= parts) break;
-        const float f = s_m[i][rr] == -INFINITY ? (s_l[i][rr] == s_l[i][rr] ? 0.f : s_l[i][rr]) : exp2_fast(s_m[i][rr] - top);
-        const float2 v = reinterpret_cast<const float2*>(&s_o[i][e >> 1][rr])[e & 1];
-        sum += s_l[i][rr] * f;
-        y0 += v.x * f;
-        y1 += v.y * f;
-      }
-      const float by = (S::E4M3 ? __ldcg(a.v_scale + pt.g) : 1.f) / sum;
-      y0 = sum == 0.f ? 0.f : y0 * by;
-      y1 = sum == 0.f ? 0.f : y1 * by;
-      const int mm = pt.m0 + rt, i = mm / A.group, h = pt.g * A.group + mm - i * A.group;
-      if (a.gate.p) {
-        const float2 g = unpack2<S::BF16>(__ldcg(reinterpret_cast<const uint32_t*>(rows_at(a.gate, pt.lo + i, h) + x + 2 * e)));
-        y0 = gated(y0, g.x);
-        y1 = gated(y1, g.y);
-      }
-      *reinterpret_cast<uint32_t*>(rows_at(a.out, pt.lo + i, h) + x + 2 * e) = pack2<S::BF16>(y0, y1);
-    }
-    __syncthreads();
-  }
 }
 
 // ---- launches ----
@@ -1036,21 +1055,21 @@ cudaError_t run(const CacheShape& c, const TreeArgs& A, int ctas, cudaStream_t s
     e = cudaFuncSetAttribute(k_attend_tree<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::DYN);
     if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  if (e == cudaSuccess) e = launch_following(k_attend_tree<S>, ctas, THREADS, S::DYN, st, A, km, vm);
-  if (e == cudaSuccess) e = launch_following(k_join_tree<S>, ctas * 4, JOIN_THREADS, 0, st, A, ctas);
-  return e;
+  if (e != cudaSuccess) return e;
+  return launch_following(k_attend_tree<S>, ctas, THREADS, S::DYN, st, A, km, vm);
 }
 template <int D>
 cudaError_t run_types(const CacheShape& c, const TreeArgs& A, int ctas, cudaStream_t st) {
   if (c.bf16) return c.e4m3 ? run<Shape<D, true, true>>(c, A, ctas, st) : run<Shape<D, true, false>>(c, A, ctas, st);
   return c.e4m3 ? run<Shape<D, false, true>>(c, A, ctas, st) : run<Shape<D, false, false>>(c, A, ctas, st);
 }
+static_assert(MAX_CTAS * 3 * 4 <= CACHE_TREE_COUNTS, "all counts");
 int ctas_of(int num_sms) { return num_sms < MAX_CTAS ? num_sms : MAX_CTAS; }
 
 }  // namespace
 
 size_t cache_attend_tree_workspace(int num_sms, int head_dim) {
-  return (size_t)ctas_of(num_sms) * (sizeof(Part) + 2 * (size_t)(M * head_dim + 2 * M) * 4);
+  return CACHE_TREE_COUNTS + (size_t)ctas_of(num_sms) * 2 * (size_t)(M * head_dim + 2 * M) * 4;
 }
 
 cudaError_t cache_attend_tree_launch(const CacheShape& S, const moe_cache_attend_tree_t& a, const CacheTreeState& w,
@@ -1067,8 +1086,8 @@ cudaError_t cache_attend_tree_launch(const CacheShape& S, const moe_cache_attend
   A.max_len = (long long)S.max_pages << S.page_log2;
   A.scale = (float)a.scale * LOG2E;
   const int ctas = ctas_of(w.num_sms);
-  A.joins = (Part*)w.workspace;
-  A.parts = (float*)(A.joins + ctas);
+  A.counts = (uint32_t*)w.workspace;
+  A.parts = (float*)((uint8_t*)w.workspace + CACHE_TREE_COUNTS);
   A.status = w.status;
   A.timeout_ns = w.timeout_ns;
   A.skip_copy = w.skip_copy;
