@@ -224,31 +224,267 @@ __device__ __forceinline__ void codes4(uint32_t v, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-// what was taken out of the values of new tokens, for the rows that see them: 32 elements from x on
+// What was taken out of the values of new tokens is added to the rows that see it: HD elements of O from x on, at `o`.
 template <class S>
-__device__ __noinline__ void add_odd(const TreeArgs& A, const Item it, const Mask& mask, int x, uint32_t (&r)[32]) {
+__device__ __noinline__ void add_odd(const TreeArgs& A, const Item it, const Mask mask, int x, uint32_t o) {
   const moe_cache_attend_tree_t& a = A.a;
   const int ps = 1 << A.page_log2;
   const int from = max(it.older, it.t0 * S::TN), upto = (int)min((int64_t)it.len, (int64_t)it.t1 * S::TN);
-  for (int p = from; p < upto; ++p) {
-    const int j = p - it.older;
-    if (!(mask.word(j >> 5) >> (j & 31) & 1)) continue;
-    const int page = __ldcg(a.tables + (size_t)it.b * a.table_stride + (p >> A.page_log2));
-    if (page < 0 || page >= A.n_pages) continue;
-    const int64_t at = page * a.v_page_stride + ((int64_t)it.g * ps + (p & (ps - 1))) * S::D + x;
+  for (int c = 0; c < S::D / 2; c += 16) {
+    uint32_t r[16];
+    __syncwarp();
+    tmem_ld16_nowait(o + c, r);
+    tmem_wait_ld(r);
+    for (int p = from; p < upto; ++p) {
+      const int j = p - it.older, page = __ldcg(a.tables + (size_t)it.b * a.table_stride + (p >> A.page_log2));
+      if (page < 0 || page >= A.n_pages || !(mask.word(j >> 5) >> (j & 31) & 1)) continue;
+      const int64_t at = page * a.v_page_stride + ((int64_t)it.g * ps + (p & (ps - 1))) * S::D + x + c;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      float v;
-      if (S::E4M3) {
-        uint32_t lo, hi;
-        e4m3x4_to_f16x4(__ldcg((const uint8_t*)a.v_cache + at + e), lo, hi);
-        v = unpack2<false>(lo).x;
-      } else {
-        v = unpack2<S::BF16>(__ldcg((const unsigned short*)a.v_cache + at + e)).x;
+      for (int e = 0; e < 16; ++e) {
+        float v;
+        if (S::E4M3) {
+          uint32_t lo, hi;
+          e4m3x4_to_f16x4(__ldcg((const uint8_t*)a.v_cache + at + e), lo, hi);
+          v = unpack2<false>(lo).x;
+        } else {
+          v = unpack2<S::BF16>(__ldcg((const unsigned short*)a.v_cache + at + e)).x;
+        }
+        if (!(fabsf(v) <= 3.4028234663852886e38f)) r[e] = __float_as_uint(__uint_as_float(r[e]) + v);
       }
-      if (!(fabsf(v) <= 3.4028234663852886e38f)) r[e] = __float_as_uint(__uint_as_float(r[e]) + v);
+    }
+    __syncwarp();
+    tmem_st16(o + c, r);
+  }
+  tmem_wait_st();
+}
+
+// The sum of parts p0, p0 + by .. below p1 of a row, on their highest base; part `skip` is the thread's own, with a base
+// and a sum of its own. Loads of several parts are on their way at once.
+template <class S>
+struct Sum {
+  float m, l, own;           // base, sum, factor of the own part
+  __device__ __forceinline__ static float factor(float pm, float pl, float m) {
+    return pm == -INFINITY ? (pl == pl ? 0.f : pl) : exp2_fast(pm - m);   // no base and a sum of NaN: all scores NaN
+  }
+  template <class F>
+  __device__ __forceinline__ void bases(F at, int p0, int p1, int by, int skip, float om, float ol, bool row) {
+    m = skip >= 0 ? om : -INFINITY;
+#pragma unroll 8
+    for (int p = p0; p < p1; p += by)
+      if (p != skip && row) m = fmaxf(m, __ldcg(at(p)));
+    own = skip >= 0 ? factor(om, ol, m) : 0.f;
+    l = 0.f;
+#pragma unroll 4
+    for (int p = p0; p < p1; p += by) {
+      float pm = om, pl = ol;
+      if (p != skip && row) {
+        pm = __ldcg(at(p));
+        pl = __ldcg(at(p) + M);
+      }
+      l = fmaf(pl, factor(pm, pl, m), l);
     }
   }
+  // 32 elements, at at(p) in the workspace, or of the thread's own part at `o` in tensor memory. In the order of the
+  // parts, and in fused steps, so that it does not matter which of them is the thread's own. By whole warps.
+  template <class F, class G>
+  __device__ __forceinline__ void add(float (&y)[32], F at, G base, int p0, int p1, int by, int skip, uint32_t o,
+                                      bool row) const {
+#pragma unroll 1
+    for (int p = p0; p < p1; p += by) {
+      uint32_t v[32];
+      float f = own;
+      if (p == skip) {
+        __syncwarp();
+        tmem_ld32(o, v);
+        tmem_wait_ld32(v);
+      } else if (row) {
+        const float4* q = reinterpret_cast<const float4*>(at(p));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 w = __ldcg(q + e * M);
+          v[4 * e] = __float_as_uint(w.x);
+          v[4 * e + 1] = __float_as_uint(w.y);
+          v[4 * e + 2] = __float_as_uint(w.z);
+          v[4 * e + 3] = __float_as_uint(w.w);
+        }
+        f = factor(__ldcg(base(p)), __ldcg(base(p) + M), m);
+      }
+      if (row)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = fmaf(__uint_as_float(v[e]), f, y[e]);
+    }
+  }
+};
+
+// 32 elements of the gate, loaded before what they multiply is there, and the output's
+template <class S>
+struct Gate {
+  uint4 v[4];
+  bool some;
+  __device__ __forceinline__ Gate(const uint16_t* at, int x) : some(at != nullptr) {
+    if (some)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __ldcg(reinterpret_cast<const uint4*>(at + x) + e);
+  }
+  // out: y vs / l, 0 where l is, times the gate
+  __device__ __forceinline__ void finish(const float (&y)[32], float l, float vs, uint16_t* out) const {
+    const float by = l == 0.f ? 0.f : __fdividef(vs, l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+      uint32_t z[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float a = l == 0.f ? 0.f : y[8 * e + 2 * x] * by, b = l == 0.f ? 0.f : y[8 * e + 2 * x + 1] * by;
+        if (some) {
+          const float2 g = unpack2<S::BF16>(w[x]);
+          a = gated(a, g.x);
+          b = gated(b, g.y);
+        }
+        z[x] = pack2<S::BF16>(a, b);
+      }
+      reinterpret_cast<uint4*>(out)[e] = make_uint4(z[0], z[1], z[2], z[3]);
+    }
+  }
+};
+
+// By whole warps, and in line: a call would spill what is live. A wait that runs out ends the CTA's work: everyone gives up at the next wait.
+__device__ __forceinline__ bool wait_for(const TreeArgs& A, Control& C, uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer();
+  do {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+  } while (__any_sync(0xFFFFFFFFu, globaltimer() - t0 <= A.timeout_ns));
+  if (!*(volatile int*)&C.abort) {
+    *(volatile int*)&C.abort = 1;
+    atomicOr(A.status, CACHE_BAD_WAIT);
+  }
+  return false;
+}
+// a barrier of the softmax's warps; n counts them
+__device__ __forceinline__ bool soft_barrier(const TreeArgs& A, Control& C, int& n) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&C.soft);
+  return wait_for(A, C, &C.soft, n++ & 1);
+}
+
+// What an item's rows get, from their O in tensor memory and the parts of other CTAs; called by the softmax's warps.
+// False: a wait ran out.
+template <class S>
+__device__ __forceinline__ bool finish_item(const TreeArgs& A, Control& C, const Item& it, const Mask& mask, int cta, int k,
+                                         uint32_t lanes, float ref, float l, int& syncs) {
+  constexpr int HD = S::D / 2;
+  const moe_cache_attend_tree_t& a = A.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = (warp - W_SOFT) >> 2, t = (warp & 3) * 32 + lane;
+  const int n = it.t1 - it.t0, m = it.m0 + t, i = m / A.group, h = it.g * A.group + m - i * A.group;
+  const bool row = t < it.rows;
+  const uint16_t* gate = a.gate.p && row ? rows_at(a.gate, it.lo + i, h) + half * HD : nullptr;
+  bool ok = true;
+  auto all_arrive = [&] { return soft_barrier(A, C, syncs); };
+  if (n && *(volatile int*)&C.odd[k % ITEMS]) add_odd<S>(A, it, mask, half * HD, lanes + S::O + half * HD);
+  const float vs = S::E4M3 ? __ldcg(a.v_scale + it.g) : 1.f;
+  const int parts = it.c1 - it.c0 + 1, step = parts > FLAT ? GROUP_OF : 1;
+  uint16_t* out = rows_at(a.out, it.lo + i, h) + half * HD;
+  // whether this CTA's part is the last of a split item; false: a wait ran out
+  bool last = false;
+  auto share_last = [&](uint32_t* count, int of, bool arrive) {
+    __threadfence();
+    if (!all_arrive()) return false;
+    if (warp == W_SOFT && lane == 0) {
+      const uint32_t before = arrive ? atomicAdd(count, 1u) : ld_acquire_u32(count);
+      C.last = before == (uint32_t)of - 1;
+      if (C.last) *count = 0;
+      __threadfence();
+    }
+    if (!all_arrive()) return false;
+    last = C.last;
+    __threadfence();
+    return true;
+  };
+  auto part_at = [&](int p) { return A.parts + (size_t)((it.c0 + p) * 2 + (p == 0)) * S::PART; };
+  auto base_at = [&](int p) { return part_at(p) + M * S::D + t; };
+  auto values_at = [&](int p, int x) { return part_at(p) + (size_t)(half * HD + x) / 4 * M * 4 + 4 * t; };
+  auto free_o = [&] {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&C.o_free);
+  };
+  const int mine = cta - it.c0;
+  // all others have arrived already: this part does not leave the CTA
+  if (parts > 1 && step == 1) ok = share_last(A.counts + 3 * it.c0, parts, false);
+  if (!ok) return false;
+  if (parts > 1 && !last) {
+    float* part = part_at(mine);
+#pragma unroll 1
+    for (int x = 0; x < HD; x += 32) {          // [D / 4][rows] of four elements
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld32(lanes + S::O + half * HD + x, r);
+      tmem_wait_ld32(r);
+      if (row) {
+        float4* to = reinterpret_cast<float4*>(part) + (half * HD + x) / 4 * M + t;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          __stcg(to + e * M, make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                         __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])));
+      }
+    }
+    if (row && half == 0) {
+      __stcg(part + M * S::D + t, ref);
+      __stcg(part + M * S::D + M + t, l);
+    }
+    // Whoever counts itself last joins: where there are many parts those of its group, and then the groups.
+    const int p0 = mine / GROUP_OF * GROUP_OF, p1 = min(parts, p0 + GROUP_OF);
+    if (step == 1) {
+      ok = share_last(A.counts + 3 * it.c0, parts, true);
+    } else {
+      free_o();
+      ok = share_last(A.counts + 3 * (it.c0 + p0) + 1 + (p0 == 0), p1 - p0, true);
+      if (ok && last) {
+        float* to = part_at(p0);
+        Sum<S> sum;
+        sum.bases(base_at, p0, p1, 1, -1, 0.f, 0.f, row);
+#pragma unroll 1
+        for (int x = 0; x < HD; x += 32) {
+          float y[32] = {};
+          sum.add(y, [&](int p) { return values_at(p, x); }, base_at, p0, p1, 1, -1, 0, row);
+          if (row)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              __stcg(reinterpret_cast<float4*>(to) + ((half * HD + x) / 4 + e) * M + t,
+                     make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
+        }
+        if (!all_arrive()) return false;            // both halves have read the row's bases
+        if (row && half == 0) {
+          __stcg(to + M * S::D + t, sum.m);
+          __stcg(to + M * S::D + M + t, sum.l);
+        }
+        ok = share_last(A.counts + 3 * it.c0, (parts + step - 1) / step, true);
+      }
+    }
+    if (!ok) return false;
+    if (!last) {
+      if (step == 1) free_o();
+      return true;
+    }
+  }
+  // the whole item, or all of its parts: in order, the CTA's own from tensor memory where it is still there
+  const bool here = step == 1;
+  Sum<S> sum;
+  sum.m = ref;
+  sum.l = l;
+  sum.own = 1.f;
+  if (parts > 1) sum.bases(base_at, 0, parts, step, here ? mine : -1, ref, l, row);
+#pragma unroll 1
+  for (int x = 0; x < HD; x += 32) {
+    const Gate<S> gate_x(gate, x);
+    float y[32] = {};
+    if (n) sum.add(y, [&](int p) { return values_at(p, x); }, base_at, parts > 1 ? 0 : mine, parts > 1 ? parts : mine + 1, step,
+                   here ? mine : -1, lanes + S::O + half * HD + x, row);
+    if (row) gate_x.finish(y, sum.l, vs, out + x);
+  }
+  if (n && here) free_o();
+  return true;
 }
 
 template <class S>
@@ -332,17 +568,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = C.tmem;
-  const uint64_t limit = A.timeout_ns;
-  // By whole warps. A wait that runs out ends the CTA's work: everyone gives up at the next wait.
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (__all_sync(ALL, mbar_try_wait(bar, parity))) return true;
-    if (__all_sync(ALL, mbar_wait_slow(bar, parity, limit))) return true;
-    if (!*(volatile int*)&C.abort) {
-      *(volatile int*)&C.abort = 1;
-      atomicOr(A.status, CACHE_BAD_WAIT);
-    }
-    return false;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(A, C, bar, parity); };
   // the next item, from the ring of items; k counts them
   auto next_item = [&](int k, Item& it) {
     if (!wait(&C.item_full[k % ITEMS], (k / ITEMS) & 1)) return false;
@@ -450,7 +676,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_arrive(&C.item_full[k % ITEMS]);
     }
   } else if (warp == W_PRODUCE) {
-    const uint64_t policy = policy_evict_first();
+    const uint64_t once = policy_evict_first(), again = policy_evict_normal();
+    uint64_t policy = once;
     const int ps = 1 << A.page_log2;
     const int box = ps < S::TN ? ps : S::TN;        // tokens of a copy
     const uint32_t bytes = (uint32_t)box * S::D * (S::E4M3 ? 1 : 2);
@@ -459,6 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     Item it;
     for (int k = 0; ok && next_item(k, it); ++k) {
       done_item(k);
+      policy = it.n * A.group <= M ? once : again;  // other rows of the request read the same tiles
       const int n = it.t1 - it.t0, held = (int)(((long long)it.len + ps - 1) >> A.page_log2);
       const int32_t* row = a.tables + (size_t)it.b * a.table_stride;
       auto entries = [&](int chunk) {               // 32 of the request's pages
@@ -730,11 +958,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int tiles = 0, items = 0, syncs = 0;
     bool ok = true;
     Item it;
-    auto all_arrive = [&] {                         // a barrier of the softmax's warps
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&C.soft);
-      return wait(&C.soft, syncs++ & 1);
-    };
+    auto all_arrive = [&] { return soft_barrier(A, C, syncs); };
     for (int k = 0; ok && next_item(k, it); ++k) {
       const int n = it.t1 - it.t0, m = it.m0 + t, i = m / A.group, h = it.g * A.group + m - i * A.group;
       const bool row = t < it.rows;
@@ -841,154 +1065,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      const bool patch = n && *(volatile int*)&C.odd[k % ITEMS], whole = it.c0 == it.c1;
-      const float vs = S::E4M3 ? __ldcg(a.v_scale + it.g) : 1.f;
-      float* part = A.parts + (size_t)(cta * 2 + (cta == it.c0)) * S::PART;
-      uint16_t* out = rows_at(a.out, it.lo + i, h) + half * HD;
-      auto finish = [&](float (&y)[8], int x, float l) {               // 8 elements of the output from x on
-        const float by = vs / l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : y[e] * by;
-        if (gate) {
-          const uint4 v = __ldcg(reinterpret_cast<const uint4*>(gate + x));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 g = unpack2<S::BF16>(w[e]);
-            y[2 * e] = gated(y[2 * e], g.x);
-            y[2 * e + 1] = gated(y[2 * e + 1], g.y);
-          }
-        }
-        *reinterpret_cast<uint4*>(out + x) = make_uint4(pack2<S::BF16>(y[0], y[1]), pack2<S::BF16>(y[2], y[3]),
-                                                        pack2<S::BF16>(y[4], y[5]), pack2<S::BF16>(y[6], y[7]));
-      };
-#pragma unroll 1
-      for (int x = 0; x < HD; x += 32) {
-        uint32_t r[32];
-        __syncwarp();
-        if (n) {
-          tmem_ld32(lanes + S::O + half * HD + x, r);
-          tmem_wait_ld32(r);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = 0;
-        }
-        if (patch) {                                // on copies: what is passed by address leaves the registers
-          const Mask seen = mask;
-          uint32_t o[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = r[e];
-          add_odd<S>(A, it, seen, half * HD + x, o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = o[e];
-        }
-        if (row)
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float y[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(r[e + z]);
-            if (whole) {
-              finish(y, x + e, l);
-            } else {                                // [D / 4][rows] of four elements
-              float4* to = reinterpret_cast<float4*>(part) + (half * HD + x + e) / 4 * M + t;
-              __stcg(to, make_float4(y[0], y[1], y[2], y[3]));
-              __stcg(to + M, make_float4(y[4], y[5], y[6], y[7]));
-            }
-          }
-      }
-      if (n) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&C.o_free);
-      }
-      if (!whole) {
-        // Whoever counts itself last joins: the parts of its group, and then the groups.
-        if (row && half == 0) {
-          __stcg(part + M * S::D + t, ref);
-          __stcg(part + M * S::D + M + t, l);
-        }
-        const int parts = it.c1 - it.c0 + 1, step = parts > FLAT ? GROUP_OF : 1;
-        auto part_at = [&](int p) { return A.parts + (size_t)((it.c0 + p) * 2 + (p == 0)) * S::PART; };
-        auto last_of = [&](uint32_t* count, int of, bool* last) {
-          __threadfence();
-          if (!all_arrive()) return false;
-          if (warp == W_SOFT && lane == 0) {
-            const bool is = atomicAdd(count, 1u) == (uint32_t)of - 1;
-            if (is) *count = 0;
-            __threadfence();
-            C.last = is;
-          }
-          if (!all_arrive()) return false;
-          *last = C.last;
-          __threadfence();
-          return true;
-        };
-        // parts p0, p0 + by .. below p1 of this thread's row, 8 elements at a time: f(elements, x, base, sum)
-        auto join = [&](int p0, int p1, int by, auto f) {
-          float top = -INFINITY, sum = 0.f;
-          for (int p = p0; p < p1; p += by) top = fmaxf(top, __ldcg(part_at(p) + M * S::D + t));
-          auto factor = [&](int p) {                // no base and a sum of NaN: all scores were NaN
-            const float* q = part_at(p) + M * S::D + t;
-            const float pm = __ldcg(q), pl = __ldcg(q + M);
-            return pm == -INFINITY ? (pl == pl ? 0.f : pl) : exp2_fast(pm - top);
-          };
-          for (int p = p0; p < p1; p += by) sum += factor(p) * __ldcg(part_at(p) + M * S::D + M + t);
-#pragma unroll 1
-          for (int x = 0; x < HD; x += 16) {
-            float4 y[4] = {};
-#pragma unroll 4
-            for (int p = p0; p < p1; p += by) {
-              const float4* q = reinterpret_cast<const float4*>(part_at(p)) + (half * HD + x) / 4 * M + t;
-              const float w = factor(p);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 v = __ldcg(q + e * M);
-                y[e] = make_float4(y[e].x + v.x * w, y[e].y + v.y * w, y[e].z + v.z * w, y[e].w + v.w * w);
-              }
-            }
-            f(y, x, top, sum);
-          }
-        };
-        const int mine = cta - it.c0;
-        bool last = false;
-        int p0 = mine / GROUP_OF * GROUP_OF;
-        if (step > 1) {
-          const int p1 = min(parts, p0 + GROUP_OF);
-          ok = last_of(A.counts + 3 * (it.c0 + p0) + 1 + (p0 == 0), p1 - p0, &last);
-          if (!ok) break;
-          if (last) {
-            float top = 0.f, sum = 0.f;
-            if (row)
-              join(p0, p1, 1, [&](float4 (&y)[4], int x, float m, float l) {
-                float4* to = reinterpret_cast<float4*>(part_at(p0)) + (half * HD + x) / 4 * M + t;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) __stcg(to + e * M, y[e]);
-                top = m;
-                sum = l;
-              });
-            ok = all_arrive();                      // both halves have read the row's bases
-            if (!ok) break;
-            if (row && half == 0) {
-              __stcg(part_at(p0) + M * S::D + t, top);
-              __stcg(part_at(p0) + M * S::D + M + t, sum);
-            }
-          }
-        }
-        if (step == 1 || last) {
-          ok = last_of(A.counts + 3 * it.c0, (parts + step - 1) / step, &last);
-          if (!ok) break;
-          if (last && row)
-            join(0, parts, step, [&](float4 (&y)[4], int x, float m, float l) {
-#pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                float v[8] = {y[e].x, y[e].y, y[e].z, y[e].w, y[e + 1].x, y[e + 1].y, y[e + 1].z, y[e + 1].w};
-                finish(v, x + 4 * e, l);
-              }
-            });
-        }
-        __syncwarp();
-      }
+      ok = finish_item<S>(A, C, it, mask, cta, k, lanes, ref, l, syncs);
       done_item(k);
     }
   }
