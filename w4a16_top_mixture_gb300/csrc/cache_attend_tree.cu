@@ -49,15 +49,17 @@ struct TreeArgs {
 template <int D_, bool BF16_, bool E4M3_>
 struct Shape {
   static constexpr int D = D_;
-  static constexpr bool BF16 = BF16_, E4M3 = E4M3_, PBF16 = BF16_ && !E4M3_;   // e4m3 values are exact in fp16
+  static constexpr bool BF16 = BF16_, E4M3 = E4M3_, MBF16 = BF16_ && !E4M3_;   // e4m3 is exact in fp16: both products' type
   static constexpr int TN = D == 256 ? 64 : 128;
   static constexpr int BLOCKS = D / 64, GROUP = BLOCKS * 1024;                 // of 8 tokens
   static constexpr int TILE = TN / 8 * GROUP, RAW = E4M3 ? TN * D : TILE;
-  static constexpr int NC = E4M3 ? 4 : 0;                                      // converted tiles
-  static constexpr int NR0 = (SMEM - MISC - NC * TILE) / RAW, NR = NR0 > 12 ? 12 : NR0;
-  static constexpr int DYN = NC * TILE + NR * RAW + MISC;
+  static constexpr int NC = E4M3 ? 3 : 0;                                      // converted tiles
+  static constexpr int CTL = MISC + (E4M3 ? 2 * M * 4 : 0);
+  static constexpr int NR0 = (SMEM - CTL - NC * TILE) / RAW, NR = NR0 > 12 ? 12 : NR0;
+  static constexpr int DYN = NC * TILE + NR * RAW + CTL;
   static constexpr uint32_t O = 0, Q = D, S0 = D + D / 2;                      // columns of tensor memory
-  static constexpr float TAU = 8.f, LIFT = PBF16 ? 0.f : 7.f;                  // fp16: 2^15 at most
+  static constexpr float TAU = 8.f, LIFT = MBF16 ? 0.f : 7.f;                  // fp16: 2^15 at most
+  static constexpr int NC1 = NC ? NC : 1;
   static constexpr int PART = M * D + 2 * M;
   static_assert(S0 + 2 * TN <= 512 && DYN <= SMEM && NR >= 4, "fits");
 };
@@ -90,9 +92,22 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float gated(float y, float x) {       // y * sigmoid(x), see cache_attend.cu
-  const float e = __expf(-fabsf(x));
-  return __fdividef(x < 0.f ? y * e : y, 1.f + e);
+// y sigmoid(x), four at a time: e = exp(-|x|) <= 1 cannot overflow, and one reciprocal of the product of the four 1 + e,
+// at most 16, does for all. Of the special functions' rate five parts in four an element are left of two.
+__device__ __forceinline__ void gated4(float (&y)[4], float2 g0, float2 g1) {
+  const float x[4] = {g0.x, g0.y, g1.x, g1.y};
+  float d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float e = __expf(-fabsf(x[i]));
+    y[i] = x[i] < 0.f ? y[i] * e : y[i];
+    d[i] = 1.f + e;
+  }
+  const float a = d[0] * d[1], b = d[2] * d[3], r = __frcp_rn(a * b), ra = r * b, rb = r * a;
+  y[0] *= ra * d[1];
+  y[1] *= ra * d[0];
+  y[2] *= rb * d[3];
+  y[3] *= rb * d[2];
 }
 __device__ __forceinline__ void tma5(void* dst, const CUtensorMap* m, int group, int page, uint64_t* bar, uint64_t policy) {
   asm volatile(
@@ -213,17 +228,6 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
   return v;
 }
 
-// e4m3 codes to 16-bit pairs, four at a time
-template <bool BF16>
-__device__ __forceinline__ void codes4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  e4m3x4_to_f16x4(v, lo, hi);
-  if (BF16) {
-    const float2 a = unpack2<false>(lo), b = unpack2<false>(hi);
-    lo = pack2<true>(a.x, a.y);
-    hi = pack2<true>(b.x, b.y);
-  }
-}
-
 // What was taken out of the values of new tokens is added to the rows that see it: HD elements of O from x on, at `o`.
 template <class S>
 __device__ __noinline__ void add_odd(const TreeArgs& A, const Item it, const Mask mask, int x, uint32_t o) {
@@ -334,14 +338,13 @@ struct Gate {
       const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
       uint32_t z[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        float a = l == 0.f ? 0.f : y[8 * e + 2 * x] * by, b = l == 0.f ? 0.f : y[8 * e + 2 * x + 1] * by;
-        if (some) {
-          const float2 g = unpack2<S::BF16>(w[x]);
-          a = gated(a, g.x);
-          b = gated(b, g.y);
-        }
-        z[x] = pack2<S::BF16>(a, b);
+      for (int x = 0; x < 4; x += 2) {
+        float q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = l == 0.f ? 0.f : y[8 * e + 2 * x + i] * by;
+        if (some) gated4(q, unpack2<S::BF16>(w[x]), unpack2<S::BF16>(w[x + 1]));
+        z[x] = pack2<S::BF16>(q[0], q[1]);
+        z[x + 1] = pack2<S::BF16>(q[2], q[3]);
       }
       reinterpret_cast<uint4*>(out)[e] = make_uint4(z[0], z[1], z[2], z[3]);
     }
@@ -388,17 +391,18 @@ __device__ __forceinline__ bool finish_item(const TreeArgs& A, Control& C, const
   // whether this CTA's part is the last of a split item; false: a wait ran out
   bool last = false;
   auto share_last = [&](uint32_t* count, int of, bool arrive) {
-    __threadfence();
     if (!all_arrive()) return false;
-    if (warp == W_SOFT && lane == 0) {
+    if (warp == W_SOFT && lane == 0) {              // its fences stand for all, on this side of each barrier
+      if (arrive) __threadfence();
       const uint32_t before = arrive ? atomicAdd(count, 1u) : ld_acquire_u32(count);
       C.last = before == (uint32_t)of - 1;
-      if (C.last) *count = 0;
-      __threadfence();
+      if (C.last) {
+        __threadfence();
+        *count = 0;
+      }
     }
     if (!all_arrive()) return false;
     last = C.last;
-    __threadfence();
     return true;
   };
   auto part_at = [&](int p) { return A.parts + (size_t)((it.c0 + p) * 2 + (p == 0)) * S::PART; };
@@ -503,6 +507,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
   const unsigned ALL = 0xFFFFFFFFu;
   uint64_t *c_full = C.new_full, *c_empty = C.fixed;
+  // [2][M], items in turn: undoes what bf16 queries over an 8-bit cache were multiplied by
+  float* undo = reinterpret_cast<float*>(ring + S::NR * S::RAW + MISC);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 12; ++i) {
@@ -761,19 +767,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       auto landed = [&](int i) {                    // the item's stage i
         const int x = at + i;
-        return S::E4M3 ? wait(&c_full[x % 4], (x / 4) & 1) : wait(&C.full[x % S::NR], (x / S::NR) & 1);
+        return S::E4M3 ? wait(&c_full[x % S::NC1], (x / S::NC1) & 1) : wait(&C.full[x % S::NR], (x / S::NR) & 1);
       };
       auto place = [&](int i, uint64_t** release) {
         const int x = at + i;
-        *release = S::E4M3 ? &c_empty[x % 4] : &C.empty[x % S::NR];
-        return smem_u32(S::E4M3 ? conv + x % 4 * S::TILE : ring + x % S::NR * S::RAW);
+        *release = S::E4M3 ? &c_empty[x % S::NC1] : &C.empty[x % S::NR];
+        return smem_u32(S::E4M3 ? conv + x % S::NC1 * S::TILE : ring + x % S::NR * S::RAW);
       };
       auto scores = [&](int j) {                    // S = Q K^T of the item's tile j
         uint64_t* release;
         const uint64_t d = desc_sw128(place(key_at(j), &release), 0, S::GROUP);
         const int left = it.len - (it.t0 + j) * S::TN;
         const int cols = left < S::TN ? (left + 15) & ~15 : S::TN;
-        const uint32_t id = idesc(S::BF16, false, cols), s = tmem + S::S0 + (uint32_t)((tiles + j) & 1) * S::TN;
+        const uint32_t id = idesc(S::MBF16, false, cols), s = tmem + S::S0 + (uint32_t)((tiles + j) & 1) * S::TN;
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < S::D / 16; ++x)
@@ -801,7 +807,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint64_t* release;
         const uint64_t d = desc_sw128(place(value_at(j, n), &release), 1024, S::GROUP);
         const int steps = left < S::TN ? (left + 15) >> 4 : S::TN / 16;
-        const uint32_t id = idesc(S::PBF16, true, S::D), p = tmem + S::S0 + (uint32_t)(g & 1) * S::TN;
+        const uint32_t id = idesc(S::MBF16, true, S::D), p = tmem + S::S0 + (uint32_t)(g & 1) * S::TN;
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < S::TN / 16; ++x)
@@ -834,6 +840,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int m = it.m0 + t, i = m / A.group;
         const uint4* q = reinterpret_cast<const uint4*>(rows_at(a.q, it.lo + i, it.g * A.group + m - i * A.group));
         constexpr int C0 = S::D / 2 < 64 ? S::D / 2 : 64;              // columns at a time
+        // bf16 queries over an 8-bit cache, in fp16: times a power of two that brings the row's largest to 2^14 or above
+        float by = 1.f;
+        if (S::E4M3 && S::BF16) {
+          uint32_t big = 0;
+          if (t < it.rows)
+#pragma unroll 8
+            for (int x = 0; x < S::D / 8; ++x) {
+              const uint4 v = __ldcg(q + x);
+              big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+            }
+          big = max(big & 0xFFFFu, big >> 16);
+          // its exponent, 2^(e - 127): by 2^(141 - e), within fp32's normal range; infinities and NaN stay what they are
+          const int e = (int)(big >> 7), f = e == 255 ? 127 : min(253, 268 - e);
+          by = __uint_as_float((uint32_t)f << 23);
+        }
 #pragma unroll
         for (int c = 0; c < S::D / 2; c += C0) {
           uint32_t r[C0];
@@ -845,12 +867,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             r[4 * x + 2] = v.z;
             r[4 * x + 3] = v.w;
           }
+          if (S::E4M3 && S::BF16)
+#pragma unroll
+            for (int x = 0; x < C0; ++x) {
+              const float2 f = unpack2<true>(r[x]);
+              r[x] = pack2<false>(f.x * by, f.y * by);
+            }
           if (turn)
 #pragma unroll
             for (int x = 0; x < C0; ++x) r[x] ^= 0x80008000u;
           if (c == 0) {
             ok = wait(&C.q_free, (items & 1) ^ 1);
             tc_fence_after();
+            if (S::E4M3 && S::BF16) undo[(items & 1) * M + t] = __uint_as_float(0x7F000000u - __float_as_uint(by));
           }
 #pragma unroll
           for (int x = 0; x < C0; x += 16) {
@@ -872,38 +901,48 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int x = 0; x < 2 * n && ok; ++x) {
           const bool key = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
           const int j = x == 0 ? 0 : x == 2 * n - 1 ? n - 1 : key ? (x + 1) / 2 : x / 2 - 1;
-          const int st = (at + x) % S::NR, cv = (at + x) % 4;
-          ok = ok && wait(&C.full[st], ((at + x) / S::NR) & 1) && wait(&c_empty[cv], (((at + x) / 4) & 1) ^ 1);
+          const int st = (at + x) % S::NR, cv = (at + x) % S::NC1;
+          ok = ok && wait(&C.full[st], ((at + x) / S::NR) & 1) && wait(&c_empty[cv], (((at + x) / S::NC1) & 1) ^ 1);
           if (!ok) break;
-          const uint8_t* from = ring + st * S::RAW;
-          uint8_t* to = conv + cv * S::TILE;
+          // a thread's vectors lie 128 apart: the same 16 elements of rows a fixed number apart
+          constexpr int VR = S::D / 16, ROWS = 128 / VR, STEPS = S::TN / ROWS;
+          const int tok = t / VR, c = t % VR;
+          const uint8_t* from = ring + st * S::RAW + t * 16;
+          uint8_t* to = conv + cv * S::TILE + (tok >> 3) * S::GROUP + (c >> 2) * 1024 + (tok & 7) * 128;
+          // lanes of neighbouring blocks store their halves in other orders: other banks
+          const int turn = c >> 2 & 1, c0 = ((2 * (c & 3)) ^ (tok & 7)) ^ turn, c1 = c0 ^ 1;
           const int tok0 = (it.t0 + j) * S::TN, left = it.len - tok0, fresh = it.older - tok0;
-          const int rows = left < S::TN ? (left + 15) & ~15 : S::TN;
-          constexpr int VR = S::D / 16;             // vectors of a row
-#pragma unroll 4
-          for (int e = t; e < rows * VR; e += 128) {
-            const int tok = e / VR, c = e % VR;
-            uint4 v = *reinterpret_cast<const uint4*>(from + e * 16);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w}, o[8];
-            if (!key && tok >= fresh) {
+          const bool look = !key && fresh < S::TN;
+#pragma unroll
+          for (int y0 = 0; y0 < STEPS; y0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4*>(from + (y0 + y) * 2048);
+            if (look)
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const uint32_t nan = __vcmpeq4(w[y] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                some = some || (nan && tok < left);
-                w[y] = tok < left ? w[y] & ~nan : 0u;
+                const int at_tok = tok + (y0 + y) * ROWS;
+                uint32_t w[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+                if (at_tok >= fresh)
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) {
+                    const uint32_t nan = __vcmpeq4(w[z] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                    some = some || (nan && at_tok < left);
+                    w[z] = at_tok < left ? w[z] & ~nan : 0u;
+                  }
+                v[y] = make_uint4(w[0], w[1], w[2], w[3]);
               }
-            }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              if (key) codes4<S::BF16>(w[y], o[2 * y], o[2 * y + 1]);
-              else codes4<false>(w[y], o[2 * y], o[2 * y + 1]);
+              uint4 lo, hi;
+              e4m3x4_to_f16x4(v[y].x, lo.x, lo.y);
+              e4m3x4_to_f16x4(v[y].y, lo.z, lo.w);
+              e4m3x4_to_f16x4(v[y].z, hi.x, hi.y);
+              e4m3x4_to_f16x4(v[y].w, hi.z, hi.w);
+              uint8_t* base = to + (y0 + y) * (ROWS / 8) * S::GROUP;
+              *reinterpret_cast<uint4*>(base + c0 * 16) = turn ? hi : lo;
+              *reinterpret_cast<uint4*>(base + c1 * 16) = turn ? lo : hi;
             }
-            uint8_t* base = to + (tok >> 3) * S::GROUP + (c >> 2) * 1024 + (tok & 7) * 128;
-            const int turn = c >> 2 & 1;            // lanes of two blocks take their halves in other orders: other banks
-            const int c0 = (2 * (c & 3)) ^ (tok & 7), c1 = c0 ^ 1;
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-            *reinterpret_cast<uint4*>(base + (turn ? c1 : c0) * 16) = turn ? hi : lo;
-            *reinterpret_cast<uint4*>(base + (turn ? c0 : c1) * 16) = turn ? lo : hi;
           }
           fence_proxy_async_smem();
           if (__any_sync(ALL, some) && lane == 0) *(volatile int*)&C.odd[k % ITEMS] = 1;
@@ -923,23 +962,30 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint8_t* v = ring + st * S::RAW;
           const int tok0 = (it.t0 + j) * S::TN, left = it.len - tok0, fresh = max(0, it.older - tok0);
           const int rows = left < S::TN ? (left + 15) & ~15 : S::TN;
-          constexpr int VR = S::D / 8;
-          for (int e = fresh * VR + t; e < rows * VR; e += 128) {
+          constexpr int VR = S::D / 8;              // vectors of a row
+          auto at_vector = [&](int e) {
             const int tok = e / VR, c = e % VR;
-            uint4* p = reinterpret_cast<uint4*>(v + (tok >> 3) * S::GROUP + (c >> 3) * 1024 + (tok & 7) * 128 +
-                                                (((c & 7) ^ (tok & 7)) << 4));
-            if (tok >= left) {
-              *p = make_uint4(0, 0, 0, 0);
-            } else {
-              const uint4 w = *p;
-              const uint4 f = make_uint4(finite2<S::BF16>(w.x), finite2<S::BF16>(w.y), finite2<S::BF16>(w.z),
+            return reinterpret_cast<uint4*>(v + (tok >> 3) * S::GROUP + (c >> 3) * 1024 + (tok & 7) * 128 +
+                                            (((c & 7) ^ (tok & 7)) << 4));
+          };
+          // an exponent of ones overflows into the bit above it
+          constexpr uint32_t EXP = S::BF16 ? 0x7F807F80u : 0x7C007C00u, ONE = S::BF16 ? 0x00800080u : 0x04000400u;
+          uint32_t over = 0;
+          const int e1 = min(left, S::TN) * VR;
+#pragma unroll 8
+          for (int e = fresh * VR + t; e < e1; e += 128) {
+            const uint4 w = *at_vector(e);
+            over |= ((w.x & EXP) + ONE) | ((w.y & EXP) + ONE) | ((w.z & EXP) + ONE) | ((w.w & EXP) + ONE);
+          }
+          if (over & 0x80008000u) {
+            some = true;
+            for (int e = fresh * VR + t; e < e1; e += 128) {
+              const uint4 w = *at_vector(e);
+              *at_vector(e) = make_uint4(finite2<S::BF16>(w.x), finite2<S::BF16>(w.y), finite2<S::BF16>(w.z),
                                          finite2<S::BF16>(w.w));
-              if (f.x != w.x || f.y != w.y || f.z != w.z || f.w != w.w) {
-                *p = f;
-                some = true;
-              }
             }
           }
+          for (int e = max(fresh, left) * VR + t; e < rows * VR; e += 128) *at_vector(e) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           if (__any_sync(ALL, some) && lane == 0) *(volatile int*)&C.odd[k % ITEMS] = 1;
           __syncwarp();
@@ -969,12 +1015,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       Mask mask;
       mask.load(A, it.lo + i, i, it.len - it.older, row && n);
       float c = fabsf(A.scale * (S::E4M3 ? __ldcg(a.k_scale + it.g) : 1.f));
-      c = c < 0x1p-149f ? 0x1p-149f : c;            // a score of -inf stays one when the scale is 0
       float ref = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++tiles) {
         ok = wait(&C.s_full[tiles & 1], (tiles >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
+        if (j == 0) {
+          if (S::E4M3 && S::BF16) c *= undo[(items & 1) * M + t];
+          c = c < 0x1p-149f ? 0x1p-149f : c;        // a score of -inf stays one when the scale is 0
+        }
         const uint32_t s = lanes + S::S0 + (uint32_t)(tiles & 1) * S::TN;
         const int rel = (it.t0 + j) * S::TN - it.older;
         const bool edge = rel + S::TN > 0;
@@ -1041,7 +1090,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float e1 = exp2_fast(fmaf(__uint_as_float(r[x][y + 1]), c, -base));
             sum0 += e0;
             sum1 += e1;
-            p[y / 2] = pack2<S::PBF16>(e0, e1);
+            p[y / 2] = pack2<S::MBF16>(e0, e1);
           }
           tmem_st16(s + half * (H / 2) + 16 * x, p);
         }
