@@ -156,6 +156,47 @@ __device__ __forceinline__ uint32_t idesc(bool bf16, bool across, int n) {
          (uint32_t)(M >> 4) << 24;
 }
 
+// Rows of 16-bit elements lie apart, and a row is a lane's: 16 bytes of 32 rows are 32 half-used sectors (128 rows of 256
+// elements took 8 us to load so, and 15 us to gate and store). So four lanes take 64 bytes of one row together, of four
+// rows in turn, and change places in registers.
+__device__ __forceinline__ void change_places(uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool high = lane & b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & b) continue;
+      uint4 t = high ? v[j] : v[j ^ b];
+      t.x = __shfl_xor_sync(0xFFFFFFFFu, t.x, b);
+      t.y = __shfl_xor_sync(0xFFFFFFFFu, t.y, b);
+      t.z = __shfl_xor_sync(0xFFFFFFFFu, t.z, b);
+      t.w = __shfl_xor_sync(0xFFFFFFFFu, t.w, b);
+      if (high) v[j] = t; else v[j ^ b] = t;
+    }
+  }
+}
+// the lane's place in the rows of its four lanes: row k's 16 bytes are the lane & 3 rd, NULL where there is no row
+struct FourRows {
+  uint16_t* at[4];
+  __device__ __forceinline__ FourRows(uint16_t* row, int lane) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t p = __shfl_sync(0xFFFFFFFFu, (unsigned long long)row, (lane & ~3) + k);
+      at[k] = p ? reinterpret_cast<uint16_t*>(p) + (lane & 3) * 8 : nullptr;
+    }
+  }
+  // 32 elements from x on, as four lanes hold them together
+  __device__ __forceinline__ void load(uint4 (&v)[4], int x) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = at[k] ? __ldcg(reinterpret_cast<const uint4*>(at[k] + x)) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void store(const uint4 (&v)[4], int x) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at[k]) *reinterpret_cast<uint4*>(at[k] + x) = v[k];
+  }
+};
+
 __device__ __forceinline__ uint16_t* rows_at(const moe_rows_t& r, int64_t row, int h) {
   return (uint16_t*)r.p + row * r.row_stride + h * r.head_stride;
 }
@@ -230,8 +271,11 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
 
 // What was taken out of the values of new tokens is added to the rows that see it: HD elements of O from x on, at `o`.
 template <class S>
-__device__ __noinline__ void add_odd(const TreeArgs& A, const Item it, const Mask mask, int x, uint32_t o) {
+__device__ __noinline__ void add_odd(const TreeArgs& A, const Item& it, int t, int x, uint32_t o) {
   const moe_cache_attend_tree_t& a = A.a;
+  const int i = (it.m0 + t) / A.group;
+  Mask mask;
+  mask.load(A, it.lo + i, i, it.len - it.older, t < it.rows);
   const int ps = 1 << A.page_log2;
   const int from = max(it.older, it.t0 * S::TN), upto = (int)min((int64_t)it.len, (int64_t)it.t1 * S::TN);
   for (int c = 0; c < S::D / 2; c += 16) {
@@ -262,94 +306,77 @@ __device__ __noinline__ void add_odd(const TreeArgs& A, const Item it, const Mas
   tmem_wait_st();
 }
 
-// The sum of parts p0, p0 + by .. below p1 of a row, on their highest base; part `skip` is the thread's own, with a base
-// and a sum of its own. Loads of several parts are on their way at once.
+// The sum of parts p0, p0 + by .. below p1 of a row, on their highest base, in the order of the parts.
 template <class S>
 struct Sum {
-  float m, l, own;           // base, sum, factor of the own part
-  __device__ __forceinline__ static float factor(float pm, float pl, float m) {
+  float m = -INFINITY, l = 0.f;
+  __device__ __forceinline__ float factor(float pm, float pl) const {
     return pm == -INFINITY ? (pl == pl ? 0.f : pl) : exp2_fast(pm - m);   // no base and a sum of NaN: all scores NaN
   }
+  // base(p): a row's base, its sum M further on
   template <class F>
-  __device__ __forceinline__ void bases(F at, int p0, int p1, int by, int skip, float om, float ol, bool row) {
-    m = skip >= 0 ? om : -INFINITY;
-#pragma unroll 8
-    for (int p = p0; p < p1; p += by)
-      if (p != skip && row) m = fmaxf(m, __ldcg(at(p)));
-    own = skip >= 0 ? factor(om, ol, m) : 0.f;
-    l = 0.f;
-#pragma unroll 4
+  __device__ __forceinline__ void bases(F base, int p0, int p1, int by) {
+#pragma unroll 2
+    for (int p = p0; p < p1; p += by) m = fmaxf(m, __ldcg(base(p)));
+#pragma unroll 2
     for (int p = p0; p < p1; p += by) {
-      float pm = om, pl = ol;
-      if (p != skip && row) {
-        pm = __ldcg(at(p));
-        pl = __ldcg(at(p) + M);
-      }
-      l = fmaf(pl, factor(pm, pl, m), l);
+      const float pm = __ldcg(base(p)), pl = __ldcg(base(p) + M);
+      l = fmaf(pl, factor(pm, pl), l);
     }
   }
-  // 32 elements, at at(p) in the workspace, or of the thread's own part at `o` in tensor memory. In the order of the
-  // parts, and in fused steps, so that it does not matter which of them is the thread's own. By whole warps.
+  __device__ __forceinline__ static void load(float4 (&v)[8], const float* at) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(at) + e * M);
+  }
+  __device__ __forceinline__ static void put(float (&y)[32], const float4 (&v)[8], float f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[4 * e] = fmaf(v[e].x, f, y[4 * e]);
+      y[4 * e + 1] = fmaf(v[e].y, f, y[4 * e + 1]);
+      y[4 * e + 2] = fmaf(v[e].z, f, y[4 * e + 2]);
+      y[4 * e + 3] = fmaf(v[e].w, f, y[4 * e + 3]);
+    }
+  }
+  // 32 elements, at at(p)
   template <class F, class G>
-  __device__ __forceinline__ void add(float (&y)[32], F at, G base, int p0, int p1, int by, int skip, uint32_t o,
-                                      bool row) const {
+  __device__ __forceinline__ void add(float (&y)[32], F at, G base, int p0, int p1, int by) const {
 #pragma unroll 1
     for (int p = p0; p < p1; p += by) {
-      uint32_t v[32];
-      float f = own;
-      if (p == skip) {
-        __syncwarp();
-        tmem_ld32(o, v);
-        tmem_wait_ld32(v);
-      } else if (row) {
-        const float4* q = reinterpret_cast<const float4*>(at(p));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 w = __ldcg(q + e * M);
-          v[4 * e] = __float_as_uint(w.x);
-          v[4 * e + 1] = __float_as_uint(w.y);
-          v[4 * e + 2] = __float_as_uint(w.z);
-          v[4 * e + 3] = __float_as_uint(w.w);
-        }
-        f = factor(__ldcg(base(p)), __ldcg(base(p) + M), m);
-      }
-      if (row)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = fmaf(__uint_as_float(v[e]), f, y[e]);
+      float4 v[8];
+      load(v, at(p));
+      put(y, v, factor(__ldcg(base(p)), __ldcg(base(p) + M)));
     }
   }
 };
 
-// 32 elements of the gate, loaded before what they multiply is there, and the output's
+// 32 elements of a row's output, y vs / l (0 where l is) times the gate's sigmoid, from x on
 template <class S>
-struct Gate {
-  uint4 v[4];
-  bool some;
-  __device__ __forceinline__ Gate(const uint16_t* at, int x) : some(at != nullptr) {
-    if (some)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __ldcg(reinterpret_cast<const uint4*>(at + x) + e);
+__device__ __forceinline__ void emit(const float (&y)[32], float l, float vs, uint16_t* gate, bool gated, uint16_t* out, int x,
+                                     int lane) {
+  uint4 g[4], z[4];
+  if (gated) {
+    FourRows(gate, lane).load(g, x);
+    change_places(g, lane);
   }
-  // out: y vs / l, 0 where l is, times the gate
-  __device__ __forceinline__ void finish(const float (&y)[32], float l, float vs, uint16_t* out) const {
-    const float by = l == 0.f ? 0.f : __fdividef(vs, l);
+  const float by = l == 0.f ? 0.f : __fdividef(vs, l);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-      uint32_t z[4];
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w[4] = {g[e].x, g[e].y, g[e].z, g[e].w};
+    uint32_t r[4];
 #pragma unroll
-      for (int x = 0; x < 4; x += 2) {
-        float q[4];
+    for (int i = 0; i < 4; i += 2) {
+      float q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = l == 0.f ? 0.f : y[8 * e + 2 * x + i] * by;
-        if (some) gated4(q, unpack2<S::BF16>(w[x]), unpack2<S::BF16>(w[x + 1]));
-        z[x] = pack2<S::BF16>(q[0], q[1]);
-        z[x + 1] = pack2<S::BF16>(q[2], q[3]);
-      }
-      reinterpret_cast<uint4*>(out)[e] = make_uint4(z[0], z[1], z[2], z[3]);
+      for (int k = 0; k < 4; ++k) q[k] = l == 0.f ? 0.f : y[8 * e + 2 * i + k] * by;
+      if (gated) gated4(q, unpack2<S::BF16>(w[i]), unpack2<S::BF16>(w[i + 1]));
+      r[i] = pack2<S::BF16>(q[0], q[1]);
+      r[i + 1] = pack2<S::BF16>(q[2], q[3]);
     }
+    z[e] = make_uint4(r[0], r[1], r[2], r[3]);
   }
-};
+  change_places(z, lane);
+  FourRows(out, lane).store(z, x);
+}
 
 // By whole warps, and in line: a call would spill what is live. A wait that runs out ends the CTA's work: everyone gives up at the next wait.
 __device__ __forceinline__ bool wait_for(const TreeArgs& A, Control& C, uint64_t* bar, uint32_t parity) {
@@ -374,120 +401,120 @@ __device__ __forceinline__ bool soft_barrier(const TreeArgs& A, Control& C, int&
 // What an item's rows get, from their O in tensor memory and the parts of other CTAs; called by the softmax's warps.
 // False: a wait ran out.
 template <class S>
-__device__ __forceinline__ bool finish_item(const TreeArgs& A, Control& C, const Item& it, const Mask& mask, int cta, int k,
-                                         uint32_t lanes, float ref, float l, int& syncs) {
+__device__ __forceinline__ bool finish_item(const TreeArgs& A, Control& C, const Item& it, int cta, int k,
+                                            uint32_t lanes, float ref, float l, int& syncs) {
   constexpr int HD = S::D / 2;
   const moe_cache_attend_tree_t& a = A.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = (warp - W_SOFT) >> 2, t = (warp & 3) * 32 + lane;
-  const int n = it.t1 - it.t0, m = it.m0 + t, i = m / A.group, h = it.g * A.group + m - i * A.group;
-  const bool row = t < it.rows;
-  const uint16_t* gate = a.gate.p && row ? rows_at(a.gate, it.lo + i, h) + half * HD : nullptr;
-  bool ok = true;
-  auto all_arrive = [&] { return soft_barrier(A, C, syncs); };
-  if (n && *(volatile int*)&C.odd[k % ITEMS]) add_odd<S>(A, it, mask, half * HD, lanes + S::O + half * HD);
+  const int lane = threadIdx.x & 31, sw = (threadIdx.x >> 5) - W_SOFT, half = sw >> 2, t = (sw & 3) * 32 + lane;
+  const int n = it.t1 - it.t0, parts = it.c1 - it.c0 + 1, step = parts > FLAT ? GROUP_OF : 1, mine = cta - it.c0;
   const float vs = S::E4M3 ? __ldcg(a.v_scale + it.g) : 1.f;
-  const int parts = it.c1 - it.c0 + 1, step = parts > FLAT ? GROUP_OF : 1;
-  uint16_t* out = rows_at(a.out, it.lo + i, h) + half * HD;
-  // whether this CTA's part is the last of a split item; false: a wait ran out
-  bool last = false;
-  auto share_last = [&](uint32_t* count, int of, bool arrive) {
-    if (!all_arrive()) return false;
-    if (warp == W_SOFT && lane == 0) {              // its fences stand for all, on this side of each barrier
-      if (arrive) __threadfence();
-      const uint32_t before = arrive ? atomicAdd(count, 1u) : ld_acquire_u32(count);
-      C.last = before == (uint32_t)of - 1;
-      if (C.last) {
-        __threadfence();
-        *count = 0;
-      }
-    }
-    if (!all_arrive()) return false;
-    last = C.last;
-    return true;
+  const bool gated = a.gate.p != nullptr;
+  // a row of the batch and its head, NULL past the item's rows
+  auto row_of = [&](const moe_rows_t& r, int t) -> uint16_t* {
+    const int m = it.m0 + t, i = m / A.group;
+    return t < it.rows ? rows_at(r, it.lo + i, it.g * A.group + m - i * A.group) : nullptr;
   };
-  auto part_at = [&](int p) { return A.parts + (size_t)((it.c0 + p) * 2 + (p == 0)) * S::PART; };
-  auto base_at = [&](int p) { return part_at(p) + M * S::D + t; };
-  auto values_at = [&](int p, int x) { return part_at(p) + (size_t)(half * HD + x) / 4 * M * 4 + 4 * t; };
-  auto free_o = [&] {
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&C.o_free);
-  };
-  const int mine = cta - it.c0;
-  // all others have arrived already: this part does not leave the CTA
-  if (parts > 1 && step == 1) ok = share_last(A.counts + 3 * it.c0, parts, false);
-  if (!ok) return false;
-  if (parts > 1 && !last) {
-    float* part = part_at(mine);
+  if (n && *(volatile int*)&C.odd[k % ITEMS]) add_odd<S>(A, C.items[k % ITEMS], t, half * HD, lanes + S::O + half * HD);
+  if (parts == 1) {
+    uint16_t *out = row_of(a.out, t), *gate = gated ? row_of(a.gate, t) : nullptr;
+    if (t - lane < it.rows)                         // the warp has rows
 #pragma unroll 1
-    for (int x = 0; x < HD; x += 32) {          // [D / 4][rows] of four elements
+      for (int x = half * HD; x < half * HD + HD; x += 32) {
+        uint32_t r[32];
+        float y[32];
+        if (n) {
+          tmem_ld32(lanes + S::O + x, r);
+          tmem_wait_ld32(r);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = n ? __uint_as_float(r[e]) : 0.f;
+        emit<S>(y, l, vs, gate, gated, out, x, lane);
+      }
+    __syncwarp();
+  } else {
+    float* part = A.parts + (size_t)(cta * 2 + (mine == 0)) * S::PART;
+#pragma unroll 1
+    for (int x = half * HD; x < half * HD + HD; x += 32) {   // [D / 4][rows] of four elements
       uint32_t r[32];
       __syncwarp();
-      tmem_ld32(lanes + S::O + half * HD + x, r);
+      tmem_ld32(lanes + S::O + x, r);
       tmem_wait_ld32(r);
-      if (row) {
-        float4* to = reinterpret_cast<float4*>(part) + (half * HD + x) / 4 * M + t;
+      if (t < it.rows) {
+        float4* to = reinterpret_cast<float4*>(part) + x / 4 * M + t;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           __stcg(to + e * M, make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
                                          __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])));
       }
     }
-    if (row && half == 0) {
+    if (t < it.rows && half == 0) {
       __stcg(part + M * S::D + t, ref);
       __stcg(part + M * S::D + M + t, l);
     }
-    // Whoever counts itself last joins: where there are many parts those of its group, and then the groups.
-    const int p0 = mine / GROUP_OF * GROUP_OF, p1 = min(parts, p0 + GROUP_OF);
-    if (step == 1) {
-      ok = share_last(A.counts + 3 * it.c0, parts, true);
-    } else {
-      free_o();
-      ok = share_last(A.counts + 3 * (it.c0 + p0) + 1 + (p0 == 0), p1 - p0, true);
-      if (ok && last) {
-        float* to = part_at(p0);
-        Sum<S> sum;
-        sum.bases(base_at, p0, p1, 1, -1, 0.f, 0.f, row);
-#pragma unroll 1
-        for (int x = 0; x < HD; x += 32) {
-          float y[32] = {};
-          sum.add(y, [&](int p) { return values_at(p, x); }, base_at, p0, p1, 1, -1, 0, row);
-          if (row)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              __stcg(reinterpret_cast<float4*>(to) + ((half * HD + x) / 4 + e) * M + t,
-                     make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
-        }
-        if (!all_arrive()) return false;            // both halves have read the row's bases
-        if (row && half == 0) {
-          __stcg(to + M * S::D + t, sum.m);
-          __stcg(to + M * S::D + M + t, sum.l);
-        }
-        ok = share_last(A.counts + 3 * it.c0, (parts + step - 1) / step, true);
+  }
+  if (n) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&C.o_free);
+  }
+  if (parts == 1) return true;
+
+  // Whoever counts itself last joins: where there are many parts those of its group, and then the groups.
+  bool last = false;
+  auto arrive = [&](uint32_t* count, int of) {
+    if (!soft_barrier(A, C, syncs)) return false;
+    if (sw == 0 && lane == 0) {                     // its fences stand for all, on this side of each barrier
+      __threadfence();
+      C.last = atomicAdd(count, 1u) == (uint32_t)of - 1;
+      if (C.last) {
+        __threadfence();
+        *count = 0;
       }
     }
-    if (!ok) return false;
-    if (!last) {
-      if (step == 1) free_o();
-      return true;
+    if (!soft_barrier(A, C, syncs)) return false;
+    last = C.last;
+    return true;
+  };
+  auto part_at = [&](int p) { return A.parts + (size_t)((it.c0 + p) * 2 + (p == 0)) * S::PART; };
+  // 32 rows and 32 elements at a time, whichever warp: f(row, x, elements, sum)
+  const int row_tiles = (it.rows + 31) / 32;
+  auto join = [&](int p0, int p1, int by, auto f) {
+#pragma unroll 1
+    for (int q = sw; q < row_tiles * (S::D / 32); q += SOFT) {
+      const int x = q / row_tiles * 32, t = q % row_tiles * 32 + lane, u = min(t, it.rows - 1);
+      auto base = [&](int p) { return part_at(p) + M * S::D + u; };
+      Sum<S> sum;
+      float y[32] = {};
+      sum.bases(base, p0, p1, by);
+      sum.add(y, [&](int p) { return part_at(p) + (size_t)(x / 4 * M + u) * 4; }, base, p0, p1, by);
+      f(t, x, y, sum);
+    }
+    __syncwarp();
+  };
+  if (step > 1) {
+    const int p0 = mine / GROUP_OF * GROUP_OF, p1 = min(parts, p0 + GROUP_OF);
+    if (!arrive(A.counts + 3 * (it.c0 + p0) + 1 + (p0 == 0), p1 - p0)) return false;
+    if (!last) return true;
+    float* to = part_at(p0);
+    join(p0, p1, 1, [&](int t, int x, const float (&y)[32], const Sum<S>& sum) {
+      if (t >= it.rows) return;
+      float4* q = reinterpret_cast<float4*>(to) + x / 4 * M + t;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) __stcg(q + e * M, make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
+    });
+    Sum<S> sum;
+    if (t < it.rows) sum.bases([&](int p) { return part_at(p) + M * S::D + t; }, p0, p1, 1);
+    if (!soft_barrier(A, C, syncs)) return false;   // all have read the group's bases
+    if (t < it.rows && half == 0) {
+      __stcg(to + M * S::D + t, sum.m);
+      __stcg(to + M * S::D + M + t, sum.l);
     }
   }
-  // the whole item, or all of its parts: in order, the CTA's own from tensor memory where it is still there
-  const bool here = step == 1;
-  Sum<S> sum;
-  sum.m = ref;
-  sum.l = l;
-  sum.own = 1.f;
-  if (parts > 1) sum.bases(base_at, 0, parts, step, here ? mine : -1, ref, l, row);
-#pragma unroll 1
-  for (int x = 0; x < HD; x += 32) {
-    const Gate<S> gate_x(gate, x);
-    float y[32] = {};
-    if (n) sum.add(y, [&](int p) { return values_at(p, x); }, base_at, parts > 1 ? 0 : mine, parts > 1 ? parts : mine + 1, step,
-                   here ? mine : -1, lanes + S::O + half * HD + x, row);
-    if (row) gate_x.finish(y, sum.l, vs, out + x);
-  }
-  if (n && here) free_o();
+  if (!arrive(A.counts + 3 * it.c0, (parts + step - 1) / step)) return false;
+  if (last)
+    join(0, parts, step, [&](int t, int x, const float (&y)[32], const Sum<S>& sum) {
+      emit<S>(y, sum.l, vs, gated ? row_of(a.gate, t) : nullptr, gated, row_of(a.out, t), x, lane);
+    });
   return true;
 }
 
@@ -838,19 +865,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the queries, turned where the scale is negative: the largest score is then the largest product
         const bool turn = A.scale * (S::E4M3 ? __ldcg(a.k_scale + it.g) : 1.f) < 0.f;
         const int m = it.m0 + t, i = m / A.group;
-        const uint4* q = reinterpret_cast<const uint4*>(rows_at(a.q, it.lo + i, it.g * A.group + m - i * A.group));
+        const FourRows q(t < it.rows ? rows_at(a.q, it.lo + i, it.g * A.group + m - i * A.group) : nullptr, lane);
         constexpr int C0 = S::D / 2 < 64 ? S::D / 2 : 64;              // columns at a time
         // bf16 queries over an 8-bit cache, in fp16: times a power of two that brings the row's largest to 2^14 or above
         float by = 1.f;
         if (S::E4M3 && S::BF16) {
           uint32_t big = 0;
-          if (t < it.rows)
-#pragma unroll 8
-            for (int x = 0; x < S::D / 8; ++x) {
-              const uint4 v = __ldcg(q + x);
-              big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-            }
+          // four lanes see parts of four rows; each row's maxima meet in its own lane
+          uint32_t rows[4] = {};
+#pragma unroll 2
+          for (int x = 0; x < S::D; x += 32) {
+            uint4 v[4];
+            q.load(v, x);
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              rows[z] = __vmaxu2(rows[z], __vmaxu2(__vmaxu2(v[z].x & 0x7FFF7FFFu, v[z].y & 0x7FFF7FFFu),
+                                                   __vmaxu2(v[z].z & 0x7FFF7FFFu, v[z].w & 0x7FFF7FFFu)));
+          }
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            rows[z] = __vmaxu2(rows[z], __shfl_xor_sync(ALL, rows[z], 1));
+            rows[z] = __vmaxu2(rows[z], __shfl_xor_sync(ALL, rows[z], 2));
+            big = (lane & 3) == z ? rows[z] : big;
+          }
           big = max(big & 0xFFFFu, big >> 16);
           // its exponent, 2^(e - 127): by 2^(141 - e), within fp32's normal range; infinities and NaN stay what they are
           const int e = (int)(big >> 7), f = e == 255 ? 127 : min(253, 268 - e);
@@ -858,35 +895,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
 #pragma unroll
         for (int c = 0; c < S::D / 2; c += C0) {
-          uint32_t r[C0];
+          uint4 v[C0 / 16][4];
 #pragma unroll
-          for (int x = 0; x < C0 / 4; ++x) {
-            const uint4 v = t < it.rows ? __ldcg(q + c / 4 + x) : make_uint4(0, 0, 0, 0);
-            r[4 * x] = v.x;
-            r[4 * x + 1] = v.y;
-            r[4 * x + 2] = v.z;
-            r[4 * x + 3] = v.w;
-          }
-          if (S::E4M3 && S::BF16)
-#pragma unroll
-            for (int x = 0; x < C0; ++x) {
-              const float2 f = unpack2<true>(r[x]);
-              r[x] = pack2<false>(f.x * by, f.y * by);
-            }
-          if (turn)
-#pragma unroll
-            for (int x = 0; x < C0; ++x) r[x] ^= 0x80008000u;
+          for (int x = 0; x < C0 / 16; ++x) q.load(v[x], 2 * c + 32 * x);
           if (c == 0) {
             ok = wait(&C.q_free, (items & 1) ^ 1);
             tc_fence_after();
             if (S::E4M3 && S::BF16) undo[(items & 1) * M + t] = __uint_as_float(0x7F000000u - __float_as_uint(by));
           }
 #pragma unroll
-          for (int x = 0; x < C0; x += 16) {
-            uint32_t v[16];
+          for (int x = 0; x < C0 / 16; ++x) {
+            change_places(v[x], lane);
+            uint32_t r[16];
 #pragma unroll
-            for (int y = 0; y < 16; ++y) v[y] = r[x + y];
-            tmem_st16(tmem + ((uint32_t)(wq * 32) << 16) + S::Q + c + x, v);
+            for (int z = 0; z < 4; ++z) {
+              r[4 * z] = v[x][z].x;
+              r[4 * z + 1] = v[x][z].y;
+              r[4 * z + 2] = v[x][z].z;
+              r[4 * z + 3] = v[x][z].w;
+            }
+#pragma unroll
+            for (int z = 0; z < 16; ++z) {
+              if (S::E4M3 && S::BF16) {
+                const float2 f = unpack2<true>(r[z]);
+                r[z] = pack2<false>(f.x * by, f.y * by);
+              }
+              if (turn) r[z] ^= 0x80008000u;
+            }
+            tmem_st16(tmem + ((uint32_t)(wq * 32) << 16) + S::Q + c + 16 * x, r);
           }
         }
         tmem_wait_st();
@@ -1006,12 +1042,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     Item it;
     auto all_arrive = [&] { return soft_barrier(A, C, syncs); };
     for (int k = 0; ok && next_item(k, it); ++k) {
-      const int n = it.t1 - it.t0, m = it.m0 + t, i = m / A.group, h = it.g * A.group + m - i * A.group;
+      const int n = it.t1 - it.t0, m = it.m0 + t, i = m / A.group;
       const bool row = t < it.rows;
-      const uint16_t* gate = a.gate.p && row ? rows_at(a.gate, it.lo + i, h) + half * HD : nullptr;
-      if (gate)
+      if (a.gate.p && row) {
+        const uint16_t* gate = rows_at(a.gate, it.lo + i, it.g * A.group + m - i * A.group) + half * HD;
 #pragma unroll
         for (int x = 0; x < HD; x += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(gate + x));
+      }
       Mask mask;
       mask.load(A, it.lo + i, i, it.len - it.older, row && n);
       float c = fabsf(A.scale * (S::E4M3 ? __ldcg(a.k_scale + it.g) : 1.f));
@@ -1114,7 +1151,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      ok = finish_item<S>(A, C, it, mask, cta, k, lanes, ref, l, syncs);
+      ok = finish_item<S>(A, C, it, cta, k, lanes, ref, l, syncs);
       done_item(k);
     }
   }
