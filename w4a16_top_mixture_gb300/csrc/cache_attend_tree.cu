@@ -103,7 +103,7 @@ __device__ __forceinline__ void gated4(float (&y)[4], float2 g0, float2 g1) {
     y[i] = x[i] < 0.f ? y[i] * e : y[i];
     d[i] = 1.f + e;
   }
-  const float a = d[0] * d[1], b = d[2] * d[3], r = __frcp_rn(a * b), ra = r * b, rb = r * a;
+  const float a = d[0] * d[1], b = d[2] * d[3], r = __fdividef(1.f, a * b), ra = r * b, rb = r * a;
   y[0] *= ra * d[1];
   y[1] *= ra * d[0];
   y[2] *= rb * d[3];
@@ -349,7 +349,7 @@ struct Sum {
   }
 };
 
-// 32 elements of a row's output, y vs / l (0 where l is) times the gate's sigmoid, from x on
+// 32 elements of a row's output, y vs / l (0 where l is 0) times the gate's sigmoid, from x on
 template <class S>
 __device__ __forceinline__ void emit(const float (&y)[32], float l, float vs, uint16_t* gate, bool gated, uint16_t* out, int x,
                                      int lane) {
@@ -358,7 +358,7 @@ __device__ __forceinline__ void emit(const float (&y)[32], float l, float vs, ui
     FourRows(gate, lane).load(g, x);
     change_places(g, lane);
   }
-  const float by = l == 0.f ? 0.f : __fdividef(vs, l);
+  const float by = l == 0.f ? 0.f : __fdividef(vs, l);       // a row that saw nothing has an O of 0
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t w[4] = {g[e].x, g[e].y, g[e].z, g[e].w};
@@ -367,7 +367,7 @@ __device__ __forceinline__ void emit(const float (&y)[32], float l, float vs, ui
     for (int i = 0; i < 4; i += 2) {
       float q[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) q[k] = l == 0.f ? 0.f : y[8 * e + 2 * i + k] * by;
+      for (int k = 0; k < 4; ++k) q[k] = y[8 * e + 2 * i + k] * by;
       if (gated) gated4(q, unpack2<S::BF16>(w[i]), unpack2<S::BF16>(w[i + 1]));
       r[i] = pack2<S::BF16>(q[0], q[1]);
       r[i + 1] = pack2<S::BF16>(q[2], q[3]);
@@ -401,10 +401,11 @@ __device__ __forceinline__ bool soft_barrier(const TreeArgs& A, Control& C, int&
 // What an item's rows get, from their O in tensor memory and the parts of other CTAs; called by the softmax's warps.
 // False: a wait ran out.
 template <class S>
-__device__ __forceinline__ bool finish_item(const TreeArgs& A, Control& C, const Item& it, int cta, int k,
-                                            uint32_t lanes, float ref, float l, int& syncs) {
+__device__ __forceinline__ bool finish_item(const TreeArgs& A, Control& C, int slot, uint32_t lanes, float ref, float l, int& syncs) {
   constexpr int HD = S::D / 2;
   const moe_cache_attend_tree_t& a = A.a;
+  const Item& it = C.items[slot];
+  const int cta = blockIdx.x;
   const int lane = threadIdx.x & 31, sw = (threadIdx.x >> 5) - W_SOFT, half = sw >> 2, t = (sw & 3) * 32 + lane;
   const int n = it.t1 - it.t0, parts = it.c1 - it.c0 + 1, step = parts > FLAT ? GROUP_OF : 1, mine = cta - it.c0;
   const float vs = S::E4M3 ? __ldcg(a.v_scale + it.g) : 1.f;
@@ -414,7 +415,7 @@ __device__ __forceinline__ bool finish_item(const TreeArgs& A, Control& C, const
     const int m = it.m0 + t, i = m / A.group;
     return t < it.rows ? rows_at(r, it.lo + i, it.g * A.group + m - i * A.group) : nullptr;
   };
-  if (n && *(volatile int*)&C.odd[k % ITEMS]) add_odd<S>(A, C.items[k % ITEMS], t, half * HD, lanes + S::O + half * HD);
+  if (n && *(volatile int*)&C.odd[slot]) add_odd<S>(A, it, t, half * HD, lanes + S::O + half * HD);
   if (parts == 1) {
     uint16_t *out = row_of(a.out, t), *gate = gated ? row_of(a.gate, t) : nullptr;
     if (t - lane < it.rows)                         // the warp has rows
@@ -1039,9 +1040,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
     int tiles = 0, items = 0, syncs = 0;
     bool ok = true;
-    Item it;
     auto all_arrive = [&] { return soft_barrier(A, C, syncs); };
-    for (int k = 0; ok && next_item(k, it); ++k) {
+    for (int k = 0; ok && wait(&C.item_full[k % ITEMS], (k / ITEMS) & 1); ++k) {
+      const Item& it = C.items[k % ITEMS];          // in shared memory: registers are short
+      if (it.b < 0) break;
       const int n = it.t1 - it.t0, m = it.m0 + t, i = m / A.group;
       const bool row = t < it.rows;
       if (a.gate.p && row) {
@@ -1104,15 +1106,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int x = half * HD; x < half * HD + HD; x += 32) {
-              uint32_t o[32];
+            for (int x = half * HD; x < half * HD + HD; x += 16) {
+              uint32_t o[16];
               __syncwarp();
-              tmem_ld32(lanes + S::O + x, o);
-              tmem_wait_ld32(o);
+              tmem_ld16_nowait(lanes + S::O + x, o);
+              tmem_wait_ld(o);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_st32(lanes + S::O + x, o);
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st16(lanes + S::O + x, o);
             }
+            tmem_wait_st();
           }
         }
         const float base = ref == -INFINITY ? 0.f : ref - S::LIFT;
@@ -1151,7 +1154,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      ok = finish_item<S>(A, C, it, cta, k, lanes, ref, l, syncs);
+      ok = finish_item<S>(A, C, k % ITEMS, lanes, ref, l, syncs);
       done_item(k);
     }
   }
