@@ -29,7 +29,7 @@ namespace moe {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int THREADS = 512, MAX_CTAS = 1024, EXTRA = 2, SHORT = 5, ITEMS = 4, M = 128;
+constexpr int THREADS = 512, MAX_CTAS = 1024, EXTRA = 7, SHORT = EXTRA + 3, ITEMS = 4, M = 128;
 constexpr int GROUP_OF = 8, FLAT = 12;    // parts that are joined at once; from FLAT + 1 on in groups first
 constexpr int SMEM = 227 * 1024, MISC = 3072;
 constexpr int W_PRODUCE = 0, W_MMA = 1, W_FIND = 2, W_SOFT = 4, W_PREP = 12, SOFT = 8;   // SOFT: warps of the softmax
@@ -271,37 +271,38 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
 
 // What was taken out of the values of new tokens is added to the rows that see it: HD elements of O from x on, at `o`.
 template <class S>
-__device__ __noinline__ void add_odd(const TreeArgs& A, const Item& it, int t, int x, uint32_t o) {
+__device__ __forceinline__ void add_odd(const TreeArgs& A, const Item& it, int t, int x, uint32_t o) {
   const moe_cache_attend_tree_t& a = A.a;
   const int i = (it.m0 + t) / A.group;
-  Mask mask;
-  mask.load(A, it.lo + i, i, it.len - it.older, t < it.rows);
+  auto sees = [&](int j) {
+    return t < it.rows && (a.masks ? __ldcg((const unsigned long long*)a.masks + (size_t)(it.lo + i) * a.mask_words + (j >> 6)) >> (j & 63) & 1
+                                   : j <= i);
+  };
   const int ps = 1 << A.page_log2;
   const int from = max(it.older, it.t0 * S::TN), upto = (int)min((int64_t)it.len, (int64_t)it.t1 * S::TN);
-  for (int c = 0; c < S::D / 2; c += 16) {
-    uint32_t r[16];
+#pragma unroll 1
+  for (int c = 0; c < S::D / 2; ++c) {              // seldom called: an element at a time, with few registers
+    uint32_t r;
     __syncwarp();
-    tmem_ld16_nowait(o + c, r);
-    tmem_wait_ld(r);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(o + c) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r) : : "memory");
+#pragma unroll 1
     for (int p = from; p < upto; ++p) {
       const int j = p - it.older, page = __ldcg(a.tables + (size_t)it.b * a.table_stride + (p >> A.page_log2));
-      if (page < 0 || page >= A.n_pages || !(mask.word(j >> 5) >> (j & 31) & 1)) continue;
+      if (page < 0 || page >= A.n_pages || !sees(j)) continue;
       const int64_t at = page * a.v_page_stride + ((int64_t)it.g * ps + (p & (ps - 1))) * S::D + x + c;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float v;
-        if (S::E4M3) {
-          uint32_t lo, hi;
-          e4m3x4_to_f16x4(__ldcg((const uint8_t*)a.v_cache + at + e), lo, hi);
-          v = unpack2<false>(lo).x;
-        } else {
-          v = unpack2<S::BF16>(__ldcg((const unsigned short*)a.v_cache + at + e)).x;
-        }
-        if (!(fabsf(v) <= 3.4028234663852886e38f)) r[e] = __float_as_uint(__uint_as_float(r[e]) + v);
+      float v;
+      if (S::E4M3) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16x4(__ldcg((const uint8_t*)a.v_cache + at), lo, hi);
+        v = unpack2<false>(lo).x;
+      } else {
+        v = unpack2<S::BF16>(__ldcg((const unsigned short*)a.v_cache + at)).x;
       }
+      if (!(fabsf(v) <= 3.4028234663852886e38f)) r = __float_as_uint(__uint_as_float(r) + v);
     }
     __syncwarp();
-    tmem_st16(o + c, r);
+    tmem_st1(o + c, r);
   }
   tmem_wait_st();
 }
@@ -313,15 +314,24 @@ struct Sum {
   __device__ __forceinline__ float factor(float pm, float pl) const {
     return pm == -INFINITY ? (pl == pl ? 0.f : pl) : exp2_fast(pm - m);   // no base and a sum of NaN: all scores NaN
   }
-  // base(p): a row's base, its sum M further on
+  // base(p): a row's base, its sum M further on; four at a time
   template <class F>
   __device__ __forceinline__ void bases(F base, int p0, int p1, int by) {
-#pragma unroll 2
-    for (int p = p0; p < p1; p += by) m = fmaxf(m, __ldcg(base(p)));
-#pragma unroll 2
-    for (int p = p0; p < p1; p += by) {
-      const float pm = __ldcg(base(p)), pl = __ldcg(base(p) + M);
-      l = fmaf(pl, factor(pm, pl), l);
+#pragma unroll 1
+    for (int p = p0; p < p1; p += 4 * by) {
+      float pm[4], pl[4], top = m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* q = base(min(p + i * by, p1 - 1));       // the last one again adds nothing
+        pm[i] = __ldcg(q);
+        pl[i] = __ldcg(q + M);
+        if (p + i * by >= p1) pm[i] = -INFINITY, pl[i] = 0.f;
+        top = fmaxf(top, pm[i]);
+      }
+      l *= m == -INFINITY ? (l == l ? 0.f : l) : exp2_fast(m - top);
+      m = top;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l = fmaf(pl[i], factor(pm[i], pl[i]), l);
     }
   }
   __device__ __forceinline__ static void load(float4 (&v)[8], const float* at) {
@@ -390,6 +400,12 @@ __device__ __forceinline__ bool wait_for(const TreeArgs& A, Control& C, uint64_t
     atomicOr(A.status, CACHE_BAD_WAIT);
   }
   return false;
+}
+// what is in flight lands, or 100 ms pass
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u) && globaltimer() - t0 < 100000000) {
+  }
 }
 // a barrier of the softmax's warps; n counts them
 __device__ __forceinline__ bool soft_barrier(const TreeArgs& A, Control& C, int& n) {
@@ -780,8 +796,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // copies in flight land before the CTA ends
     if (!ok || *(volatile int*)&C.abort) {
-      for (int i = max(0, at - S::NR); i < at; ++i) mbar_wait(&C.full[i % S::NR], (i / S::NR) & 1, 1000000);
-      for (int i = max(0, news - 8); i < news; ++i) mbar_wait(&C.new_full[i % 8], (i / 8) & 1, 1000000);
+      for (int i = max(0, at - S::NR); i < at; ++i) drain(&C.full[i % S::NR], (i / S::NR) & 1);
+      for (int i = max(0, news - 8); i < news; ++i) drain(&C.new_full[i % 8], (i / 8) & 1);
     }
   } else if (warp == W_MMA) {
     int at = 0, tiles = 0, fixes = 0, items = 0;    // stages, tiles, looked-through tiles, items with tiles so far
@@ -854,7 +870,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // what was issued ends before tensor memory is given back
     if (elect_one()) umma_commit(&C.drained);
     __syncwarp();
-    mbar_wait(&C.drained, 0, 100000000);
+    drain(&C.drained, 0);
   } else if (warp >= W_PREP) {
     const int t = threadIdx.x - W_PREP * 32, wq = warp - W_PREP;   // a row's thread
     int at = 0, items = 0, news = 0;
