@@ -53,7 +53,7 @@ struct Shape {
   static constexpr int TN = D == 256 ? 64 : 128;
   static constexpr int BLOCKS = D / 64, GROUP = BLOCKS * 1024;                 // of 8 tokens
   static constexpr int TILE = TN / 8 * GROUP, RAW = E4M3 ? TN * D : TILE;
-  static constexpr int NC = E4M3 ? 3 : 0;                                      // converted tiles
+  static constexpr int NC = E4M3 ? 4 : 0;                                      // converted tiles
   static constexpr int CTL = MISC + (E4M3 ? 2 * M * 4 : 0);
   static constexpr int NR0 = (SMEM - CTL - NC * TILE) / RAW, NR = NR0 > 12 ? 12 : NR0;
   static constexpr int DYN = NC * TILE + NR * RAW + CTL;
@@ -224,9 +224,21 @@ __device__ __forceinline__ long long units_of(const TreeArgs& A, const Request& 
   return (long long)A.Hkv * r.m_tiles * (r.tiles + EXTRA);
 }
 
-// Where tile k of an item of n tiles lies among its stages: keys one tile ahead of values, K0 K1 V0 K2 V1 .. V(n-1)
-__device__ __forceinline__ int key_at(int k) { return k ? 2 * k - 1 : 0; }
-__device__ __forceinline__ int value_at(int k, int n) { return k + 1 < n ? 2 * k + 2 : 2 * n - 1; }
+// An item's stages: keys are one tile ahead of values, K0 K1 V0 K2 V1 .. V(n-1)
+
+// a place in a ring of N stages and the parity of its round, one after another
+template <int N>
+struct Place {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int by = 1) {          // by <= N
+    at += by;
+    if (at >= N) {
+      at -= N;
+      parity ^= 1;
+    }
+  }
+};
 
 // a row's mask over its request's new tokens, as 32-bit words
 struct Mask {
@@ -557,10 +569,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 12; ++i) {
       mbar_init(&C.full[i], 1);
-      mbar_init(&C.empty[i], S::E4M3 ? 4 : 1);      // the converting warps, or the products that read it
+      mbar_init(&C.empty[i], S::E4M3 ? 2 : 1);      // the converting warps, or the products that read it
     }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&C.new_full[i], S::E4M3 ? 4 : 1);
+      mbar_init(&C.new_full[i], S::E4M3 ? 2 : 1);
       mbar_init(&C.fixed[i], S::E4M3 ? 1 : 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -731,6 +743,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int ps = 1 << A.page_log2;
     const int box = ps < S::TN ? ps : S::TN;        // tokens of a copy
     const uint32_t bytes = (uint32_t)box * S::D * (S::E4M3 ? 1 : 2);
+    Place<S::NR> to;
     int at = 0, news = 0;                           // stages filled; those with values of new tokens, 16-bit
     bool ok = true, skip = A.skip_copy && cta == 0;
     Item it;
@@ -759,12 +772,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         return __shfl_sync(ALL, ids, (p & 31) + lane & 31);
       };
       auto copy = [&](const CUtensorMap* map, int t, int id, bool values) {
-        const int st = at % S::NR;
+        const int st = to.at;
         // what is looked through first has barriers of its own: whoever looks waits for these alone, and would pass a
         // stage's barrier, by its parity, on an earlier use of the stage
         const bool fresh = !S::E4M3 && values && (int64_t)(t + 1) * S::TN > it.older;
         uint64_t* bar = fresh ? &C.new_full[news % 8] : &C.full[st];
-        ok = ok && wait(&C.empty[st], ((at / S::NR) & 1) ^ 1);
+        ok = ok && wait(&C.empty[st], to.parity ^ 1);
         if (!ok) return;
         const int64_t tok = (int64_t)t * S::TN;
         const int pages = min(S::TN / box, held - (int)(tok >> A.page_log2));
@@ -775,12 +788,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane < pages && !skip) {
           const int off = it.g * ps + (int)(tok & (ps - 1));
-          uint8_t* to = ring + st * S::RAW + lane * bytes;
-          if (S::E4M3) tma3(to, map, off, id, bar, policy);
-          else tma5(to, map, off >> 3, id, bar, policy);
+          uint8_t* stage = ring + st * S::RAW + lane * bytes;
+          if (S::E4M3) tma3(stage, map, off, id, bar, policy);
+          else tma5(stage, map, off >> 3, id, bar, policy);
         }
         skip = false;
         ++at;
+        to.next();
         news += fresh;
       };
       int kid = n ? ids_of(it.t0) : 0;
@@ -800,7 +814,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = max(0, news - 8); i < news; ++i) drain(&C.new_full[i % 8], (i / 8) & 1);
     }
   } else if (warp == W_MMA) {
-    int at = 0, tiles = 0, fixes = 0, items = 0;    // stages, tiles, looked-through tiles, items with tiles so far
+    Place<S::E4M3 ? S::NC1 : S::NR> from;           // in the order of the stages
+    int tiles = 0, fixes = 0, items = 0;            // tiles, looked-through tiles, items with tiles so far
     bool ok = true;
     Item it;
     for (int k = 0; ok && next_item(k, it); ++k) {
@@ -809,18 +824,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (n == 0) continue;
       ok = wait(&C.q_ready, items & 1);
       tc_fence_after();
-      auto landed = [&](int i) {                    // the item's stage i
-        const int x = at + i;
-        return S::E4M3 ? wait(&c_full[x % S::NC1], (x / S::NC1) & 1) : wait(&C.full[x % S::NR], (x / S::NR) & 1);
-      };
-      auto place = [&](int i, uint64_t** release) {
-        const int x = at + i;
-        *release = S::E4M3 ? &c_empty[x % S::NC1] : &C.empty[x % S::NR];
-        return smem_u32(S::E4M3 ? conv + x % S::NC1 * S::TILE : ring + x % S::NR * S::RAW);
-      };
-      auto scores = [&](int j) {                    // S = Q K^T of the item's tile j
-        uint64_t* release;
-        const uint64_t d = desc_sw128(place(key_at(j), &release), 0, S::GROUP);
+      using At = Place<S::E4M3 ? S::NC1 : S::NR>;
+      uint64_t *full = S::E4M3 ? c_full : C.full, *empty = S::E4M3 ? c_empty : C.empty;
+      auto place = [&](const At& x) { return smem_u32(S::E4M3 ? conv + x.at * S::TILE : ring + x.at * S::RAW); };
+      auto scores = [&](int j, const At& x0) {      // S = Q K^T of the item's tile j
+        const uint64_t d = desc_sw128(place(x0), 0, S::GROUP);
         const int left = it.len - (it.t0 + j) * S::TN;
         const int cols = left < S::TN ? (left + 15) & ~15 : S::TN;
         const uint32_t id = idesc(S::MBF16, false, cols), s = tmem + S::S0 + (uint32_t)((tiles + j) & 1) * S::TN;
@@ -829,14 +837,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int x = 0; x < S::D / 16; ++x)
             umma_f16_ts(s, tmem + S::Q + x * 8, d + (x / 4) * 64 + (x % 4) * 2, id, x > 0);
           umma_commit(&C.s_full[(tiles + j) & 1]);
-          umma_commit(release);
+          umma_commit(&empty[x0.at]);
           if (j == n - 1) umma_commit(&C.q_free);
         }
         __syncwarp();
       };
       for (int j = 0; j < 2 && j < n && ok; ++j) {
-        ok = landed(key_at(j));
-        if (ok) scores(j);
+        ok = wait(&full[from.at], from.parity);
+        if (ok) scores(j, from);
+        from.next();
       }
       for (int j = 0; j < n && ok; ++j) {
         const int g = tiles + j, left = it.len - (it.t0 + j) * S::TN;
@@ -844,26 +853,33 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = wait(&C.fixed[fixes % 8], (fixes / 8) & 1);
           ++fixes;
         }
-        ok = ok && landed(value_at(j, n)) && (j + 2 >= n || landed(key_at(j + 2))) &&
-             (j > 0 || wait(&C.o_free, (items & 1) ^ 1)) && wait(&C.p_ready[g & 1], (g >> 1) & 1);
+        // V of this tile, K of the one after the next; all three at once where they are ready
+        const At v = from;
+        from.next();
+        const At x2 = from;
+        const bool more = j + 2 < n;
+        if (more) from.next();
+        if (j == 0) ok = ok && wait(&C.o_free, (items & 1) ^ 1);
+        if (!__all_sync(ALL, mbar_try_wait(&full[v.at], v.parity) && (!more || mbar_try_wait(&full[x2.at], x2.parity)) &&
+                                 mbar_try_wait(&C.p_ready[g & 1], (g >> 1) & 1)))
+          ok = ok && wait(&full[v.at], v.parity) && (!more || wait(&full[x2.at], x2.parity)) &&
+               wait(&C.p_ready[g & 1], (g >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        uint64_t* release;
-        const uint64_t d = desc_sw128(place(value_at(j, n), &release), 1024, S::GROUP);
+        const uint64_t d = desc_sw128(place(v), 1024, S::GROUP);
         const int steps = left < S::TN ? (left + 15) >> 4 : S::TN / 16;
         const uint32_t id = idesc(S::MBF16, true, S::D), p = tmem + S::S0 + (uint32_t)(g & 1) * S::TN;
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < S::TN / 16; ++x)
             if (x < steps) umma_f16_ts(tmem + S::O, p + x * 8, d + (uint64_t)(x * 2 * S::GROUP >> 4), id, j > 0 || x > 0);
-          umma_commit(release);
+          umma_commit(&empty[v.at]);
           umma_commit(&C.pv_done);
           if (j == n - 1) umma_commit(&C.o_full);
         }
         __syncwarp();
-        if (j + 2 < n) scores(j + 2);
+        if (more) scores(j + 2, x2);
       }
-      at += 2 * n;
       tiles += n;
       ++items;
     }
@@ -873,7 +889,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     drain(&C.drained, 0);
   } else if (warp >= W_PREP) {
     const int t = threadIdx.x - W_PREP * 32, wq = warp - W_PREP;   // a row's thread
-    int at = 0, items = 0, news = 0;
+    int at = 0, items = 0, news = 0;                // at: stages of the items before
+    Place<S::NR> raw;                               // of an 8-bit cache: two warps take every other stage
+    Place<S::NC1> cv;
+    if (S::E4M3 && wq >> 1) {
+      raw.next();
+      cv.next();
+    }
     bool ok = true;
     Item it;
     for (int k = 0; ok && next_item(k, it); ++k) {
@@ -950,27 +972,27 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       bool some = false;                            // values that are not finite
       if (S::E4M3) {
-        // every tile, in the order of the stages
-        for (int x = 0; x < 2 * n && ok; ++x) {
+        // every tile, in the order of the stages; an item has an even number of them
+        for (int x = wq >> 1; x < 2 * n && ok; x += 2, raw.next(2), cv.next(2)) {
           const bool key = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
           const int j = x == 0 ? 0 : x == 2 * n - 1 ? n - 1 : key ? (x + 1) / 2 : x / 2 - 1;
-          const int st = (at + x) % S::NR, cv = (at + x) % S::NC1;
-          ok = ok && wait(&C.full[st], ((at + x) / S::NR) & 1) && wait(&c_empty[cv], (((at + x) / S::NC1) & 1) ^ 1);
+          if (!__all_sync(ALL, mbar_try_wait(&C.full[raw.at], raw.parity) && mbar_try_wait(&c_empty[cv.at], cv.parity ^ 1)))
+            ok = wait(&C.full[raw.at], raw.parity) && wait(&c_empty[cv.at], cv.parity ^ 1);
           if (!ok) break;
-          // a thread's vectors lie 128 apart: the same 16 elements of rows a fixed number apart
-          constexpr int VR = S::D / 16, ROWS = 128 / VR, STEPS = S::TN / ROWS;
-          const int tok = t / VR, c = t % VR;
-          const uint8_t* from = ring + st * S::RAW + t * 16;
-          uint8_t* to = conv + cv * S::TILE + (tok >> 3) * S::GROUP + (c >> 2) * 1024 + (tok & 7) * 128;
+          // a thread's vectors lie 64 apart: the same 16 elements of rows a fixed number apart
+          constexpr int VR = S::D / 16, ROWS = 64 / VR, STEPS = S::TN / ROWS;
+          const int t = threadIdx.x & 63, tok = t / VR, c = t % VR;
+          const uint8_t* from = ring + raw.at * S::RAW + t * 16;
+          uint8_t* to = conv + cv.at * S::TILE + (c >> 2) * 1024;
           // lanes of neighbouring blocks store their halves in other orders: other banks
-          const int turn = c >> 2 & 1, c0 = ((2 * (c & 3)) ^ (tok & 7)) ^ turn, c1 = c0 ^ 1;
+          const int turn = c >> 2 & 1;
           const int tok0 = (it.t0 + j) * S::TN, left = it.len - tok0, fresh = it.older - tok0;
           const bool look = !key && fresh < S::TN;
 #pragma unroll
           for (int y0 = 0; y0 < STEPS; y0 += 4) {
             uint4 v[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4*>(from + (y0 + y) * 2048);
+            for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4*>(from + (y0 + y) * 1024);
             if (look)
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
@@ -992,24 +1014,25 @@ __global__ void __launch_bounds__(THREADS, 1)
               e4m3x4_to_f16x4(v[y].y, lo.z, lo.w);
               e4m3x4_to_f16x4(v[y].z, hi.x, hi.y);
               e4m3x4_to_f16x4(v[y].w, hi.z, hi.w);
-              uint8_t* base = to + (y0 + y) * (ROWS / 8) * S::GROUP;
+              const int at_tok = tok + (y0 + y) * ROWS, c0 = ((2 * (c & 3)) ^ (at_tok & 7)) ^ turn, c1 = c0 ^ 1;
+              uint8_t* base = to + (at_tok >> 3) * S::GROUP + (at_tok & 7) * 128;
               *reinterpret_cast<uint4*>(base + c0 * 16) = turn ? hi : lo;
               *reinterpret_cast<uint4*>(base + c1 * 16) = turn ? lo : hi;
             }
           }
           fence_proxy_async_smem();
-          if (__any_sync(ALL, some) && lane == 0) *(volatile int*)&C.odd[k % ITEMS] = 1;
+          if (look && __any_sync(ALL, some) && lane == 0) *(volatile int*)&C.odd[k % ITEMS] = 1;
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&C.empty[st]);
-            mbar_arrive(&c_full[cv]);
+            mbar_arrive(&C.empty[raw.at]);
+            mbar_arrive(&c_full[cv.at]);
           }
         }
       } else {
         // values of tiles with new tokens
         int j = it.older / S::TN - it.t0;
         for (j = j < 0 ? 0 : j; j < n && ok; ++j) {
-          const int x = at + value_at(j, n), st = x % S::NR;
+          const int x = at + (j + 1 < n ? 2 * j + 2 : 2 * n - 1), st = x % S::NR;
           ok = wait(&C.new_full[news % 8], (news / 8) & 1);
           if (!ok) break;
           uint8_t* v = ring + st * S::RAW;
