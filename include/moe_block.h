@@ -423,8 +423,11 @@ MOE_API int moe_cache_tree(moe_cache_t *cache, const moe_cache_tree_t *tree, voi
  *   out[r][h] = sum_j softmax_j(scale * q[r][h] . k_j[g]) v_j[g]  * sigmoid(gate[r][h])       over the tokens j it sees.
  * A row that sees no token gives 0, rows of refused requests and of those left out too; rows past the last token are left
  * as they are. What a row does not see has no effect on it, infinities and NaN among them; what lies past a request's
- * end has none on any. Numbers as for moe_cache_attend; bf16 weights are rounded to bf16 unless the cache is e4m3. out
- * may be q or gate itself. Page ids outside the pool read as zeros and are reported. */
+ * end has none on any. A row whose scores are all -inf gives 0. Softmax statistics and sums are fp32; the weights of the
+ * second product are rounded to act_dtype, or to fp16 with an e4m3 cache (in fp16 weights below 2^-21 of the highest may
+ * lose bits and those below 2^-31 may count as none), the output once to act_dtype. bf16 queries over an e4m3 cache are
+ * multiplied in fp16, by a power of two of each row: elements 2^-28 below a row's largest lose bits. Sums are in an order
+ * that lengths and starts fix. out may be q or gate itself. Page ids outside the pool read as zeros and are reported. */
 typedef struct {
   moe_rows_t q, gate;                          /* [n_rows][n_heads][head_dim]; gate.p NULL: no gate */
   moe_rows_t out;                              /* written */
@@ -523,8 +526,8 @@ MOE_API int moe_debug_cache_check_new(const moe_cache_config_t *cfg, int max_new
 MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);
 
 /* Test control of the attention's bounded device waits: timeout_us = microseconds a wait for a copy may last before it
- * gives up (0 = the default, 500 ms); skip_copy = 1 leaves out the first copy of the next call's first CTA, so that the
- * wait for it runs out: the call ends with wrong outputs, which moe_cache_get_status reports. No fault is involved. */
+ * gives up (0 = the default, 500 ms); skip_copy = 1 leaves out the first copy of the first CTA of the next attend or
+ * attend_tree call, so that the wait for it runs out: the call ends with wrong outputs, which moe_cache_get_status reports. No fault is involved. */
 MOE_API int moe_cache_debug_set_wait(moe_cache_t *cache, uint32_t timeout_us, int skip_copy);
 
 /* Host-only check of a shape and of any of the three calls' arguments (each may be NULL): the status that
