@@ -461,16 +461,16 @@ MOE_API int moe_cache_attend_tree(moe_cache_t *cache, const moe_cache_attend_tre
  *     passes the pages that are free, that request and every later one that needs a page stay as they were.
  * A page belongs once to a table at most, and two requests that share a page both count in refs. Requests of a step that
  * ends them by moe_cache_plan give their pages back whatever refs holds: a request that shares pages ends here.
- * A count above n, a path that does not ascend or leaves the n new tokens, or n above max_new with a path: reported, the
- * request stays as it was. Page ids outside the pool are not given back, and their rows not moved; they are reported, as
- * are pages past the ring's room. lengths_out may be lengths, free_state_out may be free_state. */
+ * A count above n or path_stride, a path that does not ascend or leaves the n new tokens, or n above max_new with a path:
+ * reported, the request stays as it was. Page ids outside the pool are not given back, and their rows not moved; they are
+ * reported, as are pages past the ring's room. lengths_out may be lengths, free_state_out may be free_state. */
 typedef struct {
   const int32_t *counts;       /* [B] */
   const int32_t *lengths;      /* [B] */
   const int32_t *starts;       /* [B + 1], or NULL */
   const int32_t *slots;        /* [n_rows], or NULL */
-  const int32_t *path;         /* [B][path_stride], counts[b] of them in use, or NULL */
-  int64_t path_stride;         /* at least the largest count */
+  const int32_t *path;         /* [B][path_stride], the first counts[b] of each in use, or NULL */
+  int64_t path_stride;         /* a path's places */
   int32_t *tables;             /* [B][table_stride] */
   int64_t table_stride;
   int32_t *free_pages;         /* [n_pages] */

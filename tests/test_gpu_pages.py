@@ -176,6 +176,25 @@ def test_keep_reports_what_cannot_be_and_leaves_it(change):
     assert c.status() == (0, 0)
 
 
+def test_keep_reports_a_count_above_the_paths_places():
+    """What lies behind a request's path is not read: another request's path, or nothing that is the call's."""
+    torch = torch_()
+    rng = np.random.default_rng(8)
+    lengths, starts = np.array([40, 30, 50]), np.array([0, 8, 13, 21])
+    tables, ring, state, refs, n_pages = tables_for(rng, lengths, 16, 4)
+    c = lib.PagedCache(1, 1, 64, 16, n_pages, 3, tables.shape[1], max_new=8)
+    pools = [pool_bits(torch, (n_pages, 1, 16, 64), "f16", gen_of(3))]
+    before = bits(pools[0]).copy()
+    counts, path = np.array([3, 2, 5]), np.array([[0, 1], [2, 3], [4, 5]])
+    got = run_keep(c, c.pools(pools), counts, lengths, tables, ring, state, starts, np.zeros(21, np.int32), path, refs)
+    assert list(got[0]) == [40, 27, 50]
+    assert got[2][[0, 2]].tolist() == tables[[0, 2]].tolist()
+    for b in (0, 2):
+        used = tables[b, :-(-lengths[b] // 16)]
+        np.testing.assert_array_equal(bits(pools[0])[used], before[used])
+    assert c.status() == (-1, 16)
+
+
 def test_keep_page_ids_outside_the_pool_and_a_full_ring():
     torch = torch_()
     rng = np.random.default_rng(6)

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(THREADS) k_cache_keep(const __grid_constant__ 
     if (!out && count >= 0) {
       bool good = count <= n;
       if (good && k.path) {
-        good = n <= a.most;
+        good = n <= a.most && count <= k.path_stride;
         const int32_t* path = k.path + (size_t)b * k.path_stride;
         int before = -1;
         for (int i0 = 0; good && i0 < count; i0 += 32) {
