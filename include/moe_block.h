@@ -478,7 +478,7 @@ typedef struct {
   int32_t *free_state_out;     /* [3]: the new head and count, and the number of requests that stayed for want of pages */
   int32_t *lengths_out;        /* [B] */
   int32_t *refs;               /* [n_pages], or NULL */
-  void *const *pools;          /* [n_pools], host memory: k_cache and v_cache of every layer */
+  void *const *pools;          /* [n_pools], host memory: k_cache and v_cache of every layer, each once */
   const int64_t *page_strides; /* [n_pools], host memory */
   int64_t n_pools;             /* 0..1024 */
   int64_t n_requests, n_rows;  /* B: 0..max_requests; n_rows: 0..2^24 */
@@ -502,7 +502,7 @@ typedef struct {
   const int32_t *free_state;   /* [3] */
   int32_t *free_state_out;     /* [3]: the new head and count, and the number of entries refused */
   int32_t *refs;               /* [n_pages] */
-  void *const *pools;          /* [n_pools], host memory: k_cache and v_cache of every layer */
+  void *const *pools;          /* [n_pools], host memory: k_cache and v_cache of every layer, each once */
   const int64_t *page_strides; /* [n_pools], host memory */
   int64_t n_pools;             /* 0..1024 */
   int64_t n_entries;           /* 0..max_requests */

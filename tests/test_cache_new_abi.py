@@ -86,11 +86,19 @@ def test_fork_refuses(L, change):
 
 def test_pools_are_checked_each(L):
     for bad, want in ((P, 0), (P + 8, -1), (0, -1)):
-        pools, strides = (ctypes.c_void_p * 3)(P, bad, P), (ctypes.c_int64 * 3)(DENSE, DENSE, DENSE)
+        pools, strides = (ctypes.c_void_p * 3)(P + 4096, bad, P + 8192), (ctypes.c_int64 * 3)(DENSE, DENSE, DENSE)
         at = dict(pools=ctypes.addressof(pools), strides=ctypes.addressof(strides), n_pools=3)
         assert status(L, keep=at) == want and status(L, fork=at) == want
         strides[2] = DENSE - 64
         assert status(L, keep=at) == -1 and status(L, fork=at) == -1
+
+
+def test_a_pool_named_twice_is_refused(L):
+    for at in ((P, P), (P, P + 16, P), (P + 16, P, P + 32, P)):
+        n = len(at)
+        pools, strides = (ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*([DENSE] * n))
+        a = dict(pools=ctypes.addressof(pools), strides=ctypes.addressof(strides), n_pools=n)
+        assert status(L, keep=a) == -1 and status(L, fork=a) == -1
 
 
 def test_null_handles(L):

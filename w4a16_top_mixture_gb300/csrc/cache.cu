@@ -130,6 +130,10 @@ bool pools_ok(const CacheShape& S, void* const* pools, const int64_t* strides, i
   if (n < 0 || n > 1024 || (n > 0 && (!pools || !strides))) return false;
   for (int64_t i = 0; i < n; ++i)
     if (!pool_ok(S, pools[i], strides[i])) return false;
+  // rows that move in a pool named twice would move twice; a model's few pools are compared in a microsecond or two
+  for (int64_t i = 1; i < n; ++i)
+    for (int64_t j = 0; j < i; ++j)
+      if (pools[i] == pools[j]) return false;
   return true;
 }
 int check_tree(const moe_cache_config_t& cfg, const moe_cache_tree_t& t) {

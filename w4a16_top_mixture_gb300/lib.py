@@ -616,7 +616,7 @@ class PagedCache:
         return out
 
     def pools(self, tensors):
-        """The pools of all layers, keys and values, for keep and fork: made once, when the pools are."""
+        """The pools of all layers, keys and values, each once, for keep and fork: made once, when the pools are."""
         return CachePools(self, tensors)
 
     def _masks(self, t, rows):
