@@ -522,12 +522,14 @@ MOE_API int moe_debug_cache_check_new(const moe_cache_config_t *cfg, int max_new
  * are wrong, and later such calls leave theirs unwritten until this call has reported it) or MOE_ERR_INVALID_ARG (a call met a
  * value on the device that it could not use), and clears what it reported. *flags (may be NULL) receives the raw bits:
  * 1 a wait ran out, 2 a length, 4 a page id or slot, 8 a free_state out of range or more pages than the ring has room
- * for, 16 starts, a parent, a count, a path or an entry that cannot be. Not while a stream is being captured: a wait for the device ends the capture with an error. */
+ * for, 16 starts, a parent, a count, a path or an entry that cannot be. Not while a stream is being captured: a wait for
+ * the device ends the capture with an error. */
 MOE_API int moe_cache_get_status(moe_cache_t *cache, uint32_t *flags);
 
 /* Test control of the attention's bounded device waits: timeout_us = microseconds a wait for a copy may last before it
  * gives up (0 = the default, 500 ms); skip_copy = 1 leaves out the first copy of the first CTA of the next attend or
- * attend_tree call, so that the wait for it runs out: the call ends with wrong outputs, which moe_cache_get_status reports. No fault is involved. */
+ * attend_tree call, so that the wait for it runs out: the call ends with wrong outputs, which moe_cache_get_status
+ * reports. No fault is involved. */
 MOE_API int moe_cache_debug_set_wait(moe_cache_t *cache, uint32_t timeout_us, int skip_copy);
 
 /* Host-only check of a shape and of any of the three calls' arguments (each may be NULL): the status that

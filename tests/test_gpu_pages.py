@@ -320,3 +320,65 @@ def test_many_pools_with_page_strides():
     compare(run_keep(c, c.pools(pools), counts, lengths, tables, ring, state, starts, None, path), want)
     for p, w in zip(pools, want[5]):
         np.testing.assert_array_equal(bits(p.contiguous()), w)
+
+
+def test_keep_and_fork_replayed_from_a_graph_and_on_another_stream():
+    """A step's keep and the forks after it, in place: eager, on another stream, and from a graph with other counts and paths
+    in the same tensors."""
+    torch = torch_()
+    rng = np.random.default_rng(12)
+    B, page = 40, 16
+    new = rng.integers(1, 20, B)
+    lengths = rng.integers(0, 200, B) + new
+    starts = np.concatenate([[0], np.cumsum(new)])
+    tables, ring, state, refs, n_pages = tables_for(rng, lengths, page, 200, [(0, 1, 1), (2, 3, 1)])
+    wide = np.full((B, 20), -5, np.int32)
+    wide[:, :tables.shape[1]] = tables
+    c = lib.PagedCache(2, 2, 64, page, n_pages, B, 20, max_new=20)
+    first = [pool_bits(torch, (n_pages, 2, page, 64), "f16", gen_of(4)) for _ in range(3)]
+    start = [ints(x) for x in (lengths, state, wide, ring, refs)]
+    counts, path = ints(np.zeros(B)), ints(np.zeros((B, 20)))
+    src, dst, st = ints([0, 2, 2]), ints([5, 7, 6]), ints(starts)
+
+    def choose():
+        k = np.minimum(new, rng.integers(0, 20, B))
+        k[[5, 6, 7]] = -1
+        counts.copy_(ints(k))
+        path.copy_(ints(paths(rng, new, k, 20)))
+
+    now, pools = [x.clone() for x in start], [p.clone() for p in first]
+    at = c.pools(pools)
+
+    def step(stream=None):
+        ln, fs, tb, rg, rf = now
+        both = lib.CacheState(ln, fs)
+        c.keep(counts, ln, tb, rg, fs, at, starts=st, path=path, refs=rf, out=both, stream=stream)
+        c.fork(src, dst, ln, tb, rg, fs, rf, at, out=both, stream=stream)
+
+    def run(f):
+        for a, b in zip(now + pools, start + first):
+            a.copy_(b)
+        torch.cuda.synchronize()
+        f()
+        torch.cuda.synchronize()
+        return [x.cpu().numpy() for x in now] + [bits(p).copy() for p in pools]
+
+    choose()
+    k = counts.cpu().numpy()
+    kept = O.keep(k, lengths, starts, [False] * B, path.cpu().numpy(), wide, ring, state, refs, [bits(p) for p in first], page, n_pages)
+    want = O.fork(src.cpu().numpy(), dst.cpu().numpy(), kept[0], kept[2], kept[3], kept[1], kept[4], kept[5], page, n_pages)
+    got = run(step)
+    compare(got[:5], want)
+    for p, w in zip(got[5:], want[5]):
+        np.testing.assert_array_equal(p, w)
+    side = torch.cuda.Stream()
+    for a, b in zip(run(lambda: step(side)), got):
+        np.testing.assert_array_equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        choose()
+        for a, b in zip(run(graph.replay), run(step)):
+            np.testing.assert_array_equal(a, b)
+    assert c.status() == (0, 0)

@@ -86,7 +86,8 @@ struct Item {
 
 struct Control {
   // new_full, fixed: of the tiles that are looked through, or (c_full, c_empty) of the converted ones
-  uint64_t full[12], empty[12], new_full[8], fixed[8], s_full[2], p_ready[2], pv_done, q_ready, q_free, o_free, o_full, drained, pair[4][2], soft;
+  uint64_t full[12], empty[12], new_full[8], fixed[8], s_full[2], p_ready[2], pv_done, q_ready, q_free, o_free, o_full,
+      drained, pair[4][2], soft;
   uint64_t item_full[ITEMS], item_empty[ITEMS];
   long long sums[THREADS / 32];
   int longest[THREADS / 32];
@@ -415,7 +416,8 @@ __device__ __forceinline__ void emit(const float (&y)[32], float l, float vs, ui
   FourRows(out, lane).store(z, x);
 }
 
-// By whole warps, and in line: a call would spill what is live. A wait that runs out ends the CTA's work: everyone gives up at the next wait.
+// By whole warps, and in line: a call would spill what is live. A wait that runs out ends its role's work, and so, as what
+// it would have given is waited for, the CTA's.
 __device__ __forceinline__ bool wait_for(const TreeArgs& A, Control& C, uint64_t* bar, uint32_t parity) {
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer();
