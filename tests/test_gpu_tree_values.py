@@ -1,0 +1,144 @@
+"""Values that are not finite, or large, in the attention of several new tokens: in items that are split over CTAs, in rows that
+see nothing, at the ends of the types' ranges, and the time that a call takes over them.
+
+The reference is the formula in float64 on the GPU, a request at a time; its bound is that of test_gpu_tree.py."""
+import pytest
+
+from test_gpu_cache import U, ints, torch_
+from test_gpu_tree import tree_case
+from w4a16_top_mixture_gb300 import build, lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    lib.load_library()
+
+
+def cache_of(d, n_pages, width, Hq, Hkv, D, page, act, cache, most):
+    return lib.PagedCache(Hq, Hkv, D, page, n_pages, len(d["lengths"]), width, dtype=act, cache_dtype=cache, max_new=most)
+
+
+def reference(d, page, scale):
+    """(out, size, mag, seen) of the rows of all requests: the masked softmax in float64, where a weight of a value that a row
+    does not see is no product at all. Of values that are not finite a row gets their sum, whatever their weights."""
+    torch = torch_()
+    q = d["q"].double()
+    rows, Hq, D = q.shape
+    k_pool, v_pool = d["k_cache"].double(), d["v_cache"].double()
+    Hkv = k_pool.shape[1]
+    out, size = torch.zeros_like(q), torch.zeros_like(q)
+    mag, seen = torch.zeros(rows, Hq, 1, device="cuda").double(), torch.zeros(rows, 1, 1, device="cuda").double()
+    starts = d["starts"].tolist()
+    for b, n in enumerate(d["lengths"].tolist()):
+        lo, hi = starts[b], starts[b + 1]
+        m, pos = hi - lo, torch.arange(n, device="cuda")
+        if m == 0 or ("slots" in d and int(d["slots"][lo]) < 0):
+            continue
+        new = torch.arange(m, device="cuda")
+        sees = torch.ones(m, n, dtype=torch.bool, device="cuda")
+        sees[:, n - m:] = (d["masks"][lo:hi][:, new // 64] >> (new % 64) & 1).bool() if "masks" in d else new[:, None] >= new
+        seen[lo:hi, 0, 0] = sees.sum(1).double()
+        pages = d["tables"][b].long()[pos // page]
+        k, v = k_pool[pages, :, pos % page], v_pool[pages, :, pos % page]          # [n, Hkv, D]
+        if "k_scale" in d:
+            k, v = k * d["k_scale"].double()[:, None], v * d["v_scale"].double()[:, None]
+        s = torch.zeros(m, Hq, n, device="cuda").double()
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            s[:, h] = q[lo:hi, h] @ k[:, g].T * scale
+            mag[lo:hi, h, 0] = torch.where(sees, q[lo:hi, h].abs() @ k[:, g].abs().T, 0.0).amax(1) * abs(scale)
+            p = torch.softmax(s[:, h].masked_fill(~sees, -float("inf")), 1)
+            p = torch.where(sees.any(1, keepdim=True), p, 0.0)
+            fine = torch.where(v[:, g].isfinite(), v[:, g], 0.0)
+            y, z = p @ fine, p @ fine.abs()
+            of = lambda what: sees.double() @ what.double() > 0                    # noqa: E731
+            up, down, none = of(v[:, g] == float("inf")), of(v[:, g] == -float("inf")), of(v[:, g].isnan())
+            y = torch.where(up, float("inf"), torch.where(down, -float("inf"), y))
+            out[lo:hi, h], size[lo:hi, h] = torch.where(none | (up & down), float("nan"), y), z
+    if "gate" in d:
+        sg = torch.sigmoid(d["gate"].double())
+        out, size = torch.where(seen > 0, out * sg, 0.0), size * sg
+    return out, size, mag, seen
+
+
+def check(d, got, page, act, cache, scale=None):
+    torch = torch_()
+    rows, D = int(d["starts"][-1]), d["q"].shape[2]
+    want, size, mag, seen = (t[:rows] for t in reference(d, page, D ** -0.5 if scale is None else scale))
+    got = got[:rows].double()
+    up = U["f16"] if cache == "e4m3" else U[act]
+    tol = U[act] * want.abs() + size * (up + 2 * D * 2.0 ** -23 * mag + 2.0 ** -21 * mag + (seen / 16 + 232) * 2.0 ** -23) + 2.0 ** -24
+    ok = want.isfinite()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert (got[want.isinf()] == want[want.isinf()]).all()
+    bad = ((got - want).abs() > tol) & ok
+    assert not bad.any(), (bad.nonzero()[:4], (got - want).abs()[bad][:4], tol[bad][:4])
+    return want
+
+
+def spoil(d, b, older, page, where):
+    """where: (new token, element, value) for request b's values, key-value head 0."""
+    for j, x, value in where:
+        at = older + j
+        d["v_cache"][int(d["tables"][b, at // page]), 0, at % page, x] = value
+
+
+INF = float("inf")
+ODD = [(2, 256, 16, "f16", "f16"), (2, 64, 32, "f16", "e4m3"), (2, 128, 64, "bf16", "bf16"), (2, 256, 16, "bf16", "e4m3"),
+       (4, 64, 16, "bf16", "bf16"), (2, 128, 16, "f16", "e4m3")]
+
+
+@pytest.mark.parametrize("masks", ["tree", None])
+@pytest.mark.parametrize("Hq,D,page,act,cache", ODD)
+@pytest.mark.parametrize("reqs", [[(6000, 150, 0)], [(30000, 150, 0)], [(2000 + 77 * i, 150 - i, 0) for i in range(9)]],
+                         ids=["parts of a few tiles", "groups of parts", "two or three parts"])
+def test_values_that_are_not_finite_in_items_of_several_parts(reqs, Hq, D, page, act, cache, masks):
+    """New tokens with NaN or infinities lie in two to four tiles, so on either side of a border between CTAs in some item."""
+    torch = torch_()
+    d, n_pages, width = tree_case(reqs, Hq, 1, D, page, act, cache, D + len(reqs), len(reqs) > 1, masks, 3)
+    nan = [float("nan")]
+    for b, (older, n, _) in enumerate(reqs):
+        few = [(0, 5, nan[0]), (n // 2, 9, nan[0]), (n - 1, 7, nan[0]), (n - 1, D - 1, nan[0])]
+        if cache != "e4m3":
+            few += [(1, 11, INF), (63, 12, -INF), (64, 13, INF), (n - 2, 13, -INF), (n - 1, 14, INF), (n - 3, 14, INF)]
+        spoil(d, b, older, page, few if b % 2 == 0 else few[2:])
+    c = cache_of(d, n_pages, width, Hq, 1, D, page, act, cache, 150)
+    out = c.attend_tree(**d)
+    assert c.status() == (0, 0)
+    want = check(d, out, page, act, cache)
+    assert not want.isfinite().all() and want.isfinite().any()
+    assert torch.equal(c.attend_tree(**d).view(torch.int16), out.view(torch.int16))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,act,cache", [(16, 2, 256, 16, "f16", "f16"), (32, 8, 128, 64, "bf16", "bf16"), (8, 2, 64, 16, "f16", "e4m3")])
+@pytest.mark.parametrize("masks", ["tree", None])
+@pytest.mark.parametrize("kind", ["one", "all NaN", "all infinite"])
+def test_values_that_are_not_finite_do_not_hold_up_the_others(Hq, Hkv, D, page, act, cache, masks, kind):
+    """One request of a batch of chunks has them. No wait of the call comes near 2 ms, and the other requests get the same bytes."""
+    torch = torch_()
+    if cache == "e4m3" and kind == "all infinite":
+        pytest.skip("e4m3 has no infinities")
+    reqs = [(250 * i, 256, 0) for i in range(12)]
+    d, n_pages, width = tree_case(reqs, Hq, Hkv, D, page, act, cache, 3, False, masks, 4)
+    c = cache_of(d, n_pages, width, Hq, Hkv, D, page, act, cache, 256)
+    base = c.attend_tree(**d)
+    older, at = reqs[5][0], d["tables"][5].long()
+    if kind == "one":
+        spoil(d, 5, older, page, [(0, 3, float("nan") if cache == "e4m3" else INF)])
+    else:
+        pos = torch.arange(older, older + 256, device="cuda")
+        d["v_cache"][at[pos // page], :, pos % page] = torch.tensor(float("nan") if kind == "all NaN" else INF, device="cuda").to(d["v_cache"].dtype)
+    c.set_wait(timeout_us=2000)
+    out = c.attend_tree(**d)
+    assert c.status() == (0, 0)
+    s = d["starts"].tolist()
+    assert torch.equal(out[:s[5]], base[:s[5]]) and torch.equal(out[s[6]:], base[s[6]:])
+    one = {**d, "q": d["q"][s[5]:s[6]], "starts": ints([0, 256]), "tables": d["tables"][5:6], "lengths": d["lengths"][5:6],
+           "slots": d["slots"][s[5]:s[6]]}
+    if masks:
+        one["masks"] = d["masks"][s[5]:s[6]]
+    want = check(one, out[s[5]:s[6]], page, act, cache)
+    assert not want.isfinite().all()

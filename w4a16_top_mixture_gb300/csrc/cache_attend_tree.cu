@@ -89,12 +89,16 @@ struct Control {
   uint64_t full[12], empty[12], new_full[8], fixed[8], s_full[2], p_ready[2], pv_done, q_ready, q_free, o_free, o_full,
       drained, pair[4][2], soft;
   uint64_t item_full[ITEMS], item_empty[ITEMS];
-  long long sums[THREADS / 32];
-  int longest[THREADS / 32];
   Item items[ITEMS];
-  int odd[ITEMS];            // values that are not finite were taken out
+  uint4 odd[ITEMS][CACHE_MAX_NEW / 128];   // bits of the new tokens whose values were not finite, in this CTA's tiles
   int last;                  // this CTA's part is the last to arrive
-  float top[2][2][M];        // maxima of the halves of a row's tokens in a tile; their sums at an item's end
+  union {
+    struct {                 // of the warps' requests, read before the first item is given out
+      long long sums[THREADS / 32];
+      int longest[THREADS / 32];
+    };
+    float top[2][2][M];      // maxima of the halves of a row's tokens in a tile; their sums at an item's end
+  };
   uint32_t tmem;
   int abort;
 };
@@ -156,6 +160,18 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                  "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
+               : "memory");
+}
+// 8 columns, valid on return; stored without a wait
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 // a shared-memory descriptor of blocks in the 128-byte swizzle: bytes between blocks along the other dimension of the
@@ -297,42 +313,62 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
   return v;
 }
 
-// What was taken out of the values of new tokens is added to the rows that see it: HD elements of O from x on, at `o`.
+// What was taken out of the values of new tokens is added to the rows that see it: half of O's elements from x on, at `o`.
+// Of the noted tokens 32 are looked at together, a lane's each and 8 elements at a time: whether a row gets an infinity or a
+// NaN is a vote over the lanes and the row's mask, however many tokens hold one. 24 chunks of 256 tokens, 16 over 2 heads of
+// 256, 307 us: 331 where one value of one request is infinite, 556 where all of its new ones are NaN, 622 infinite (an element
+// of a token after the other: 64 to 69 ms).
 template <class S>
-__device__ __forceinline__ void add_odd(const TreeArgs& A, const Item& it, int t, int x, uint32_t o) {
+__device__ __forceinline__ void add_odd(const TreeArgs& A, const Item& it, const uint4* odd, int t, int x, uint32_t o) {
   const moe_cache_attend_tree_t& a = A.a;
-  const int i = (it.m0 + t) / A.group;
-  auto sees = [&](int j) {
-    return t < it.rows && (a.masks ? __ldcg((const unsigned long long*)a.masks + (size_t)(it.lo + i) * a.mask_words + (j >> 6)) >> (j & 63) & 1
-                                   : j <= i);
-  };
-  const int ps = 1 << A.page_log2;
-  const int from = max(it.older, it.t0 * S::TN), upto = (int)min((int64_t)it.len, (int64_t)it.t1 * S::TN);
+  const unsigned ALL = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31, i = (it.m0 + t) / A.group, ps = 1 << A.page_log2;
 #pragma unroll 1
-  for (int c = 0; c < S::D / 2; ++c) {              // seldom called: an element at a time, with few registers
-    uint32_t r;
-    __syncwarp();
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(o + c) : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r) : : "memory");
-#pragma unroll 1
-    for (int p = from; p < upto; ++p) {
-      const int j = p - it.older, page = __ldcg(a.tables + (size_t)it.b * a.table_stride + (p >> A.page_log2));
-      if (page < 0 || page >= A.n_pages || !sees(j)) continue;
-      const int64_t at = page * a.v_page_stride + ((int64_t)it.g * ps + (p & (ps - 1))) * S::D + x + c;
-      float v;
-      if (S::E4M3) {
-        uint32_t lo, hi;
-        e4m3x4_to_f16x4(__ldcg((const uint8_t*)a.v_cache + at), lo, hi);
-        v = unpack2<false>(lo).x;
-      } else {
-        v = unpack2<S::BF16>(__ldcg((const unsigned short*)a.v_cache + at)).x;
-      }
-      if (!(fabsf(v) <= 3.4028234663852886e38f)) r = __float_as_uint(__uint_as_float(r) + v);
+  for (int k = 0; k < CACHE_MAX_NEW / 32; ++k) {
+    const uint32_t noted = *(volatile const uint32_t*)(reinterpret_cast<const uint32_t*>(odd) + k);
+    if (!noted) continue;
+    const bool own = noted >> lane & 1;
+    const int p = it.older + (own ? 32 * k + lane : 0);
+    const int page = own ? __ldcg(a.tables + (size_t)it.b * a.table_stride + (p >> A.page_log2)) : -1;
+    const bool mine = page >= 0 && page < A.n_pages;
+    const int64_t at = (mine ? page : 0) * a.v_page_stride + ((int64_t)it.g * ps + (p & (ps - 1))) * S::D + x;
+    uint32_t sees = 0;                              // of these tokens, by the lane's row
+    if (t < it.rows) {
+      if (a.masks) sees = __ldcg(reinterpret_cast<const uint32_t*>(a.masks + (size_t)(it.lo + i) * a.mask_words) + k);
+      else sees = i < 32 * k ? 0u : i >= 32 * k + 31 ? ~0u : (2u << (i & 31)) - 1;
     }
-    __syncwarp();
-    tmem_st1(o + c, r);
+#pragma unroll 1
+    for (int c = 0; c < S::D / 2; c += 8) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (mine && !S::E4M3) v = __ldcg(reinterpret_cast<const uint4*>((const uint16_t*)a.v_cache + at + c));
+      if (mine && S::E4M3) {
+        const uint2 w = __ldcg(reinterpret_cast<const uint2*>((const uint8_t*)a.v_cache + at + c));
+        e4m3x4_to_f16x4(w.x, v.x, v.y);
+        e4m3x4_to_f16x4(w.y, v.z, v.w);
+      }
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t r[8];
+      __syncwarp();
+      tmem_ld8(o + c, r);
+      bool nan = true;                              // in all rows: they stay so
+#pragma unroll
+      for (int e = 0; e < 8; ++e) nan = nan && (r[e] & 0x7FFFFFFFu) > 0x7F800000u;
+      if (__all_sync(ALL, nan || t >= it.rows)) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 f = unpack2<S::BF16 && !S::E4M3>(w[e / 2]);
+        const float y = e & 1 ? f.y : f.x;
+        const bool up = !S::E4M3 && __ballot_sync(ALL, y == INFINITY) & sees;    // e4m3 has no infinities
+        const bool down = !S::E4M3 && __ballot_sync(ALL, y == -INFINITY) & sees;
+        if (up) r[e] = __float_as_uint(__uint_as_float(r[e]) + INFINITY);
+        if (down) r[e] = __float_as_uint(__uint_as_float(r[e]) - INFINITY);
+        if (__ballot_sync(ALL, y != y) & sees) r[e] = 0x7FFFFFFFu;
+      }
+      __syncwarp();
+      tmem_st8(o + c, r);
+    }
+    tmem_wait_st();                                 // before these columns are read again
   }
-  tmem_wait_st();
 }
 
 // The sum of parts p0, p0 + by .. below p1 of a row, on their highest base, in the order of the parts.
@@ -460,7 +496,11 @@ __device__ __forceinline__ bool finish_item(const TreeArgs& A, Control& C, int s
     const int m = it.m0 + t, i = m / A.group;
     return t < it.rows ? rows_at(r, it.lo + i, it.g * A.group + m - i * A.group) : nullptr;
   };
-  if (n && *(volatile int*)&C.odd[slot]) add_odd<S>(A, it, t, half * HD, lanes + S::O + half * HD);
+  if (n) {
+    const uint4 *odd = C.odd[slot], b0 = odd[0], b1 = odd[1];
+    if (__builtin_expect(b0.x | b0.y | b0.z | b0.w | b1.x | b1.y | b1.z | b1.w, 0))
+      add_odd<S>(A, it, odd, t, half * HD, lanes + S::O + half * HD);
+  }
   if (parts == 1) {
     uint16_t *out = row_of(a.out, t), *gate = gated ? row_of(a.gate, t) : nullptr;
     if (t - lane < it.rows)                         // the warp has rows
@@ -726,6 +766,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int t0 = min((int)(u - first), q.tiles), t1 = (int)min((long long)q.tiles, end - first);
         if (q.tiles ? t0 < t1 : u == first) {
           if (!wait(&C.item_empty[k % ITEMS], ((k / ITEMS) & 1) ^ 1)) break;
+          if (lane < CACHE_MAX_NEW / 128) C.odd[k % ITEMS][lane] = make_uint4(0, 0, 0, 0);
+          __syncwarp();
           if (lane == 0) {
             Item it;
             it.b = base + l;
@@ -741,7 +783,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             it.c0 = t0 == 0 ? cta : (int)quotient(first, share);
             it.c1 = t1 == q.tiles ? cta : (int)quotient(first + q.tiles - 1, share);
             C.items[k % ITEMS] = it;
-            C.odd[k % ITEMS] = 0;
             mbar_arrive(&C.item_full[k % ITEMS]);
           }
           ++k;
@@ -987,7 +1028,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&C.q_ready);
         ++items;
       }
-      bool some = false;                            // values that are not finite
+      // a new token whose values are not finite
+      auto note = [&](int j) { atomicOr(reinterpret_cast<uint32_t*>(C.odd[k % ITEMS]) + (j >> 5), 1u << (j & 31)); };
       if (S::E4M3) {
         // every tile, in the order of the stages; an item has an even number of them
         for (int x = wq >> 1; x < 2 * n && ok; x += 2, raw.next(2), cv.next(2)) {
@@ -1005,25 +1047,30 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int turn = c >> 2 & 1;
           const int tok0 = (it.t0 + j) * S::TN, left = it.len - tok0, fresh = it.older - tok0;
           const bool look = !key && fresh < S::TN;
+          // What is looked through is mended in the raw tile, a thread's own vectors before it converts them: within the
+          // conversion the code of it cost every tile (128 requests over e4m3 caches 132 us, 165 so).
+          if (look) {
+            const int y1 = fresh > tok ? (fresh - tok + ROWS - 1) / ROWS : 0;
+#pragma unroll 1
+            for (int y = y1; y < STEPS; ++y) {
+              const int at_tok = tok + y * ROWS;
+              uint4* at_raw = reinterpret_cast<uint4*>(const_cast<uint8_t*>(from) + y * 1024);
+              const uint4 w = *at_raw;
+              const uint4 nan = make_uint4(__vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
+                                           __vcmpeq4(w.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu), __vcmpeq4(w.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu));
+              if (at_tok >= left) {
+                *at_raw = make_uint4(0, 0, 0, 0);
+              } else if (nan.x | nan.y | nan.z | nan.w) {
+                note(at_tok - fresh);
+                *at_raw = make_uint4(w.x & ~nan.x, w.y & ~nan.y, w.z & ~nan.z, w.w & ~nan.w);
+              }
+            }
+          }
 #pragma unroll
           for (int y0 = 0; y0 < STEPS; y0 += 4) {
             uint4 v[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4*>(from + (y0 + y) * 1024);
-            if (look)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int at_tok = tok + (y0 + y) * ROWS;
-                uint32_t w[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-                if (at_tok >= fresh)
-#pragma unroll
-                  for (int z = 0; z < 4; ++z) {
-                    const uint32_t nan = __vcmpeq4(w[z] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                    some = some || (nan && at_tok < left);
-                    w[z] = at_tok < left ? w[z] & ~nan : 0u;
-                  }
-                v[y] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               uint4 lo, hi;
@@ -1038,7 +1085,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           fence_proxy_async_smem();
-          if (look && __any_sync(ALL, some) && lane == 0) *(volatile int*)&C.odd[k % ITEMS] = 1;
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&C.empty[raw.at]);
@@ -1071,16 +1117,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             over |= ((w.x & EXP) + ONE) | ((w.y & EXP) + ONE) | ((w.z & EXP) + ONE) | ((w.w & EXP) + ONE);
           }
           if (over & 0x80008000u) {
-            some = true;
             for (int e = fresh * VR + t; e < e1; e += 128) {
               const uint4 w = *at_vector(e);
-              *at_vector(e) = make_uint4(finite2<S::BF16>(w.x), finite2<S::BF16>(w.y), finite2<S::BF16>(w.z),
+              const uint4 f = make_uint4(finite2<S::BF16>(w.x), finite2<S::BF16>(w.y), finite2<S::BF16>(w.z),
                                          finite2<S::BF16>(w.w));
+              if ((w.x ^ f.x) | (w.y ^ f.y) | (w.z ^ f.z) | (w.w ^ f.w)) {
+                note(tok0 + e / VR - it.older);
+                *at_vector(e) = f;
+              }
             }
           }
           for (int e = max(fresh, left) * VR + t; e < rows * VR; e += 128) *at_vector(e) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
-          if (__any_sync(ALL, some) && lane == 0) *(volatile int*)&C.odd[k % ITEMS] = 1;
           __syncwarp();
           if (lane == 0) mbar_arrive(&C.fixed[news % 8]);
           ++news;
