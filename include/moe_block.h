@@ -421,9 +421,9 @@ MOE_API int moe_cache_tree(moe_cache_t *cache, const moe_cache_tree_t *tree, voi
  * there): row r, new token i of its request, sees the P older tokens and those new tokens j whose bit j is set in its
  * mask; without masks those with j <= i, a chain. With g the key-value head of query head h,
  *   out[r][h] = sum_j softmax_j(scale * q[r][h] . k_j[g]) v_j[g]  * sigmoid(gate[r][h])       over the tokens j it sees.
- * A row that sees no token gives 0, rows of refused requests and of those left out too; rows past the last token are left
- * as they are. What a row does not see has no effect on it, infinities and NaN among them; what lies past a request's
- * end has none on any. A row whose scores are all -inf gives 0. Softmax statistics and sums are fp32; the weights of the
+ * A row that sees no token gives 0 whatever its gate holds, rows of refused requests and of those left out too; rows past the
+ * last token are left as they are. What a row does not see has no effect on it, infinities and NaN among them; what lies past
+ * a request's end has none on any. A row whose scores are all -inf gives 0, whatever its values and gate. Softmax statistics and sums are fp32; the weights of the
  * second product are rounded to act_dtype, or to fp16 with an e4m3 cache (in fp16 weights below 2^-21 of the highest may
  * lose bits and those below 2^-31 may count as none), the output once to act_dtype. bf16 queries over an e4m3 cache are
  * multiplied in fp16, by a power of two of each row: elements 2^-28 below a row's largest lose bits. Sums are in an order

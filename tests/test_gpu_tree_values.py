@@ -142,3 +142,46 @@ def test_values_that_are_not_finite_do_not_hold_up_the_others(Hq, Hkv, D, page, 
         one["masks"] = d["masks"][s[5]:s[6]]
     want = check(one, out[s[5]:s[6]], page, act, cache)
     assert not want.isfinite().all()
+
+
+@pytest.mark.parametrize("Hq,D,page,act,cache", ODD[:4])
+@pytest.mark.parametrize("reqs", [[(37, 6, 1), (0, 20, 0), (90, 4, 0)], [(0, 256, 0)]], ids=["short", "several parts"])
+def test_rows_that_see_nothing_give_zero_whatever_their_gate(reqs, Hq, D, page, act, cache):
+    """0 without a token, not 0 times the gate's sigmoid: rows of refused and of left-out requests, and rows whose masks are empty
+    in requests without older tokens, under gates that are NaN."""
+    torch = torch_()
+    d, n_pages, width = tree_case(reqs, Hq, 1, D, page, act, cache, D, True, "any", 4, 2)
+    c = cache_of(d, n_pages, width, Hq, 1, D, page, act, cache, 256)
+    base = c.attend_tree(**d)
+    rows = int(d["starts"][-1])
+    empty = (reference(d, page, 1.0)[3] == 0).view(-1)
+    assert empty[:rows].any() and not empty[:rows].all()
+    d["gate"] = torch.where(empty[:, None, None], float("nan"), d["gate"].float()).to(d["gate"].dtype)
+    got = c.attend_tree(**d)
+    assert c.status() == (0, 0)
+    assert torch.equal(got[:rows], base[:rows]) and (got[:rows][empty[:rows]] == 0).all()
+    d["lengths"][len(reqs) - 1] = 1                            # fewer than its new ones: left out
+    d["gate"].fill_(float("nan"))
+    got = c.attend_tree(**d)
+    assert c.status() == (-1, 2)
+    assert (got[int(d["starts"][-2]):rows] == 0).all()
+
+
+@pytest.mark.parametrize("older", [30, 3000])
+@pytest.mark.parametrize("Hq,D,page,act,cache", [ODD[0], ODD[2], ODD[4]])
+def test_rows_whose_scores_are_all_minus_infinity_give_zero(older, Hq, D, page, act, cache):
+    """Whatever their values and gates; rows of another request in the batch, and of other heads, are as they were."""
+    torch = torch_()
+    d, n_pages, width = tree_case([(older, 5, 0), (60, 3, 0)], 2 * Hq, 2, D, page, act, cache, 7, True, "tree", 1)
+    d["q"][..., 0] = 1.0
+    c = lib.PagedCache(2 * Hq, 2, D, page, n_pages, 2, width, dtype=act, cache_dtype=cache, max_new=5)
+    base = c.attend_tree(**d)
+    pos = torch.arange(older + 5, device="cuda")
+    pages = d["tables"][0].long()[pos // page]
+    d["k_cache"][pages, 0, pos % page, 0] = -INF
+    d["v_cache"][pages[:7], 0, pos[:7] % page, 4] = INF
+    d["gate"][1, 0, 9] = float("nan")
+    got = c.attend_tree(**d)
+    assert c.status() == (0, 0)
+    assert (got[:5, :Hq] == 0).all()
+    assert torch.equal(got[5:], base[5:]) and torch.equal(got[:5, Hq:], base[:5, Hq:])

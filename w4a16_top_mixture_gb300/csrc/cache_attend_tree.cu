@@ -423,7 +423,8 @@ struct Sum {
   }
 };
 
-// 32 elements of a row's output, y vs / l (0 where l is 0) times the gate's sigmoid, from x on
+// 32 elements of a row's output, y vs / l times the gate's sigmoid, from x on; 0 where l is 0, the row saw nothing or scores of
+// -inf alone, whatever O (0 times an infinite value) and the gate hold
 template <class S>
 __device__ __forceinline__ void emit(const float (&y)[32], float l, float vs, uint16_t* gate, bool gated, uint16_t* out, int x,
                                      int lane) {
@@ -432,7 +433,8 @@ __device__ __forceinline__ void emit(const float (&y)[32], float l, float vs, ui
     FourRows(gate, lane).load(g, x);
     change_places(g, lane);
   }
-  const float by = l == 0.f ? 0.f : __fdividef(vs, l);       // a row that saw nothing has an O of 0
+  const float by = __fdividef(vs, l);
+  const bool none = l == 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t w[4] = {g[e].x, g[e].y, g[e].z, g[e].w};
@@ -446,7 +448,7 @@ __device__ __forceinline__ void emit(const float (&y)[32], float l, float vs, ui
       r[i] = pack2<S::BF16>(q[0], q[1]);
       r[i + 1] = pack2<S::BF16>(q[2], q[3]);
     }
-    z[e] = make_uint4(r[0], r[1], r[2], r[3]);
+    z[e] = none ? make_uint4(0, 0, 0, 0) : make_uint4(r[0], r[1], r[2], r[3]);
   }
   change_places(z, lane);
   FourRows(out, lane).store(z, x);
