@@ -426,7 +426,8 @@ MOE_API int moe_cache_tree(moe_cache_t *cache, const moe_cache_tree_t *tree, voi
  * a request's end has none on any. A row whose scores are all -inf gives 0, whatever its values and gate. Softmax statistics and sums are fp32; the weights of the
  * second product are rounded to act_dtype, or to fp16 with an e4m3 cache (in fp16 weights below 2^-21 of the highest may
  * lose bits and those below 2^-31 may count as none), the output once to act_dtype. bf16 queries over an e4m3 cache are
- * multiplied in fp16, by a power of two of each row: elements 2^-28 below a row's largest lose bits. Sums are in an order
+ * multiplied in fp16, by a power of two of each row: elements 2^-28 below a row's largest lose bits. Over a bf16 cache weights
+ * are 1 at most: the sums stay in fp32's range where the tokens' number times their largest value does. Sums are in an order
  * that lengths and starts fix. out may be q or gate itself. Page ids outside the pool read as zeros and are reported. */
 typedef struct {
   moe_rows_t q, gate;                          /* [n_rows][n_heads][head_dim]; gate.p NULL: no gate */

@@ -185,3 +185,27 @@ def test_rows_whose_scores_are_all_minus_infinity_give_zero(older, Hq, D, page, 
     assert c.status() == (0, 0)
     assert (got[:5, :Hq] == 0).all()
     assert torch.equal(got[5:], base[5:]) and torch.equal(got[:5, Hq:], base[:5, Hq:])
+
+
+@pytest.mark.parametrize("older,size", [(370, 2.0 ** 100), (370, 2.0 ** 117), (370, -2.0 ** 117), (3000, 2.0 ** 114)])
+def test_large_bf16_values_under_scores_that_rise(older, size):
+    """A row's base may stay below its highest score by a factor of 2^8; its weights stay at 1 or below all the same, so that the
+    sum over the tokens is within fp32's range where n times the largest value is: 373 2^117 < 2^126, 3003 2^114 < 2^126."""
+    torch = torch_()
+    D, page = 128, 64
+    d, n_pages, width = tree_case([(older, 3, 0)], 4, 1, D, page, "bf16", "bf16", 11, False, None)
+    n = older + 3
+    pos = torch.arange(n, device="cuda")
+    pages, off = d["tables"][0].long()[pos // page], pos % page
+    d["q"].zero_()
+    d["q"][..., 0] = 1.0
+    d["k_cache"][pages, 0, off] = 0.0
+    d["k_cache"][pages, 0, off, 0] = torch.where(pos < 128, 0.0, 5.4375).bfloat16()    # 2^7.84 in weights
+    d["v_cache"][pages, 0, off] = torch.randn(n, D, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).clamp(-1, 1).bfloat16()
+    d["v_cache"][pages, 0, off] *= size
+    d["v_cache"][pages, 0, off, 3] = size
+    c = cache_of(d, n_pages, width, 4, 1, D, page, "bf16", "bf16", 3)
+    out = c.attend_tree(**d, scale=1.0)
+    assert c.status() == (0, 0)
+    check(d, out, page, "bf16", "bf16", 1.0)
+    assert (out[:3, :, 3].double() - size).abs().max() <= 2.0 ** -6 * abs(size)

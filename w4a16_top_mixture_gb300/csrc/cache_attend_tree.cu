@@ -18,7 +18,8 @@
 // side, whatever the pages: as K it is read along d, as V along the tokens, by the descriptors' strides alone.
 //   Bases. P = 2^(score - base): the base is a row's first maximum and follows when one passes it by more than TAU, since
 // that rescales O (2000 cycles; with TAU 2 some warp of the eight did at nearly every tile). fp16 weights are lifted by
-// 2^LIFT, so that a long tail below the highest keeps its bits.
+// 2^LIFT, so that a long tail below the highest keeps its bits; bf16 weights are lowered to 1 at most, so that O stays in
+// range as far as n times the largest value does.
 //   Values that are not finite. A weight of 0 does not keep NaN out of a product. What lies past a request's end is zeroed
 // in shared memory; a new token's value that some rows do not see is looked at, and where it is not finite, zeroed too and
 // added at the item's end to the rows that see it.
@@ -71,7 +72,7 @@ struct Shape {
   static constexpr int NR0 = (SMEM - CTL - NC * TILE) / RAW, NR = NR0 > 12 ? 12 : NR0;
   static constexpr int DYN = NC * TILE + NR * RAW + CTL;
   static constexpr uint32_t O = 0, Q = D, S0 = D + D / 2;                      // columns of tensor memory
-  static constexpr float TAU = 8.f, LIFT = MBF16 ? 0.f : 7.f;                  // fp16: 2^15 at most
+  static constexpr float TAU = 8.f, LIFT = MBF16 ? -TAU : 7.f;                 // weights: 1 or 2^15 at most
   static constexpr int NC1 = NC ? NC : 1;
   static constexpr int PART = M * D + 2 * M;
   static_assert(S0 + 2 * TN <= 512 && DYN <= SMEM && NR >= 4, "fits");
