@@ -1,6 +1,7 @@
 """Host-side checks, without a GPU, of the cache's calls for several new tokens of a request: what is refused, with which
 status, before any device is touched; what lib.PagedCache hands over; and the float64 oracle against hand-worked cases."""
 import ctypes
+import time
 import types
 
 import numpy as np
@@ -99,6 +100,30 @@ def test_a_pool_named_twice_is_refused(L):
         pools, strides = (ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*([DENSE] * n))
         a = dict(pools=ctypes.addressof(pools), strides=ctypes.addressof(strides), n_pools=n)
         assert status(L, keep=a) == -1 and status(L, fork=a) == -1
+
+
+def test_pools_are_told_apart_in_time_that_grows_with_their_number(L):
+    """Up to 1024 of them at every keep and fork: a pool named twice is found wherever it stands, and eight times the pools take
+    nothing like 64 times as long."""
+    c = lib.CacheConfig(*OK.values())
+    best = {}
+    for n in (128, 1024):
+        pools = (ctypes.c_void_p * n)(*(P + 4096 * (i * 7919 % 100003) for i in range(n)))
+        strides = (ctypes.c_int64 * n)(*([DENSE] * n))
+        a = dict(pools=ctypes.addressof(pools), strides=ctypes.addressof(strides), n_pools=n)
+        for i, j in ((0, n - 1), (n // 2, n // 2 + 1), (3, n // 3), (n - 2, n - 1)):
+            was, pools[j] = pools[j], pools[i]
+            assert status(L, keep=a) == -1 and status(L, fork=a) == -1
+            pools[j] = was
+        args = lib.CACHE_KEEP.pack(*{**KEEP, **a}.values())
+        times = []
+        for _ in range(60):
+            t = time.perf_counter()
+            for _ in range(10):
+                assert L.moe_debug_cache_check_new(ctypes.byref(c), 64, None, None, args, None) == 0
+            times.append(time.perf_counter() - t)
+        best[n] = min(times)
+    assert best[1024] < 20 * best[128], best
 
 
 def test_null_handles(L):
