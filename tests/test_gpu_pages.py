@@ -382,3 +382,25 @@ def test_keep_and_fork_replayed_from_a_graph_and_on_another_stream():
         for a, b in zip(run(graph.replay), run(step)):
             np.testing.assert_array_equal(a, b)
     assert c.status() == (0, 0)
+
+
+@pytest.mark.parametrize("cache,heads,dim", [("f16", 2, 64), ("e4m3", 1, 128), ("bf16", 1, 256)])
+@pytest.mark.parametrize("share", [False, True])
+def test_keep_of_256_new_tokens_in_pages_of_16(cache, heads, dim, share):
+    """They lie in 17 pages, the most that a request's rows can move over; where two requests share them, all 17 are exchanged."""
+    torch = torch_()
+    rng = np.random.default_rng(17)
+    lengths, new = np.array([271, 271, 300]), np.array([256, 256, 256])
+    starts = np.concatenate([[0], np.cumsum(new)])
+    tables, ring, state, refs, n_pages = tables_for(rng, lengths, 16, 40, [(0, 1, 17)] if share else [])
+    c = lib.PagedCache(heads, heads, dim, 16, n_pages, 3, tables.shape[1], dtype="bf16" if cache == "bf16" else "f16", cache_dtype=cache,
+                       max_new=256)
+    pools = [pool_bits(torch, (n_pages, heads, 16, dim), cache, gen_of(i)) for i in range(3)]
+    path = np.full((3, 256), -3, np.int32)
+    path[0, :255], path[1, :128], path[2, :256] = np.arange(1, 256), np.arange(1, 256, 2), np.arange(256)
+    counts, before = np.array([255, 128, 256]), [bits(p).copy() for p in pools]
+    want = O.keep(counts, lengths, starts, [False] * 3, path, tables, ring, state, refs, before, 16, n_pages)
+    compare(run_keep(c, c.pools(pools), counts, lengths, tables, ring, state, starts, None, path, refs), want)
+    for p, w in zip(pools, want[5]):
+        np.testing.assert_array_equal(bits(p), w)
+    assert c.status() == (0, 0) and (not share or (want[2][:2] != tables[:2])[:, :9].all())

@@ -113,7 +113,6 @@ struct Kept {
   int page0, rows0;          // first page and row that change, of those that stay
   int older, moved;          // its older tokens; whether new ones move
   uint32_t exchange;         // bit i: page0 + i is exchanged
-  int pages;                 // given back to the ring
 };
 
 __global__ void __launch_bounds__(THREADS) k_cache_keep(const __grid_constant__ KeepArgs a) {
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(THREADS) k_cache_keep(const __grid_constant__ 
   // what each request keeps, which of its pages it gives back, and how many fresh ones it needs
   for (int l = warp, b; (b = l * ctas + rank) < a.B; l += WARPS) {
     Kept q;
-    q.page0 = q.rows0 = q.older = q.moved = q.pages = 0;
+    q.page0 = q.rows0 = q.older = q.moved = 0;
     q.exchange = 0;
     int n, count = __ldcg(k.counts + b);
     bool out;
@@ -407,9 +406,9 @@ struct MoveArgs {
 };
 
 // A warp moves a request's rows of one head in two pools: what it looks up (the record, the path, the pages, one after
-// another) is looked up once for both, and 8 KB of each lane's rows are on their way at once. Without a path no row is both
-// read and written, and a request's rows are cut into chunks of a warp each; with one they are read and written in order.
-// 256 requests, 6 rows of 512 bytes in 20 pools each: 28.8 us with the deciding, where a warp to each pool took 42.4.
+// another) is looked up once for both, and 8 KB of its rows are on their way at once, 256 bytes a lane. Without a path no
+// row is both read and written, and a request's rows are cut into chunks of a warp each; with one they are read and written in
+// order. 256 requests, 6 rows of 512 bytes in 20 pools each: 28.8 us with the deciding, where a warp to each pool took 42.4.
 __global__ void __launch_bounds__(MOVE_THREADS) k_cache_move(const __grid_constant__ MoveArgs a) {
   constexpr int U = 8;
   const int lane = threadIdx.x & 31, ps = 1 << a.page_log2;
