@@ -209,3 +209,24 @@ def test_large_bf16_values_under_scores_that_rise(older, size):
     assert c.status() == (0, 0)
     check(d, out, page, "bf16", "bf16", 1.0)
     assert (out[:3, :, 3].double() - size).abs().max() <= 2.0 ** -6 * abs(size)
+
+
+FULL = [([(500 + 60 * i, 5 + i % 12, 0) for i in range(128)], (16, 2, 256, 16, "bf16", "e4m3")), ([(250 * i, 256, 0) for i in range(24)], (16, 2, 128, 64, "bf16", "bf16")),
+        ([(40 * i % 900, 1 + i % 40, i % 11 == 5) for i in range(300)], (16, 2, 256, 16, "f16", "f16")), ([(80 * 2 ** i % 8100, 64, 0) for i in range(16)], (16, 2, 256, 16, "f16", "f16")),
+        ([(0 if i % 7 else 3000, (256, 1, 9, 64, 0)[i % 5], i % 13 == 4) for i in range(90)], (8, 2, 64, 16, "f16", "e4m3")),
+        ([(1000 + i, 1, 0) for i in range(200)] + [(2000, 256, 0), (0, 200, 0)], (16, 2, 128, 32, "f16", "e4m3"))]
+
+
+@pytest.mark.parametrize("masks", ["tree", None])
+@pytest.mark.parametrize("reqs,shape", FULL, ids=["trees, e4m3", "chunks", "300 mixed", "ragged", "mixed steps, e4m3", "decoding and prompts, e4m3"])
+def test_every_request_of_long_batches(reqs, shape, masks):
+    """Decoding requests, drafts, chunks, refused and empty ones in one batch, all of them compared."""
+    torch = torch_()
+    Hq, Hkv, D, page, act, cache = shape
+    d, n_pages, width = tree_case(reqs, Hq, Hkv, D, page, act, cache, len(reqs), True, masks, 4, 3)
+    c = cache_of(d, n_pages, width, Hq, Hkv, D, page, act, cache, 256)
+    out = torch.full_like(d["q"], 7.0).contiguous()
+    c.attend_tree(**d, out=out)
+    assert c.status() == (0, 0)
+    check(d, out, page, act, cache)
+    assert (out[int(d["starts"][-1]):] == 7.0).all()
