@@ -404,3 +404,45 @@ def test_keep_of_256_new_tokens_in_pages_of_16(cache, heads, dim, share):
     for p, w in zip(pools, want[5]):
         np.testing.assert_array_equal(bits(p), w)
     assert c.status() == (0, 0) and (not share or (want[2][:2] != tables[:2])[:, :9].all())
+
+
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+def test_pages_that_lie_past_2_to_the_32_bytes(cache):
+    """Pools whose pages are far apart give what dense ones do: attention with values that are not finite, a path kept, a fork."""
+    torch = torch_()
+    rng = np.random.default_rng(21)
+    n_pages, apart = 90, 1 << 26 if cache == "e4m3" else 1 << 25
+    lengths, starts = np.array([70, 30, 0]), np.array([0, 20, 25, 25])
+    c = lib.PagedCache(4, 1, 64, 16, n_pages, 3, 6, cache_dtype=cache, max_new=20)
+    tables = np.full((3, 6), -1, np.int32)
+    tables[0, :5], tables[1, :2] = [89, 88, 3, 80, 77], [85, 86]
+    free = [87, 84, 83, 70, 1]
+    ring = np.full(n_pages, -9, np.int32)
+    ring[:5] = free
+    refs = np.zeros(n_pages, np.int32)
+    refs[88] = 1                                              # someone else holds it too
+    dense = [torch.randn((n_pages, 1, 16, 64), device="cuda", generator=gen_of(i)).to(dt(cache)) for i in range(2)]
+    dense[1][80, 0, 3, 9] = float("nan")                      # a new token's value
+    far = [torch.empty((n_pages, apart), dtype=dense[0].dtype, device="cuda")[:, :1024].view(n_pages, 1, 16, 64) for _ in dense]
+    for a, b in zip(far, dense):
+        a.copy_(b)
+    q = torch.randn(25, 4, 64, device="cuda", generator=gen_of(5)).half()
+    scales = dict(k_scale=torch.ones(1, device="cuda"), v_scale=torch.ones(1, device="cuda")) if cache == "e4m3" else {}
+    one, two = (c.attend_tree(q, ints(starts), ints(tables), ints(lengths), *p, **scales) for p in (dense, far))
+    assert torch.equal(one.view(torch.int16), two.view(torch.int16)) and one.isnan().any() and not one.isnan().all()
+    counts, path = np.array([9, 3, 0]), np.zeros((3, 20), np.int32)
+    path[0, :9], path[1, :3] = [0, 2, 3, 5, 7, 11, 13, 17, 19], [0, 2, 4]
+    both = []
+    for pools in (dense, far):
+        at = c.pools(pools)
+        ln, fs, tb, rg, rf = ints(lengths), ints([0, 5, 0]), ints(tables), ints(ring), ints(refs)
+        s = lib.CacheState(ln, fs)
+        c.keep(ints(counts), ln, tb, rg, fs, at, starts=ints(starts), path=ints(path), refs=rf, out=s)
+        c.fork(ints([0]), ints([2]), ln, tb, rg, fs, rf, at, out=s)
+        both.append([x.tolist() for x in (ln, fs, tb, rg, rf)] + [bits(p[sorted(set(tables[tables >= 0].tolist() + free))].contiguous()) for p in pools])
+    want = O.keep(counts, lengths, starts, [False] * 3, path, tables, ring, np.array([0, 5, 0]), refs, [], 16, n_pages)
+    want = O.fork([0], [2], want[0], want[2], want[3], want[1], want[4], [], 16, n_pages)
+    assert both[0][:5] == [np.asarray(w).tolist() for w in want[:5]] and both[1][:5] == both[0][:5]
+    for a, b in zip(both[0][5:], both[1][5:]):
+        np.testing.assert_array_equal(a, b)
+    assert c.status() == (0, 0)

@@ -230,3 +230,32 @@ def test_every_request_of_long_batches(reqs, shape, masks):
     assert c.status() == (0, 0)
     check(d, out, page, act, cache)
     assert (out[int(d["starts"][-1]):] == 7.0).all()
+
+
+@pytest.mark.parametrize("older", [0, 5000])
+@pytest.mark.parametrize("Hq,D,page,act,cache", [(2, 64, 32, "bf16", "e4m3"), (5, 256, 16, "bf16", "bf16"), (3, 128, 16, "f16", "f16")])
+def test_gates_far_from_zero(older, Hq, D, page, act, cache):
+    """exp(-|gate|) in fp32 is off by 2 + 1.17 |gate| steps, 2^-16 at its smallest normal value, then by steps of 2^-149; all tokens
+    hold one value, so the output is that value times the sigmoid. One reciprocal of four factors adds a few steps of 2^-23."""
+    torch = torch_()
+    d, n_pages, width = tree_case([(older, 6, 0)], Hq, 1, D, page, act, cache, D, True, None)
+    n = older + 6
+    pos = torch.arange(n, device="cuda")
+    value = 448.0 if cache == "e4m3" else 1e4
+    d["v_cache"][d["tables"][0].long()[pos // page], 0, pos % page] = torch.tensor(value, device="cuda").to(d["v_cache"].dtype)
+    y = float(torch.tensor(value).to(d["v_cache"].dtype))
+    if cache == "e4m3":
+        d["v_scale"].fill_(20.0)
+        y *= 20.0
+    gates = torch.tensor([-INF, -110, -104, -100, -95, -90, -89, -88.5, -88, -87.5, -87, -80, -40, -11, -3, 0, 2, 17, 87, 88, 89, 104, INF], device="cuda")
+    shape = d["gate"].shape
+    d["gate"] = gates.repeat(-(-d["gate"].numel() // len(gates)))[:d["gate"].numel()].view(shape).to(d["gate"].dtype)
+    c = cache_of(d, n_pages, width, Hq, 1, D, page, act, cache, 6)
+    out = c.attend_tree(**d).double()
+    x = d["gate"].double()
+    want = y * torch.exp(x.clamp(max=0)) / (1 + torch.exp(-x.abs()))
+    up = U["f16"] if cache == "e4m3" else U[act]
+    least = 2.0 ** -134 if act == "bf16" else 2.0 ** -25
+    tol = want * (U[act] + up + (n / 16 + 232) * 2.0 ** -23 + 2.0 ** -16) + 3 * y * 2.0 ** -149 + least
+    err = (out - want).abs()
+    assert (err <= tol).all(), (x[err > tol][:9], out[err > tol][:9], want[err > tol][:9])
