@@ -428,7 +428,8 @@ MOE_API int moe_cache_tree(moe_cache_t *cache, const moe_cache_tree_t *tree, voi
  * lose bits and those below 2^-31 may count as none), the output once to act_dtype. bf16 queries over an e4m3 cache are
  * multiplied in fp16, by a power of two of each row: elements 2^-28 below a row's largest lose bits. Over a bf16 cache weights
  * are 1 at most: the sums stay in fp32's range where the tokens' number times their largest value does. Sums are in an order
- * that lengths and starts fix. out may be q or gate itself. Page ids outside the pool read as zeros and are reported. */
+ * that lengths and starts fix. out may be q or gate itself. Page ids outside the pool read as zeros and are reported. Requests
+ * with one new token may be among the others; where all have one, moe_cache_attend does the same, mostly faster. */
 typedef struct {
   moe_rows_t q, gate;                          /* [n_rows][n_heads][head_dim]; gate.p NULL: no gate */
   moe_rows_t out;                              /* written */

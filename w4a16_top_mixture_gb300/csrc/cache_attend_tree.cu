@@ -9,8 +9,8 @@
 // the tiles; more than FLAT of them in groups first (one request of 131072 tokens has 76 for each head).
 //   Roles. One warp finds the CTA's items, one copies (TMA, a ring of stages, keys one tile ahead of values), one issues
 // the products, eight do the softmax, two threads to a row, and four prepare: the queries go to tensor memory, where they
-// are the first operand; 8-bit tiles are converted to fp16 (two pairs of warps, every other stage each: a stage takes some
-// 500 cycles to convert and as many to hand over); and values of tiles with new tokens are looked through (below).
+// are the first operand; 8-bit tiles are converted to fp16 (two pairs of warps, every other stage each); and values of tiles
+// with new tokens are looked through (below).
 //   Tensor memory. O, Q and two S: the products of one tile run during the softmax of the other. P lies where S was. With
 // Q there a product reads shared memory for its second operand alone (64 columns: 32.5 cycles, 48.5 with Q in shared
 // memory), and all of it holds stages.
@@ -23,14 +23,18 @@
 //   Values that are not finite. A weight of 0 does not keep NaN out of a product. What lies past a request's end is zeroed
 // in shared memory; a new token's value that some rows do not see is looked at, and where it is not finite, zeroed too and
 // added at the item's end to the rows that see it.
-//   Local memory. With 227 KB of shared memory there is next to no L1: spills and calls cost more here than anything they
-// save, so that nothing is called out of line.
-// Measured (16 query over 2 key-value heads of 256 unless said): 64 requests of 4096 tokens, 8 new ones each, 101 us,
-// 5.4 TB/s (a copy runs at 6.7); 16 new ones over an e4m3 cache 98 us; 32 over 8 heads of 128, 16 new ones, 180 us, 6.1
-// TB/s; one request of 131072 tokens, 5 new ones, 77 us, of which the tiles are 40, joins 25; one of 130 tokens 13.5 us. Above
-// 128 rows the tiles come from L2 once for each 128: 256 new tokens of 16 requests of 8192 tokens 594 us, 0.91 PFLOP/s.
-// What is left: 6 us until the first scores, an item's end (5 to 12 us for 128 gated rows: arithmetic and instructions that
-// are not in the instruction cache, 150 KB of code), and the tiles' way from L2 for wide trees and chunks.
+//   Local memory. With 227 KB of shared memory there is next to no L1, so that spills and calls cost what a load from L2 does:
+// nothing is called out of line (an item's end so was 30 to 50 % slower). At 128 registers the compiler spills 8 bytes a
+// thread or none with heads of 256, 44 to 88 with smaller ones.
+// Measured (16 query over 2 key-value heads of 256 unless said): 64 requests of 4096 tokens, 8 new ones each, 100 us, 5.5
+// TB/s (a copy runs at 6.7); 16 new ones over an e4m3 cache 86 us, 3.4 TB/s; 32 over 8 heads of 128, 16 new ones, 178 us, 6.2
+// TB/s; heads of 64, 8 new ones, 133 us in 16 bits and 138 over e4m3 (4.1 and 2.0 TB/s); one request of 131072 tokens, 5 new
+// ones, 72 us, of which the tiles' bytes are 40; one of 130 tokens 13.7 us. Above 128 rows the tiles come from L2 once for
+// each 128: 256 new tokens of 16 requests of 8192 tokens 584 us, 0.93 PFLOP/s.
+// What is left is this design's: a tile's scores, maxima, weights and hand-over one after another in one set of warps, rows
+// of the 128 that do not exist, 6 us until the first scores, an item's end on the warps that the next item waits for (5 to 12
+// us for 128 gated rows), and the tiles' way from L2 for wide trees and chunks. One token of each request is moe_cache_attend's:
+// its tiles have the heads as their narrow side, and it takes 7.7 us for 130 tokens, 50 us for the 64 requests over e4m3.
 #include <cuda.h>
 
 #include <atomic>
@@ -44,7 +48,10 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int THREADS = 512, MAX_CTAS = 1024, EXTRA = 7, SHORT = EXTRA + 3, ITEMS = 4, M = 128;
-constexpr int GROUP_OF = 8, FLAT = 12;    // parts of a group; parts that are joined without groups
+// Parts of a group, and parts that are joined without groups: 76 parts of one request of 131072 tokens take 72 us in groups of 8,
+// 78 in groups of 4 and 75 of 16; four requests of 20000, 19 parts each, 50 us in groups and 58 without; 6 for FLAT changes
+// nothing measured.
+constexpr int GROUP_OF = 8, FLAT = 12;
 constexpr int SMEM = 227 * 1024, MISC = 3 * 1024;
 constexpr int W_PRODUCE = 0, W_MMA = 1, W_FIND = 2, W_SOFT = 4, W_PREP = 12, SOFT = 8;   // SOFT: warps of the softmax
 
@@ -233,9 +240,13 @@ __device__ __forceinline__ uint16_t* rows_at(const moe_rows_t& r, int64_t row, i
 }
 
 // ---- the division of the work ----
-// A request's items are of n_tiles tiles and EXTRA units for what an item's beginning and end cost (16 requests with trees of
-// 64, 80 to 8191 tokens: 93 us with 2 of them, 83 with 4, 76 with 7, 79 with 12; while no item is longer than SHORT, a CTA
-// takes whole items).
+// A request's items are of n_tiles tiles and EXTRA units for what an item's beginning and end cost. 16 requests with trees of
+// 64, 80 to 8191 tokens, in us with 3, 5, 7, 10 of them: heads of 256 with a gate 88, 77, 70, 70, without 65, 62, 62, 63 (over
+// e4m3 a few less); of 128 80, 66, 65, 70 and 64, 58, 61, 66; of 64 53, 52, 55, 59 and 46, 50, 53, 57. Long even batches and
+// single requests do not depend on it. One number for all of them is a compromise: heads of 64 would have 5 or less.
+// While no item is longer than SHORT units, a CTA's share is at least the longest item: 64 requests of 190 tokens take 18 us so
+// and 30 with even shares, 8 of 130 tokens 14.3 and 16.4. Items are whole only where all are of one length: 40 requests of 20
+// to 190 tokens are split at borders inside items all the same, and take 27 us so and 18 with even shares.
 struct Request {
   int lo, n, older, len, tiles, m_tiles;
 };
